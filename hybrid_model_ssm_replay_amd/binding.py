@@ -11,7 +11,8 @@ import os
 
 KIND_MAMBA2, KIND_GDN = 0, 1
 FMT_F32, FMT_F16_SR, FMT_F8E4M3, FMT_F4E2M1_B16, FMT_F4E2M1_CS = 0, 1, 2, 3, 4
-STATUS_ACCEPT_CLAMPED, STATUS_BAD_POINTERS = 0x1, 0x2
+STATUS_ACCEPT_CLAMPED, STATUS_BAD_POINTERS, STATUS_BAD_PROMPT = 0x1, 0x2, 0x4
+DT_F32, DT_BF16 = 0, 1
 FLAG_DECAY_SKIP = 0x1
 FLAG_BF16_RECORDS = 0x2
 FLAG_RECORDS_IN_RING = 0x4
@@ -58,6 +59,38 @@ class replay_ctx(ctypes.Structure):
                 ("t_pending", ctypes.c_int32), ("magic", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
 
 
+class replay_prompt(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("sequences", ctypes.c_int32), ("seq_start", ctypes.c_void_p),
+                ("rows", ctypes.c_void_p), ("resume", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class replay_short_conv(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("taps", ctypes.c_int32), ("slots", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("width", ctypes.c_int32 * 3), ("reserved", ctypes.c_int32), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("ring", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class replay_gated_norm_args(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("channels", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("weight_len", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("z_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("norm_first", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("y_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("y", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
+class replay_accept_args(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("drafts", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("target_dtype", ctypes.c_int32), ("draft_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("target_seq_stride", ctypes.c_int64), ("target_row_stride", ctypes.c_int64),
+                ("draft_seq_stride", ctypes.c_int64), ("draft_row_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("target", ctypes.c_void_p),
+                ("draft", ctypes.c_void_p), ("uniforms", ctypes.c_void_p), ("accepted", ctypes.c_void_p),
+                ("next", ctypes.c_void_p)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -86,6 +119,16 @@ _SIG = {
     "replay_snapshot_verify": (ctypes.c_int, [ctypes.POINTER(replay_config), _P, _P, ctypes.c_int32, _P, _P,
                                               ctypes.POINTER(replay_record), _P, _P]),
     "replay_snapshot_commit": (ctypes.c_int, [ctypes.POINTER(replay_config), _P, _P, ctypes.c_int32, _P]),
+    "replay_short_conv_step": (ctypes.c_int, [ctypes.POINTER(replay_short_conv), _P, ctypes.c_int64, ctypes.c_int64,
+                                              ctypes.c_int32, _P, _P, _P, _P]),
+    "replay_short_conv_prompt": (ctypes.c_int, [ctypes.POINTER(replay_short_conv), ctypes.POINTER(replay_prompt), _P,
+                                                ctypes.c_int64, _P, _P, _P, _P]),
+    "replay_scan_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(replay_config), ctypes.c_int32, ctypes.c_int32]),
+    "replay_scan_prompt": (ctypes.c_int, [ctypes.POINTER(replay_config), ctypes.POINTER(replay_prompt),
+                                          ctypes.POINTER(replay_record), _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
+    "replay_gated_norm": (ctypes.c_int, [ctypes.POINTER(replay_gated_norm_args), _P]),
+    "replay_accept_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "replay_accept_drafts": (ctypes.c_int, [ctypes.POINTER(replay_accept_args), _P, _P]),
     "replay_hbm_probe": (ctypes.c_int, [_P, _P, ctypes.c_size_t, ctypes.c_int, _P]),
 }
 EXPORTS = tuple(_SIG)
@@ -110,7 +153,8 @@ def load_library(path: str | None = None):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    for i, st in enumerate((replay_config, replay_buffers, replay_record, replay_ctx)):
+    for i, st in enumerate((replay_config, replay_buffers, replay_record, replay_ctx, replay_ring_view, replay_prompt,
+                            replay_short_conv, replay_gated_norm_args, replay_accept_args)):
         if lib.replay_abi_sizeof(i) != ctypes.sizeof(st):
             raise ImportError(f"ABI mismatch for {st.__name__}: C {lib.replay_abi_sizeof(i)} "
                               f"vs ctypes {ctypes.sizeof(st)}")
@@ -224,3 +268,42 @@ def replay_snapshot_commit(cfg, cur: int, accepted: int, T: int, stream: int) ->
 
 def replay_hbm_probe(src: int, dst: int, nbytes: int, mode: int, stream: int) -> None:
     _check("replay_hbm_probe", load_library().replay_hbm_probe(src, dst, nbytes, mode, stream or None))
+
+
+def replay_short_conv_step(conv: replay_short_conv, x: int, seq_stride: int, row_stride: int, T: int, outs,
+                           stream: int) -> None:
+    _check("replay_short_conv_step",
+           load_library().replay_short_conv_step(ctypes.byref(conv), x or None, seq_stride, row_stride, T,
+                                                 *[o or None for o in outs], stream or None))
+
+
+def replay_short_conv_prompt(conv: replay_short_conv, prompt: replay_prompt, x: int, row_stride: int, outs,
+                             stream: int) -> None:
+    _check("replay_short_conv_prompt",
+           load_library().replay_short_conv_prompt(ctypes.byref(conv), ctypes.byref(prompt), x or None, row_stride,
+                                                   *[o or None for o in outs], stream or None))
+
+
+def replay_scan_workspace_bytes(cfg, tokens: int, sequences: int) -> int:
+    return load_library().replay_scan_workspace_bytes(ctypes.byref(cfg), tokens, sequences)
+
+
+def replay_scan_prompt(cfg, prompt: replay_prompt, rec: replay_record, A: int, D: int, initial: int, state: int, y: int,
+                       y_dtype: int, workspace: int, stream: int) -> None:
+    _check("replay_scan_prompt",
+           load_library().replay_scan_prompt(ctypes.byref(cfg), ctypes.byref(prompt), ctypes.byref(rec), A or None,
+                                             D or None, initial or None, state or None, y or None, y_dtype,
+                                             workspace or None, stream or None))
+
+
+def replay_gated_norm(args: replay_gated_norm_args, stream: int) -> None:
+    _check("replay_gated_norm", load_library().replay_gated_norm(ctypes.byref(args), stream or None))
+
+
+def replay_accept_workspace_bytes(batch: int, vocab: int) -> int:
+    return load_library().replay_accept_workspace_bytes(batch, vocab)
+
+
+def replay_accept_drafts(args: replay_accept_args, workspace: int, stream: int) -> None:
+    _check("replay_accept_drafts", load_library().replay_accept_drafts(ctypes.byref(args), workspace or None,
+                                                                       stream or None))

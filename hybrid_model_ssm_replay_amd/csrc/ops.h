@@ -1,0 +1,167 @@
+// Shared parts of the operators around the recurrence (short convolution,
+// prompt scan, gated norm, draft acceptance): packed sequences, element types,
+// launch declarations.
+#pragma once
+
+#include "common.h"
+
+namespace rssm {
+
+// ---- element types ------------------------------------------------------------
+// V consecutive elements of type T (float, or bf16_t: the upper half of a
+// float32) as float32.  V > 1 is one aligned access of V sizeof(T) bytes (two
+// for eight floats); the caller has checked the alignment.
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T *p, float (&v)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + i);
+        v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = p[i];
+    }
+  } else {
+    if constexpr (V % 2 == 0) {
+      typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+      const words w = *reinterpret_cast<const words *>(p);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        uint32_t u;
+        if constexpr (V == 2)
+          u = *reinterpret_cast<const uint32_t *>(&w);
+        else
+          u = w[i / 2];
+        v[i] = __uint_as_float(u << 16);
+        v[i + 1] = __uint_as_float(u & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __uint_as_float((uint32_t)p[i] << 16);
+    }
+  }
+}
+
+// Two float32 values as bf16, rounded to nearest even, the first in the low
+// half (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 h2 __attribute__((ext_vector_type(2)));
+  const f2 v = {a, b};
+  const h2 h = __builtin_convertvector(v, h2);
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// The store that goes with load_vec; bf16 rounds to nearest even (half a step,
+// 2^-9 of the value at most 2^-8): the array's type asks for it.
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = v[i];
+    }
+  } else if constexpr (V % 2 == 0) {
+    if constexpr (V == 2) {
+      *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
+    } else {
+      typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+      words w;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) w[i / 2] = pack_bf16(v[i], v[i + 1]);
+      *reinterpret_cast<words *>(p) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = (bf16_t)pack_bf16(v[i], 0.f);
+  }
+}
+
+// v / (1 + exp(-v)) by the hardware exponential and reciprocal (about 1e-7
+// relative each).  exp(-v) overflows to infinity for v < -88, where the result is -0.
+__device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
+
+// ---- packed sequences -----------------------------------------------------------
+struct Packed {
+  int tokens, n, batch;
+  const int32_t *start;   // [n + 1]
+  const int32_t *rows;    // [n] or NULL
+  const uint8_t *resume;  // [n] or NULL
+  int32_t *status;        // or NULL
+};
+
+__device__ __forceinline__ int clamp_start(const Packed &p, int i) {
+  const int s = p.start[i];
+  return s < 0 ? 0 : s > p.tokens ? p.tokens : s;
+}
+
+// Work items of `size` tokens without knowing the lengths on the host: sequence
+// i owns the items base_i .. base_{i+1} - 1 with base_i = start_i / size + i,
+// which are at least ceil(length_i / size) and at least one; tokens / size + n
+// items cover every sequence, and those past a sequence's end do nothing.
+__host__ __device__ inline int items_of(int tokens, int n, int size) { return tokens / size + n; }
+struct Item {
+  int seq, index, begin, len;  // sequence, item within it, its first row and length
+};
+__device__ __forceinline__ Item find_item(const Packed &p, int item, int size) {
+  int lo = 0, hi = p.n - 1;  // the last i with base_i <= item
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (clamp_start(p, mid) / size + mid <= item)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int b = clamp_start(p, lo), e = clamp_start(p, lo + 1);
+  return Item{lo, item - (b / size + lo), b, e > b ? e - b : 0};
+}
+
+// Batch row of sequence i; -1 (and the status bit) if it is out of range.
+__device__ __forceinline__ int batch_row(const Packed &p, int i, bool report) {
+  const int r = p.rows ? p.rows[i] : i;
+  if (r >= 0 && r < p.batch) return r;
+  if (report && p.status) atomicOr(p.status, REPLAY_STATUS_BAD_PROMPT);
+  return -1;
+}
+
+// ---- launches -------------------------------------------------------------------
+struct ShortConvArgs {
+  int C, K, slots, batch, dtype, silu;
+  int w[3];
+  const float *weight, *bias;
+  void *ring;
+  const int32_t *pos;
+  int32_t *status;
+  const void *x;
+  int64_t seq_stride, row_stride;
+  int T;       // step: tokens a row
+  Packed p;    // prompt
+  void *out[3];
+};
+int launch_short_conv_step(const ShortConvArgs &a, hipStream_t st);
+int launch_short_conv_prompt(const ShortConvArgs &a, hipStream_t st);
+
+struct ScanArgs {
+  int H, G, P, N, bf16, y_bf16;
+  Packed p;
+  const void *x, *Bm, *Cm;
+  const float *dt, *A, *D, *initial;
+  float *state;
+  void *y;
+  void *workspace;
+};
+size_t scan_workspace(const ScanArgs &a);
+int launch_scan(const ScanArgs &a, hipStream_t st);
+
+int launch_gated_norm(const replay_gated_norm_args &a, hipStream_t st);
+
+size_t accept_workspace(int batch, int vocab);
+int launch_accept(const replay_accept_args &a, void *workspace, hipStream_t st);
+
+}  // namespace rssm

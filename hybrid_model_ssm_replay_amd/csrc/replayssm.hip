@@ -166,6 +166,10 @@ size_t replay_abi_sizeof(int which) {
     case 2: return sizeof(replay_record);
     case 3: return sizeof(replay_ctx);
     case 4: return sizeof(replay_ring_view);
+    case 5: return sizeof(replay_prompt);
+    case 6: return sizeof(replay_short_conv);
+    case 7: return sizeof(replay_gated_norm_args);
+    case 8: return sizeof(replay_accept_args);
     default: return 0;
   }
 }

@@ -71,6 +71,7 @@ extern "C" {
 /* Sticky bits of the device status word. */
 #define REPLAY_STATUS_ACCEPT_CLAMPED 0x1 /* commit got accepted < 0 or > drafts pending */
 #define REPLAY_STATUS_BAD_POINTERS 0x2   /* ckpt_pos < 0 or pos - ckpt_pos outside 0..L: sequence skipped */
+#define REPLAY_STATUS_BAD_PROMPT 0x4     /* a prompt's batch row outside 0..batch-1: sequence skipped */
 
 /*
  * Every output is read from the state that includes its own token [P3,
@@ -242,7 +243,8 @@ size_t replay_pointer_words(const replay_config *cfg);
 /* Static text for a return code. */
 const char *replay_strerror(int code);
 /* sizeof of the ABI structs, for bindings: 0 replay_config, 1 replay_buffers,
- * 2 replay_record, 3 replay_ctx, 4 replay_ring_view. */
+ * 2 replay_record, 3 replay_ctx, 4 replay_ring_view, 5 replay_prompt,
+ * 6 replay_short_conv, 7 replay_gated_norm_args, 8 replay_accept_args. */
 size_t replay_abi_sizeof(int which);
 
 /* ---- the decode calls -------------------------------------------------- */
@@ -329,6 +331,180 @@ int replay_ring_fields(const replay_ctx *ctx, replay_ring_view *view);
  * the producer writes between this call and the step or verify it feeds, on
  * the same stream (or ordered after it).  REPLAY_EINVAL unless RECORDS_IN_RING. */
 int replay_record_slots(const replay_ctx *ctx, int32_t *slots, void *stream);
+
+/* ---- around the recurrence: short convolution, prompts, norm, draft acceptance ----
+ *
+ * The operators a layer needs next to the decode step: the short causal
+ * convolution in front of it, the scan that turns a prompt into a checkpoint,
+ * the gated norm behind it, and the test that says how many drafts to commit.
+ * They share the conventions at the top of this file.  Vector arrays have an
+ * element type (REPLAY_DT_*); sums, statistics and states are float32 or wider.
+ */
+
+/* Element types. */
+#define REPLAY_DT_F32 0
+#define REPLAY_DT_BF16 1
+
+/* Sequences of several prompts, packed one after the other.
+ *   tokens     rows of the packed arrays (0 allowed).
+ *   sequences  prompts in this call, 1..batch.
+ *   seq_start  device int32 [sequences + 1], non-decreasing, within 0..tokens:
+ *              sequence i is rows seq_start[i] .. seq_start[i + 1] - 1 (it may
+ *              be empty).  Values are clamped into that range, never followed
+ *              outside it.
+ *   rows       device int32 [sequences]: the batch row (state, ring, pos) of
+ *              each sequence, all different; NULL: row i.  A sequence whose row
+ *              is outside 0..batch-1 is skipped and REPLAY_STATUS_BAD_PROMPT set.
+ *   resume     device uint8 [sequences]: nonzero: the sequence continues what
+ *              the row holds; zero: it starts from nothing.  NULL: see the calls.
+ *   status     device int32, sticky bits, or NULL. */
+typedef struct replay_prompt {
+  int32_t tokens;
+  int32_t sequences;
+  const int32_t *seq_start;
+  const int32_t *rows;
+  const uint8_t *resume;
+  int32_t *status;
+} replay_prompt;
+
+/* The short causal depthwise convolution of a layer,
+ *   y[t][c] = act(bias[c] + sum_k weight[c][k] x[t - taps + 1 + k][c]),
+ * and its state: a ring of raw inputs, [slots][batch][channels] in dtype, where
+ * the input at position p of a sequence lives in slot p mod slots.  Positions
+ * are the layer's own (replay_current_pointers), so rejecting drafts moves a
+ * pointer and restores nothing, as for the recurrent state.
+ *   taps       2..4.
+ *   slots      >= taps - 1 + T for every step of T tokens.
+ *   silu       1: act(v) = v / (1 + exp(-v)); 0: act(v) = v.
+ *   width      the outputs are split by channel into up to three arrays
+ *              (Mamba-2 x, B, C; GDN q, k, v), each contiguous: widths >= 0
+ *              that add up to channels.
+ *   weight     float32 [channels][taps] (the last tap meets the newest input).
+ *   bias       float32 [channels] or NULL.
+ *   status     device int32, sticky bits, or NULL.
+ * Sums are float32; outputs have dtype. */
+typedef struct replay_short_conv {
+  int32_t channels;
+  int32_t taps;
+  int32_t slots;
+  int32_t batch;
+  int32_t dtype;
+  int32_t silu;
+  int32_t width[3];
+  int32_t reserved;
+  const float *weight;
+  const float *bias;
+  void *ring;
+  const int32_t *pos;
+  int32_t *status;
+} replay_short_conv;
+
+/* T tokens (one, or T drafts) for every row of the batch, at positions
+ * pos[b] .. pos[b] + T - 1: x rows at x + b seq_stride + t row_stride elements (>= 0),
+ * outputs out0 [batch][T][width[0]] and so on.  The inputs are written to their
+ * ring slots; pos is not changed (the layer's step or commit moves it).  A row
+ * whose pos is negative is skipped and REPLAY_STATUS_BAD_POINTERS set. */
+int replay_short_conv_step(const replay_short_conv *conv, const void *x, int64_t seq_stride, int64_t row_stride,
+                           int32_t T, void *out0, void *out1, void *out2, void *stream);
+
+/* Packed prompts: x rows at x + t row_stride, outputs out0 [tokens][width[0]]
+ * and so on.  The ring's slots of the taps - 1 positions before pos[row] are
+ * the history: read where resume is nonzero (NULL: no sequence resumes), else
+ * taken as zeros, and replaced by the sequence's last inputs, so a step at
+ * pos[row] continues from there.  pos NULL: 0 for every row. */
+int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt *prompt, const void *x,
+                             int64_t row_stride, void *out0, void *out1, void *out2, void *stream);
+
+/* The Mamba-2 recurrence over packed prompts, S <- exp(dt A) S + dt x B^T,
+ * y = S C + D x for every token of every sequence.  cfg gives kind (Mamba-2),
+ * batch, heads, groups, head_dim, state_dim and REPLAY_FLAG_BF16_RECORDS;
+ * window, max_draft and formats are ignored.  rec: x [tokens][heads][P],
+ * B, C [tokens][groups][N], dt [tokens][heads] (positive), as for a step.
+ *   initial    float32 [batch][heads][P][N]: where a resumed sequence starts
+ *              (resume NULL: every sequence); NULL: every sequence starts from 0.
+ *   state      float32 [batch][heads][P][N]: rows of the call's sequences are
+ *              written with the state after their last token (an empty
+ *              sequence: its start).  It may be `initial`, and it may be the
+ *              F32 checkpoint of a layer whose windows are empty in those rows.
+ *   y          [tokens][heads][P] in y_dtype (REPLAY_DT_F32; REPLAY_DT_BF16 with
+ *              bf16 records only).
+ *   workspace  replay_scan_workspace_bytes bytes (256-byte aligned), or NULL
+ *              when that is 0.
+ * A NaN or infinity in one token reaches that head's later tokens, and may
+ * reach earlier ones of the same 64-token stretch of the same sequence; it
+ * never reaches another sequence. */
+size_t replay_scan_workspace_bytes(const replay_config *cfg, int32_t tokens, int32_t sequences);
+int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, const replay_record *rec,
+                       const float *A, const float *D, const float *initial, float *state, void *y, int32_t y_dtype,
+                       void *workspace, void *stream);
+
+/* The gated norm behind the recurrence, over groups of `group` consecutive
+ * channels (channels % group == 0), per token:
+ *   gate first (norm_first 0):  h = y silu(z),  out = w h / sqrt(mean(h^2) + eps)
+ *   norm first (norm_first 1):  out = w y / sqrt(mean(y^2) + eps) silu(z)
+ * Rows of y, z, out start at multiples of their strides (elements; >= 0 for y
+ * and z, whose rows may repeat, >= channels for out); each array has its type.
+ * weight: float32 [weight_len], weight_len = channels or group (one vector
+ * shared by the groups).  Statistics are float32. */
+typedef struct replay_gated_norm_args {
+  int32_t tokens;
+  int32_t channels;
+  int32_t group;
+  int32_t weight_len;
+  int32_t y_dtype;
+  int32_t z_dtype;
+  int32_t out_dtype;
+  int32_t norm_first;
+  float eps;
+  int32_t reserved;
+  int64_t y_stride;
+  int64_t z_stride;
+  int64_t out_stride;
+  const void *y;
+  const void *z;
+  const float *weight;
+  void *out;
+} replay_gated_norm_args;
+int replay_gated_norm(const replay_gated_norm_args *args, void *stream);
+
+/* Which drafts to keep: draft i (token x_i = tokens[b][i], i < lengths[b]) is
+ * accepted while every earlier one is and u_i q_i(x_i) < p_i(x_i), with u_i =
+ * uniforms[b][i] in [0, 1).  After the a accepted ones a token is drawn from
+ * max(p_a - q_a, 0), scaled to sum 1, if draft a was refused, or from p_a if
+ * none was left (a = lengths[b]): the smallest v whose running sum exceeds
+ * uniforms[b][drafts] times the total (float64 sums), at most the last v with
+ * any weight.  So the tokens follow the target's distribution exactly.
+ *   target     p: [batch][drafts + 1][vocab], rows vocab long at the given
+ *              strides (elements, >= 0); draft: q: [batch][drafts][vocab], or NULL:
+ *              the drafts were certain (q_i = 1 at x_i, 0 elsewhere).
+ *   lengths    device int32 [batch], clamped to 0..drafts; NULL: drafts.
+ *   accepted   int32 [batch]: a, ready for replay_commit.
+ *   next       int32 [batch]: the drawn token; -1 if p_a has no weight at all.
+ * A residual without weight (p nowhere above q) draws from p_a.  NaN and
+ * negative probabilities have no weight; a draft token outside 0..vocab-1 is
+ * refused and has q = 0.
+ *   workspace  replay_accept_workspace_bytes bytes, 16-byte aligned. */
+typedef struct replay_accept_args {
+  int32_t batch;
+  int32_t drafts; /* 0 .. 2^20: 0 draws from p_0 */
+  int32_t vocab;
+  int32_t target_dtype;
+  int32_t draft_dtype;
+  int32_t reserved;
+  int64_t target_seq_stride;
+  int64_t target_row_stride;
+  int64_t draft_seq_stride;
+  int64_t draft_row_stride;
+  const int32_t *tokens;
+  const int32_t *lengths;
+  const void *target;
+  const void *draft;
+  const float *uniforms;
+  int32_t *accepted;
+  int32_t *next;
+} replay_accept_args;
+size_t replay_accept_workspace_bytes(int32_t batch, int32_t vocab);
+int replay_accept_drafts(const replay_accept_args *args, void *workspace, void *stream);
 
 /* ---- in-run baselines (for measurement, not part of the replay method) ---- */
 

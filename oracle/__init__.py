@@ -34,4 +34,6 @@ Modules:
   verify, commit, rollback).
 * ``session``: the layer-level calls (init / step / flush / verify / commit)
   built twice: stepwise (the definition) and replay (the method).
+* ``layer_ops``: the operators around the recurrence (short convolution, prompt
+  scan, gated norm, draft acceptance).
 """
