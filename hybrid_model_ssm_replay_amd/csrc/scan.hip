@@ -1,66 +1,576 @@
 // Mamba-2 recurrence over packed prompts: S <- exp(dt A) S + dt x B^T, y = S C + D x.
 //
-// One workgroup per (sequence, head) walks its tokens in order with the state
-// in registers: thread (p, j) holds columns 16 j .. 16 j + 15 of row p.
+// Chunks of Q tokens (64; 32 with float32 records) turn it into matrix products.
+// With a_t the sum of dt A over the chunk's tokens up to t and S0 the state before it:
+//   G = C B^T,   M[t][j] = G[t][j] e^{a_t - a_j} dt_j  (j <= t, else 0),
+//   y_t = e^{a_t} S0 C_t + sum_j M[t][j] x_j + D x_t,
+//   S1  = e^{a_Q} S0 + sum_j (e^{a_Q - a_j} dt_j x_j) B_j^T.
+//
+// Decays are never differences of long sums: a chunk is cut into blocks of 16
+// tokens, and e^{a_t - a_j} is e^{(sum inside t's block up to t)} times the
+// whole blocks' decays between times e^{(sum inside j's block after j)}, three
+// factors of at most 1; only inside one block is it the exponential of a
+// difference, of running sums held as two float32 (the float64 sum and what
+// rounding left of it), so that the difference is good to float32 itself.
+//
+// A workgroup takes up to 128 columns of x (heads of one group, which share
+// B, C and G) of one sequence, and walks its chunks; a wave owns 32 columns of
+// one head with their whole state in registers (S^T as accumulators of
+// v_mfma_f32_16x16x32_bf16: lane l holds rows n = 4 (l / 16) + i of column p =
+// l % 16).  That layout is at once the operand layout of S C^T with the sum
+// over n taken in the order n = 32 k + 16 (i / 4) + 4 (l / 16) + i % 4, so the
+// state never leaves its wave, and G^T as accumulators is in the same way the
+// operand M of M x.  B^T and x^T operands come from row-major LDS tiles by the
+// transposing LDS read (lane l gets column l % 16 of rows 4 (l / 16) .. + 3).
+//
+// Precision.  bf16 records enter the products as they are, float32 records as
+// three bf16 pieces (their sum is the value; products of pieces below 2^-24 are
+// dropped).  The weighted inputs of the state update are always three pieces:
+// the state stays float32.  M and S in the output products are three pieces for
+// float32 outputs, and one bf16 for bf16 outputs: 2^-9 of each term on average
+// next to the output's own 2^-9.
 #include "ops.h"
 
 namespace rssm {
 namespace {
 
-template <typename R, typename Y>
-__global__ __launch_bounds__(1024) void scan_k(ScanArgs a) {
-  const int seq = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int row = batch_row(a.p, seq, h == 0 && threadIdx.x == 0);
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kCols = 128;        // x columns of a workgroup
+constexpr int kXs = kCols + 16;   // row strides of the LDS tiles in elements: no bank twice in a read
+constexpr float kLog2e = 1.4426950408889634f;
+
+union Frag {  // eight bf16 of one lane: an operand of the 16x16x32 product
+  s16x8 v;
+  s16x4 h[2];
+  uint32_t w[4];
+};
+
+__device__ __forceinline__ floatx4 mfma32(const Frag &a, const Frag &b, floatx4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ s16x4 read_tr(const bf16_t *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
+
+// The upper halves of two words: b's in the upper half.
+__device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ float cut(float v) { return __uint_as_float(bits(v) & 0xFFFF0000u); }
+
+// Two values as MP words of bf16 pairs: one piece rounds to nearest, three
+// pieces cut (8 bits each: together the 24 bits of the value).
+template <int MP>
+__device__ __forceinline__ void pieces(float a, float b, uint32_t (&w)[MP]) {
+  if constexpr (MP == 1) {
+    w[0] = pack_bf16(a, b);
+  } else {
+    w[0] = upper(bits(a), bits(b));
+    a -= cut(a), b -= cut(b);
+    w[1] = upper(bits(a), bits(b));
+    a -= cut(a), b -= cut(b);
+    w[2] = upper(bits(a), bits(b));
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float row_shift(float v) {  // within 16 lanes, zeros shifted in
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double row_shift(double v) {
+  const int2 w = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, w.x, CTRL, 0xF, 0xF, true),
+                                              __builtin_amdgcn_update_dpp(0, w.y, CTRL, 0xF, 0xF, true)));
+}
+
+struct ScanPlan {
+  int seg;        // tokens of a segment (a multiple of 64), or 0: sequences are not split
+  int items;      // segments of all sequences
+  int hw, wph;    // heads of a workgroup, waves of a head
+  int nb;         // workgroups of a group
+  FastDiv per, per_group;  // workgroups of an item (G nb), and nb
+  float *state;   // [items][H][P N]: a segment's own state, then its start
+  float *decay;   // [items][H]
+};
+
+// The parts of one launch.  kAll: sequences in one piece.  kOwn: every segment but
+// the last of a sequence leaves the state it would build from zero, and its
+// decay.  kFrom: segments start from the states that combine_k left.
+enum { kAll = 0, kOwn = 1, kFrom = 2 };
+
+template <typename R, typename Y, int NK, int MODE>
+__global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void scan_k(ScanArgs a, ScanPlan plan) {
+  constexpr int IP = sizeof(R) == 4 ? 3 : 1;             // pieces of an input
+  constexpr int MP = sizeof(Y) == 4 ? 3 : 1;             // pieces of M and S
+  constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;       // blocks and tokens of a chunk
+  constexpr int KB = QB / 2;                             // 32-token steps
+  constexpr int NT = 2 * NK, Ns = 32 * NK + 8;
+  constexpr int V = 16 / (int)sizeof(R);                 // elements of a 16-byte load
+  constexpr int NV = 32 * NK / V, XV = kCols / V;        // loads of a row
+  constexpr int LB = Q * NV / kThreads > 0 ? Q * NV / kThreads : 1, LX = Q * XV / kThreads;
+  constexpr bool OUT = MODE != kOwn;
+  constexpr int TILES = QB * (QB + 1) / 2;
+  __shared__ __attribute__((aligned(16))) bf16_t sB[IP][Q][Ns];
+  __shared__ __attribute__((aligned(16))) bf16_t sC[OUT ? IP : 1][OUT ? Q : 1][Ns];
+  __shared__ __attribute__((aligned(16))) bf16_t sX[IP][Q][kXs];
+  __shared__ float4 sG[OUT ? TILES : 1][kWave];
+  __shared__ __attribute__((aligned(16))) float sc[kWaves][5][kWave];  // per token, see below
+
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int r = lane % 16, q = lane / 16;
+  const int bid = xcd_remap(blockIdx.x, gridDim.x);
+  const int item = fdiv(bid, plan.per);
+  const int in_item = bid - item * (int)plan.per.d;
+  const int g = fdiv(in_item, plan.per_group), blk = in_item - g * (int)plan.per_group.d;
+  const int Hg = a.H / a.G, P = a.P, N = a.N;
+
+  int seq, begin, len, t_first = 0, t_end;
+  if constexpr (MODE == kAll) {
+    seq = item;
+    begin = clamp_start(a.p, seq);
+    len = max(0, clamp_start(a.p, seq + 1) - begin);
+    t_end = len;
+  } else {
+    const Item it = find_item(a.p, item, plan.seg);
+    seq = it.seq, begin = it.begin, len = it.len;
+    t_first = it.index * plan.seg;
+    if (it.index < 0 || (it.index > 0 && t_first >= len)) return;
+    t_end = min(len, t_first + plan.seg);
+    if (MODE == kOwn && t_end == len) return;  // nothing starts from the last segment's state
+  }
+  const int row = batch_row(a.p, seq, in_item == 0 && tid == 0 && MODE != kOwn && t_first == 0);
   if (row < 0) return;
-  const int b = clamp_start(a.p, seq), e = max(b, clamp_start(a.p, seq + 1));
-  const int J = a.N / 16;
-  const int p = threadIdx.x / J, j = threadIdx.x % J;
-  const int g = h / (a.H / a.G);
-  float s[16];
-  const size_t at = (((size_t)row * a.H + h) * a.P + p) * a.N + 16 * j;
+
+  const int hi = wave / plan.wph;
+  const int h0 = g * Hg + blk * plan.hw;                       // the workgroup's first head
+  const int nh = min(plan.hw, Hg - blk * plan.hw);
+  const bool active = hi < nh;
+  const int h = h0 + (active ? hi : 0);
+  const int pt0 = (wave % plan.wph) * 2;
+  const int np = active ? min(2, P / 16 - pt0) : 0;            // this wave's 16-column tiles
+  const int xcol = (active ? hi : 0) * P + (np > 0 ? 16 * pt0 : 0);
+  const int ncols = nh * P;
+  const float Al = a.A[h] * kLog2e;
+
+  // The state: S^T tile nt of column tile pt.
+  floatx4 S[NT][2];
+  const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt0 + r) * N + 4 * q;
+  const size_t states = (size_t)a.H * P * N;
+  bool split = false;
+  if constexpr (MODE == kFrom) split = len > plan.seg;
   const bool known = a.initial && (!a.p.resume || a.p.resume[seq]);
+  const float *from = nullptr;
+  if constexpr (MODE != kOwn) from = split ? plan.state + item * states : known ? a.initial + row * states : nullptr;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = known ? a.initial[at + i] : 0.f;
-  const float A = a.A[h], D = a.D[h];
-  for (int t = b; t < e; ++t) {
-    const float dt = a.dt[(size_t)t * a.H + h];
-    const float x = ldr<R>((const R *)a.x + ((size_t)t * a.H + h) * a.P + p);
-    const R *Bp = (const R *)a.Bm + ((size_t)t * a.G + g) * a.N + 16 * j;
-    const R *Cp = (const R *)a.Cm + ((size_t)t * a.G + g) * a.N + 16 * j;
-    const float dec = expf(dt * A), dx = dt * x;
-    float y = 0.f;
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 bv = ldr4<R>(Bp + i), cv = ldr4<R>(Cp + i);
-      s[i] = fmaf(dec, s[i], dx * bv.x), s[i + 1] = fmaf(dec, s[i + 1], dx * bv.y);
-      s[i + 2] = fmaf(dec, s[i + 2], dx * bv.z), s[i + 3] = fmaf(dec, s[i + 3], dx * bv.w);
-      y = fmaf(s[i], cv.x, fmaf(s[i + 1], cv.y, fmaf(s[i + 2], cv.z, fmaf(s[i + 3], cv.w, y))));
+    for (int pt = 0; pt < 2; ++pt) {
+      S[nt][pt] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (from && pt < np && 16 * nt < N) {
+        const float4 v = ld4(from + tile0 + (size_t)16 * pt * N + 16 * nt);
+        S[nt][pt] = floatx4{v.x, v.y, v.z, v.w};
+      }
     }
-    for (int d = 1; d < J; d <<= 1) y += __shfl_xor(y, d, kWave);
-    if (j == 0) {
-      float o[1] = {fmaf(D, x, y)};
-      store_vec<Y, 1>((Y *)a.y + ((size_t)t * a.H + h) * a.P + p, o);
+
+  // Global to registers, and registers to LDS.
+  uint4 pB[LB], pC[OUT ? LB : 1], pX[LX];
+  const size_t rB = (size_t)a.G * N, rX = (size_t)a.H * P;
+  const R *Bg = (const R *)a.Bm + (size_t)begin * rB + (size_t)g * N;
+  const R *Cg = (const R *)a.Cm + (size_t)begin * rB + (size_t)g * N;
+  const R *Xg = (const R *)a.x + (size_t)begin * rX + (size_t)h0 * P;
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int idx = i * kThreads + tid, t = t0 + idx / NV, c = idx % NV * V;
+      const bool in = idx < Q * NV && t < t_end && c < N;
+      pB[i] = in ? *reinterpret_cast<const uint4 *>(Bg + t * rB + c) : make_uint4(0, 0, 0, 0);
+      if constexpr (OUT) pC[i] = in ? *reinterpret_cast<const uint4 *>(Cg + t * rB + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+      const int idx = i * kThreads + tid, t = t0 + idx / XV, c = idx % XV * V;
+      pX[i] = t < t_end && c < ncols ? *reinterpret_cast<const uint4 *>(Xg + t * rX + c) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto put = [&](uint4 v, bf16_t *at, int piece) {  // at: the first piece's place; piece: elements between pieces
+    if constexpr (IP == 1) {
+      *reinterpret_cast<uint4 *>(at) = v;
+    } else {
+      uint32_t lo[3], hi3[3];
+      pieces<3>(__uint_as_float(v.x), __uint_as_float(v.y), lo);
+      pieces<3>(__uint_as_float(v.z), __uint_as_float(v.w), hi3);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2 *>(at + k * piece) = make_uint2(lo[k], hi3[k]);
+    }
+  };
+  auto spill = [&]() {
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int idx = i * kThreads + tid;
+      if (idx < Q * NV) {
+        put(pB[i], &sB[0][idx / NV][idx % NV * V], Q * Ns);
+        if constexpr (OUT) put(pC[i], &sC[0][idx / NV][idx % NV * V], Q * Ns);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+      const int idx = i * kThreads + tid;
+      put(pX[i], &sX[0][idx / XV][idx % XV * V], Q * kXs);
+    }
+  };
+  const float *dtg = a.dt + (size_t)begin * a.H + h;
+  auto fetch_dt = [&](int t0) {
+    const int t = t0 + lane;
+    return lane < Q && t < t_end && active ? dtg[(size_t)t * a.H] : 0.f;
+  };
+
+  // Operand of 32 columns of a row-major tile: row r of block b, columns in the order of an accumulator pair.
+  auto rows = [&](const bf16_t *tile, int stride, int b, int k) {
+    Frag f;
+    const bf16_t *p = tile + (16 * b + r) * stride + 32 * k + 4 * q;
+    f.h[0] = *reinterpret_cast<const s16x4 *>(p);
+    f.h[1] = *reinterpret_cast<const s16x4 *>(p + 16);
+    return f;
+  };
+  // Operand of 32 tokens: column c0 + r, tokens in the same order.
+  auto cols = [&](const bf16_t *tile, int stride, int c0, int k) {
+    Frag f;
+    const bf16_t *p = tile + (32 * k + 4 * q + r / 4) * stride + c0 + 4 * (r % 4);
+    f.h[0] = read_tr(p);
+    f.h[1] = read_tr(p + 16 * stride);
+    return f;
+  };
+
+  float decay = 1.f;
+  fetch(t_first);
+  float dtv = fetch_dt(t_first);
+  for (int t0 = t_first; t0 < t_end; t0 += Q) {
+    lds_barrier();  // every wave is done with the last chunk's tiles
+    spill();
+    const float dt = dtv;
+    if (t0 + Q < t_end) {
+      fetch(t0 + Q);
+      dtv = fetch_dt(t0 + Q);
+    }
+    // Decays: lane = token.
+    double sum = dt;
+    float suf = dt;
+    sum += row_shift<0x111>(sum), suf += row_shift<0x101>(suf);
+    sum += row_shift<0x112>(sum), suf += row_shift<0x102>(suf);
+    sum += row_shift<0x114>(sum), suf += row_shift<0x104>(suf);
+    sum += row_shift<0x118>(sum), suf += row_shift<0x108>(suf);
+    suf = row_shift<0x101>(suf);  // the tokens after this one
+    const float pre = (float)sum;
+    const float epre = __builtin_amdgcn_exp2f(Al * pre);
+    sc[wave][0][lane] = pre;
+    sc[wave][1][lane] = epre;
+    sc[wave][2][lane] = __builtin_amdgcn_exp2f(Al * suf) * dt;
+    if constexpr (OUT) {
+      sc[wave][3][lane] = dt;
+      sc[wave][4][lane] = (float)(sum - (double)pre);
+    }
+    float E[QB];  // the blocks' decays
+#pragma unroll
+    for (int b = 0; b < QB; ++b) E[b] = __uint_as_float(__builtin_amdgcn_readlane(bits(epre), 16 * b + 15));
+    lds_barrier();
+
+    floatx4 Yt[QB][2];
+    if constexpr (OUT) {
+      // G^T tiles (rows j, columns t), shared by the workgroup's heads.
+      for (int i = wave; i < TILES; i += kWaves) {
+        int tb = 0;
+        while ((tb + 1) * (tb + 2) / 2 <= i) ++tb;
+        const int jb = i - tb * (tb + 1) / 2;
+        floatx4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          Frag bf[IP], cf[IP];
+#pragma unroll
+          for (int u = 0; u < IP; ++u) bf[u] = rows(&sB[u][0][0], Ns, jb, k), cf[u] = rows(&sC[u][0][0], Ns, tb, k);
+#pragma unroll
+          for (int u = IP - 1; u >= 0; --u)
+#pragma unroll
+            for (int v = IP - 1 - u; v >= 0; --v) acc = mfma32(bf[u], cf[v], acc);
+        }
+        sG[i][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      }
+      // S0 C^T, transposed: rows p, columns t.
+#pragma unroll
+      for (int tb = 0; tb < QB; ++tb)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) Yt[tb][pt] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (np > 0) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          Frag sp[2][MP];
+#pragma unroll
+          for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const floatx4 &s = S[2 * k + i / 2][pt];
+              uint32_t w[MP];
+              pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
+#pragma unroll
+              for (int u = 0; u < MP; ++u) sp[pt][u].w[i] = w[u];
+            }
+#pragma unroll
+          for (int tb = 0; tb < QB; ++tb) {
+            Frag cf[IP];
+#pragma unroll
+            for (int u = 0; u < IP; ++u) cf[u] = rows(&sC[u][0][0], Ns, tb, k);
+#pragma unroll
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+              for (int u = MP - 1; u >= 0; --u)
+#pragma unroll
+                for (int v = 0; v < IP; ++v)
+                  if (u + v < 3) Yt[tb][pt] = mfma32(sp[pt][u], cf[v], Yt[tb][pt]);
+          }
+        }
+        float f = 1.f;
+#pragma unroll
+        for (int tb = 0; tb < QB; ++tb) {
+          const float e = f * sc[wave][1][16 * tb + r];
+          Yt[tb][0] *= e;
+          Yt[tb][1] *= e;
+          f *= E[tb];
+        }
+      }
+      lds_barrier();  // G is complete
+    }
+
+    if (np > 0) {
+      Frag xf[KB][2][IP];
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+          for (int u = 0; u < IP; ++u) xf[k][pt][u] = cols(&sX[u][0][0], kXs, xcol + (pt < np ? 16 * pt : 0), k);
+      if constexpr (OUT) {
+#pragma unroll
+        for (int tb = 0; tb < QB; ++tb) {
+          const float pt_ = sc[wave][0][16 * tb + r], lt = sc[wave][4][16 * tb + r], et = sc[wave][1][16 * tb + r];
+#pragma unroll
+          for (int k = 0; k <= tb / 2; ++k) {
+            Frag mf[MP];
+#pragma unroll
+            for (int u = 0; u < MP; ++u) mf[u].v = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int jb = 2 * k + half;
+              if (jb > tb) continue;
+              const float4 gv = sG[tb * (tb + 1) / 2 + jb][lane];
+              const float gm[4] = {gv.x, gv.y, gv.z, gv.w};
+              float m[4];
+              if (jb < tb) {
+                float f = et;  // t's block up to t, and the whole blocks between
+#pragma unroll
+                for (int b = 0; b < QB; ++b)
+                  if (b > jb && b < tb) f *= E[b];
+                const float4 w = *reinterpret_cast<const float4 *>(&sc[wave][2][16 * jb + 4 * q]);
+                m[0] = gm[0] * (f * w.x), m[1] = gm[1] * (f * w.y), m[2] = gm[2] * (f * w.z), m[3] = gm[3] * (f * w.w);
+              } else {
+                const float4 p4 = *reinterpret_cast<const float4 *>(&sc[wave][0][16 * jb + 4 * q]);
+                const float4 d4 = *reinterpret_cast<const float4 *>(&sc[wave][3][16 * jb + 4 * q]);
+                const float4 l4 = *reinterpret_cast<const float4 *>(&sc[wave][4][16 * jb + 4 * q]);
+                const float pj[4] = {p4.x, p4.y, p4.z, p4.w}, dj[4] = {d4.x, d4.y, d4.z, d4.w};
+                const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float v = gm[i] * (__builtin_amdgcn_exp2f(Al * ((pt_ - pj[i]) + (lt - lj[i]))) * dj[i]);
+                  m[i] = 4 * q + i <= r ? v : 0.f;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t w[MP];
+                pieces<MP>(m[2 * i], m[2 * i + 1], w);
+#pragma unroll
+                for (int u = 0; u < MP; ++u) mf[u].w[2 * half + i] = w[u];
+              }
+            }
+#pragma unroll
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+              for (int u = MP - 1; u >= 0; --u)
+#pragma unroll
+                for (int v = 0; v < IP; ++v)
+                  if (u + v < 3) Yt[tb][pt] = mfma32(xf[k][pt][v], mf[u], Yt[tb][pt]);
+          }
+        }
+        // y: this lane holds four neighbouring channels of token 16 tb + r.
+        const float D = a.D[h];
+#pragma unroll
+        for (int tb = 0; tb < QB; ++tb) {
+          const int t = t0 + 16 * tb + r;
+          if (t < t_end) {
+#pragma unroll
+            for (int pt = 0; pt < 2; ++pt)
+              if (pt < np) {
+                float o[4];
+                float x4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = IP - 1; u >= 0; --u) {
+                  float v[4];
+                  load_vec<bf16_t, 4>(&sX[u][16 * tb + r][xcol + 16 * pt + 4 * q], v);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) x4[i] += v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = fmaf(D, x4[i], Yt[tb][pt][i]);
+                store_vec<Y, 4>((Y *)a.y + ((size_t)(begin + t) * a.H + h) * P + 16 * (pt0 + pt) + 4 * q, o);
+              }
+          }
+        }
+      }
+      // The state after the chunk.
+      float all = 1.f;
+#pragma unroll
+      for (int b = 0; b < QB; ++b) all *= E[b];
+      decay *= all;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) S[nt][pt] *= all;
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        float f1 = 1.f;
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+          if (b > 2 * k + 1) f1 *= E[b];
+        const float f0 = f1 * E[2 * k + 1];
+        const float4 w0 = *reinterpret_cast<const float4 *>(&sc[wave][2][32 * k + 4 * q]);
+        const float4 w1 = *reinterpret_cast<const float4 *>(&sc[wave][2][32 * k + 16 + 4 * q]);
+        const float w[8] = {f0 * w0.x, f0 * w0.y, f0 * w0.z, f0 * w0.w, f1 * w1.x, f1 * w1.y, f1 * w1.z, f1 * w1.w};
+        Frag xw[2][3];
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float lo = 0.f, hi2 = 0.f;
+#pragma unroll
+            for (int u = IP - 1; u >= 0; --u) {
+              lo += __uint_as_float(xf[k][pt][u].w[i] << 16);
+              hi2 += __uint_as_float(xf[k][pt][u].w[i] & 0xFFFF0000u);
+            }
+            uint32_t pw[3];
+            pieces<3>(lo * w[2 * i], hi2 * w[2 * i + 1], pw);
+#pragma unroll
+            for (int u = 0; u < 3; ++u) xw[pt][u].w[i] = pw[u];
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          Frag bf[IP];
+#pragma unroll
+          for (int u = 0; u < IP; ++u) bf[u] = cols(&sB[u][0][0], Ns, 16 * nt, k);
+#pragma unroll
+          for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+            for (int u = 2; u >= 0; --u)
+#pragma unroll
+              for (int v = 0; v < IP; ++v)
+                if (u + v < 3) S[nt][pt] = mfma32(bf[v], xw[pt][u], S[nt][pt]);
+        }
+      }
     }
   }
+
+  float *to = MODE == kOwn ? plan.state + item * states : t_end == len ? a.state + row * states : nullptr;
+  if (to) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) st4(a.state + at + i, make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]));
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt)
+        if (pt < np && 16 * nt < N)
+          st4(to + tile0 + (size_t)16 * pt * N + 16 * nt, make_float4(S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]));
+  }
+  if (MODE == kOwn && np > 0 && wave % plan.wph == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
+}
+
+// Where each segment of a split sequence starts: the segment before it decays
+// that one's start and adds its own state.  One thread, four state elements.
+__global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan, FastDiv blocks) {
+  const int seq = fdiv(blockIdx.x, blocks);
+  const int begin = clamp_start(a.p, seq), len = clamp_start(a.p, seq + 1) - begin;
+  const int row = batch_row(a.p, seq, false);
+  const int e = ((blockIdx.x - seq * (int)blocks.d) * kThreads + threadIdx.x) * 4;
+  const int PN = a.P * a.N;
+  if (len <= plan.seg || row < 0 || e >= a.H * PN) return;
+  const int item0 = begin / plan.seg + seq, n = (len + plan.seg - 1) / plan.seg, h = e / PN;
+  const size_t states = (size_t)a.H * PN;
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.initial && (!a.p.resume || a.p.resume[seq])) run = ld4(a.initial + row * states + e);
+  for (int i = 0; i < n; ++i) {
+    float *at = plan.state + (item0 + i) * states + e;
+    const float d = i + 1 < n ? plan.decay[(size_t)(item0 + i) * a.H + h] : 0.f;
+    const float4 own = i + 1 < n ? ld4(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    st4(at, run);
+    run = make_float4(fmaf(run.x, d, own.x), fmaf(run.y, d, own.y), fmaf(run.z, d, own.z), fmaf(run.w, d, own.w));
+  }
+}
+
+ScanPlan make_plan(const ScanArgs &a) {
+  ScanPlan p{};
+  p.wph = (a.P + 31) / 32;
+  p.hw = kWaves / p.wph;
+  const int Hg = a.H / a.G;
+  p.nb = (Hg + p.hw - 1) / p.hw;
+  const int per = a.G * p.nb;
+  p.per = make_fastdiv((uint32_t)per);
+  p.per_group = make_fastdiv((uint32_t)p.nb);
+  // Split sequences along the length when there are too few to fill the card.
+  const int want = (512 + per - 1) / per;
+  const int seg = ((a.p.tokens + want - 1) / want + 63) / 64 * 64;
+  p.seg = a.p.n >= want || seg >= a.p.tokens ? 0 : seg < 256 ? 256 : seg;
+  if (p.seg >= a.p.tokens) p.seg = 0;
+  p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
+  return p;
+}
+
+size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.items * a.H * 4 + 255) / 256 * 256; }
+
+template <typename R, typename Y, int NK>
+int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
+  const int64_t blocks = (int64_t)p.items * p.per.d;
+  const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffLL || (int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  const dim3 grid((uint32_t)blocks), block(kThreads);
+  if (!p.seg) {
+    hipLaunchKernelGGL((scan_k<R, Y, NK, kAll>), grid, block, 0, st, a, p);
+  } else {
+    hipLaunchKernelGGL((scan_k<R, Y, NK, kOwn>), grid, block, 0, st, a, p);
+    hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), block, 0, st, a, p, make_fastdiv((uint32_t)per_seq));
+    hipLaunchKernelGGL((scan_k<R, Y, NK, kFrom>), grid, block, 0, st, a, p);
+  }
+  return (int)hipGetLastError();
+}
+
+template <typename R, typename Y>
+int launch_n(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
+  if (a.N <= 32) return launch<R, Y, 1>(a, p, st);
+  if (a.N == 64) return launch<R, Y, 2>(a, p, st);
+  return launch<R, Y, 4>(a, p, st);
 }
 
 }  // namespace
 
-size_t scan_workspace(const ScanArgs &) { return 0; }
+size_t scan_workspace(const ScanArgs &a) {
+  const ScanPlan p = make_plan(a);
+  return p.seg ? decay_bytes(a, p) + (size_t)p.items * a.H * a.P * a.N * 4 : 0;
+}
 
 int launch_scan(const ScanArgs &a, hipStream_t st) {
-  const int64_t blocks = (int64_t)a.p.n * a.H;
-  if (blocks > 0x7fffffffLL) return (int)hipErrorInvalidValue;
-  const dim3 grid((uint32_t)blocks), block(a.P * (a.N / 16));
-  if (!a.bf16)
-    hipLaunchKernelGGL((scan_k<float, float>), grid, block, 0, st, a);
-  else if (a.y_bf16)
-    hipLaunchKernelGGL((scan_k<bf16_t, bf16_t>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((scan_k<bf16_t, float>), grid, block, 0, st, a);
-  return (int)hipGetLastError();
+  ScanPlan p = make_plan(a);
+  p.decay = (float *)a.workspace;
+  p.state = p.seg ? (float *)((char *)a.workspace + decay_bytes(a, p)) : nullptr;
+  if (!a.bf16) return launch_n<float, float>(a, p, st);
+  return a.y_bf16 ? launch_n<bf16_t, bf16_t>(a, p, st) : launch_n<bf16_t, float>(a, p, st);
 }
 
 }  // namespace rssm
