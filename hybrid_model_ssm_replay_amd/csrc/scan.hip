@@ -88,12 +88,23 @@ __device__ __forceinline__ double row_shift(double v) {
                                               __builtin_amdgcn_update_dpp(0, w.y, CTRL, 0xF, 0xF, true)));
 }
 
+// Four entries of M of one lane: rounded to bf16, or float32 to be cut in pieces when used.
+template <int MP>
+struct MTile {
+  typedef float4 type;
+};
+template <>
+struct MTile<1> {
+  typedef uint2 type;
+};
+
 struct ScanPlan {
   int seg;        // tokens of a segment (a multiple of 64), or 0: sequences are not split
   int items;      // segments of all sequences
   int hw, wph;    // heads of a workgroup, waves of a head
   int nb;         // workgroups of a group
-  FastDiv per, per_group;  // workgroups of an item (G nb), and nb
+  int units;      // items x groups: the workgroups of a unit share B and C
+  FastDiv fnb, fG;
   float *state;   // [items][H][P N]: a segment's own state, then its start
   float *decay;   // [items][H]
 };
@@ -118,15 +129,18 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
   __shared__ __attribute__((aligned(16))) bf16_t sB[IP][Q][Ns];
   __shared__ __attribute__((aligned(16))) bf16_t sC[OUT ? IP : 1][OUT ? Q : 1][Ns];
   __shared__ __attribute__((aligned(16))) bf16_t sX[IP][Q][kXs];
-  __shared__ float4 sG[OUT ? TILES : 1][kWave];
-  __shared__ __attribute__((aligned(16))) float sc[kWaves][5][kWave];  // per token, see below
+  typedef typename MTile<MP>::type mtile;
+  __shared__ mtile sM[OUT ? kWaves : 1][OUT ? TILES : 1][kWave];            // per head of the workgroup
+  __shared__ __attribute__((aligned(16))) float sc[kWaves][5][kWave];     // per head and token, see below
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int r = lane % 16, q = lane / 16;
-  const int bid = xcd_remap(blockIdx.x, gridDim.x);
-  const int item = fdiv(bid, plan.per);
-  const int in_item = bid - item * (int)plan.per.d;
-  const int g = fdiv(in_item, plan.per_group), blk = in_item - g * (int)plan.per_group.d;
+  // Unit u on XCD u % 8 (workgroup i runs on XCD i % 8): a unit's workgroups share an
+  // L2, and items without work, which come at the end of each sequence, spread over the XCDs.
+  const int k8 = blockIdx.x / kXcds, u8 = fdiv(k8, plan.fnb);
+  const int unit = u8 * kXcds + blockIdx.x % kXcds, blk = k8 - u8 * plan.nb;
+  if (unit >= plan.units) return;
+  const int item = fdiv(unit, plan.fG), g = unit - item * a.G;
   const int Hg = a.H / a.G, P = a.P, N = a.N;
 
   int seq, begin, len, t_first = 0, t_end;
@@ -143,7 +157,7 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
     t_end = min(len, t_first + plan.seg);
     if (MODE == kOwn && t_end == len) return;  // nothing starts from the last segment's state
   }
-  const int row = batch_row(a.p, seq, in_item == 0 && tid == 0 && MODE != kOwn && t_first == 0);
+  const int row = batch_row(a.p, seq, g == 0 && blk == 0 && tid == 0 && MODE != kOwn && t_first == 0);
   if (row < 0) return;
 
   const int hi = wave / plan.wph;
@@ -177,24 +191,41 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
       }
     }
 
-  // Global to registers, and registers to LDS.
+  // Global to registers, and registers to LDS.  Rows are uniform, a thread adds
+  // its place in them; whole chunks of full width need no checks.
   uint4 pB[LB], pC[OUT ? LB : 1], pX[LX];
   const size_t rB = (size_t)a.G * N, rX = (size_t)a.H * P;
   const R *Bg = (const R *)a.Bm + (size_t)begin * rB + (size_t)g * N;
   const R *Cg = (const R *)a.Cm + (size_t)begin * rB + (size_t)g * N;
   const R *Xg = (const R *)a.x + (size_t)begin * rX + (size_t)h0 * P;
+  constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one load
+  const int tB = tid / NV, cB = tid % NV * V, tX = tid / XV, cX = tid % XV * V;
+  const uint32_t oB = (uint32_t)(tB * rB + cB) * sizeof(R), oX = (uint32_t)(tX * rX + cX) * sizeof(R);
+  const bool full_width = N == 32 * NK && ncols == kCols;
+  auto load16 = [](const void *base, uint32_t off) {
+    return *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + off);
+  };
   auto fetch = [&](int t0) {
+    const R *Bt = Bg + t0 * rB, *Ct = Cg + t0 * rB, *Xt = Xg + t0 * rX;
+    if (full_width && t0 + Q <= t_end) {
 #pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      const int idx = i * kThreads + tid, t = t0 + idx / NV, c = idx % NV * V;
-      const bool in = idx < Q * NV && t < t_end && c < N;
-      pB[i] = in ? *reinterpret_cast<const uint4 *>(Bg + t * rB + c) : make_uint4(0, 0, 0, 0);
-      if constexpr (OUT) pC[i] = in ? *reinterpret_cast<const uint4 *>(Cg + t * rB + c) : make_uint4(0, 0, 0, 0);
-    }
+      for (int i = 0; i < LB; ++i) {
+        pB[i] = load16(Bt + i * RB * rB, oB);
+        if constexpr (OUT) pC[i] = load16(Ct + i * RB * rB, oB);
+      }
 #pragma unroll
-    for (int i = 0; i < LX; ++i) {
-      const int idx = i * kThreads + tid, t = t0 + idx / XV, c = idx % XV * V;
-      pX[i] = t < t_end && c < ncols ? *reinterpret_cast<const uint4 *>(Xg + t * rX + c) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < LX; ++i) pX[i] = load16(Xt + i * RX * rX, oX);
+    } else {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < LB; ++i) {
+        const bool in = t0 + i * RB + tB < t_end && cB < N;
+        pB[i] = in ? load16(Bt + i * RB * rB, oB) : zero;
+        if constexpr (OUT) pC[i] = in ? load16(Ct + i * RB * rB, oB) : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < LX; ++i)
+        pX[i] = t0 + i * RX + tX < t_end && cX < ncols ? load16(Xt + i * RX * rX, oX) : zero;
     }
   };
   auto put = [&](uint4 v, bf16_t *at, int piece) {  // at: the first piece's place; piece: elements between pieces
@@ -211,17 +242,11 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
   auto spill = [&]() {
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      const int idx = i * kThreads + tid;
-      if (idx < Q * NV) {
-        put(pB[i], &sB[0][idx / NV][idx % NV * V], Q * Ns);
-        if constexpr (OUT) put(pC[i], &sC[0][idx / NV][idx % NV * V], Q * Ns);
-      }
+      put(pB[i], &sB[0][i * RB + tB][cB], Q * Ns);
+      if constexpr (OUT) put(pC[i], &sC[0][i * RB + tB][cB], Q * Ns);
     }
 #pragma unroll
-    for (int i = 0; i < LX; ++i) {
-      const int idx = i * kThreads + tid;
-      put(pX[i], &sX[0][idx / XV][idx % XV * V], Q * kXs);
-    }
+    for (int i = 0; i < LX; ++i) put(pX[i], &sX[0][i * RX + tX][cX], Q * kXs);
   };
   const float *dtg = a.dt + (size_t)begin * a.H + h;
   auto fetch_dt = [&](int t0) {
@@ -267,12 +292,14 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
     suf = row_shift<0x101>(suf);  // the tokens after this one
     const float pre = (float)sum;
     const float epre = __builtin_amdgcn_exp2f(Al * pre);
-    sc[wave][0][lane] = pre;
-    sc[wave][1][lane] = epre;
-    sc[wave][2][lane] = __builtin_amdgcn_exp2f(Al * suf) * dt;
-    if constexpr (OUT) {
-      sc[wave][3][lane] = dt;
-      sc[wave][4][lane] = (float)(sum - (double)pre);
+    if (active && pt0 == 0) {
+      sc[hi][0][lane] = pre;
+      sc[hi][1][lane] = epre;
+      sc[hi][2][lane] = __builtin_amdgcn_exp2f(Al * suf) * dt;
+      if constexpr (OUT) {
+        sc[hi][3][lane] = dt;
+        sc[hi][4][lane] = (float)(sum - (double)pre);
+      }
     }
     float E[QB];  // the blocks' decays
 #pragma unroll
@@ -281,7 +308,7 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
 
     floatx4 Yt[QB][2];
     if constexpr (OUT) {
-      // G^T tiles (rows j, columns t), shared by the workgroup's heads.
+      // G^T tiles (rows j, columns t), and M^T from them for each of the workgroup's heads.
       for (int i = wave; i < TILES; i += kWaves) {
         int tb = 0;
         while ((tb + 1) * (tb + 2) / 2 <= i) ++tb;
@@ -297,7 +324,32 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
 #pragma unroll
             for (int v = IP - 1 - u; v >= 0; --v) acc = mfma32(bf[u], cf[v], acc);
         }
-        sG[i][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        for (int hd = 0; hd < nh; ++hd) {
+          const float ah = a.A[h0 + hd] * kLog2e;
+          float m[4];
+          if (jb < tb) {
+            float f = sc[hd][1][16 * tb + r];  // t's block up to t, and the whole blocks between
+            for (int b = jb + 1; b < tb; ++b) f *= sc[hd][1][16 * b + 15];
+            const float4 w = *reinterpret_cast<const float4 *>(&sc[hd][2][16 * jb + 4 * q]);
+            m[0] = acc[0] * (f * w.x), m[1] = acc[1] * (f * w.y), m[2] = acc[2] * (f * w.z), m[3] = acc[3] * (f * w.w);
+          } else {
+            const float p1 = sc[hd][0][16 * tb + r], l1 = sc[hd][4][16 * tb + r];
+            const float4 p4 = *reinterpret_cast<const float4 *>(&sc[hd][0][16 * jb + 4 * q]);
+            const float4 d4 = *reinterpret_cast<const float4 *>(&sc[hd][3][16 * jb + 4 * q]);
+            const float4 l4 = *reinterpret_cast<const float4 *>(&sc[hd][4][16 * jb + 4 * q]);
+            const float pj[4] = {p4.x, p4.y, p4.z, p4.w}, dj[4] = {d4.x, d4.y, d4.z, d4.w};
+            const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v = acc[e] * (__builtin_amdgcn_exp2f(ah * ((p1 - pj[e]) + (l1 - lj[e]))) * dj[e]);
+              m[e] = 4 * q + e <= r ? v : 0.f;
+            }
+          }
+          if constexpr (MP == 1)
+            sM[hd][i][lane] = make_uint2(pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3]));
+          else
+            sM[hd][i][lane] = make_float4(m[0], m[1], m[2], m[3]);
+        }
       }
       // S0 C^T, transposed: rows p, columns t.
 #pragma unroll
@@ -335,13 +387,13 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
         float f = 1.f;
 #pragma unroll
         for (int tb = 0; tb < QB; ++tb) {
-          const float e = f * sc[wave][1][16 * tb + r];
+          const float e = f * sc[hi][1][16 * tb + r];
           Yt[tb][0] *= e;
           Yt[tb][1] *= e;
           f *= E[tb];
         }
       }
-      lds_barrier();  // G is complete
+      lds_barrier();  // M is complete
     }
 
     if (np > 0) {
@@ -355,44 +407,26 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
       if constexpr (OUT) {
 #pragma unroll
         for (int tb = 0; tb < QB; ++tb) {
-          const float pt_ = sc[wave][0][16 * tb + r], lt = sc[wave][4][16 * tb + r], et = sc[wave][1][16 * tb + r];
 #pragma unroll
           for (int k = 0; k <= tb / 2; ++k) {
             Frag mf[MP];
 #pragma unroll
-            for (int u = 0; u < MP; ++u) mf[u].v = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
             for (int half = 0; half < 2; ++half) {
               const int jb = 2 * k + half;
-              if (jb > tb) continue;
-              const float4 gv = sG[tb * (tb + 1) / 2 + jb][lane];
-              const float gm[4] = {gv.x, gv.y, gv.z, gv.w};
-              float m[4];
-              if (jb < tb) {
-                float f = et;  // t's block up to t, and the whole blocks between
+              if (jb > tb) {
 #pragma unroll
-                for (int b = 0; b < QB; ++b)
-                  if (b > jb && b < tb) f *= E[b];
-                const float4 w = *reinterpret_cast<const float4 *>(&sc[wave][2][16 * jb + 4 * q]);
-                m[0] = gm[0] * (f * w.x), m[1] = gm[1] * (f * w.y), m[2] = gm[2] * (f * w.z), m[3] = gm[3] * (f * w.w);
-              } else {
-                const float4 p4 = *reinterpret_cast<const float4 *>(&sc[wave][0][16 * jb + 4 * q]);
-                const float4 d4 = *reinterpret_cast<const float4 *>(&sc[wave][3][16 * jb + 4 * q]);
-                const float4 l4 = *reinterpret_cast<const float4 *>(&sc[wave][4][16 * jb + 4 * q]);
-                const float pj[4] = {p4.x, p4.y, p4.z, p4.w}, dj[4] = {d4.x, d4.y, d4.z, d4.w};
-                const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float v = gm[i] * (__builtin_amdgcn_exp2f(Al * ((pt_ - pj[i]) + (lt - lj[i]))) * dj[i]);
-                  m[i] = 4 * q + i <= r ? v : 0.f;
-                }
+                for (int u = 0; u < MP; ++u) mf[u].h[half] = s16x4{0, 0, 0, 0};
+                continue;
               }
+              const mtile m = sM[hi][tb * (tb + 1) / 2 + jb][lane];
+              if constexpr (MP == 1) {
+                mf[0].w[2 * half] = m.x, mf[0].w[2 * half + 1] = m.y;
+              } else {
+                uint32_t w0[MP], w1[MP];
+                pieces<MP>(m.x, m.y, w0);
+                pieces<MP>(m.z, m.w, w1);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t w[MP];
-                pieces<MP>(m[2 * i], m[2 * i + 1], w);
-#pragma unroll
-                for (int u = 0; u < MP; ++u) mf[u].w[2 * half + i] = w[u];
+                for (int u = 0; u < MP; ++u) mf[u].w[2 * half] = w0[u], mf[u].w[2 * half + 1] = w1[u];
               }
             }
 #pragma unroll
@@ -445,8 +479,8 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
         for (int b = 0; b < QB; ++b)
           if (b > 2 * k + 1) f1 *= E[b];
         const float f0 = f1 * E[2 * k + 1];
-        const float4 w0 = *reinterpret_cast<const float4 *>(&sc[wave][2][32 * k + 4 * q]);
-        const float4 w1 = *reinterpret_cast<const float4 *>(&sc[wave][2][32 * k + 16 + 4 * q]);
+        const float4 w0 = *reinterpret_cast<const float4 *>(&sc[hi][2][32 * k + 4 * q]);
+        const float4 w1 = *reinterpret_cast<const float4 *>(&sc[hi][2][32 * k + 16 + 4 * q]);
         const float w[8] = {f0 * w0.x, f0 * w0.y, f0 * w0.z, f0 * w0.w, f1 * w1.x, f1 * w1.y, f1 * w1.z, f1 * w1.w};
         Frag xw[2][3];
 #pragma unroll
@@ -522,14 +556,15 @@ ScanPlan make_plan(const ScanArgs &a) {
   const int Hg = a.H / a.G;
   p.nb = (Hg + p.hw - 1) / p.hw;
   const int per = a.G * p.nb;
-  p.per = make_fastdiv((uint32_t)per);
-  p.per_group = make_fastdiv((uint32_t)p.nb);
+  p.fnb = make_fastdiv((uint32_t)p.nb);
+  p.fG = make_fastdiv((uint32_t)a.G);
   // Split sequences along the length when there are too few to fill the card.
   const int want = (512 + per - 1) / per;
   const int seg = ((a.p.tokens + want - 1) / want + 63) / 64 * 64;
   p.seg = a.p.n >= want || seg >= a.p.tokens ? 0 : seg < 256 ? 256 : seg;
   if (p.seg >= a.p.tokens) p.seg = 0;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
+  p.units = p.items * a.G;
   return p;
 }
 
@@ -537,7 +572,7 @@ size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.ite
 
 template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
-  const int64_t blocks = (int64_t)p.items * p.per.d;
+  const int64_t blocks = ((int64_t)p.items * a.G + kXcds - 1) / kXcds * kXcds * p.nb;
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffLL || (int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
   const dim3 grid((uint32_t)blocks), block(kThreads);
