@@ -14,7 +14,7 @@
 // rounding left of it), so that the difference is good to float32 itself.
 //
 // A workgroup takes up to 128 columns of x (heads of one group, which share
-// B, C and G) of one sequence, and walks its chunks; a wave owns 32 columns of
+// B, C and G) of one sequence, and walks its chunks; a wave owns 16 columns of
 // one head with their whole state in registers (S^T as accumulators of
 // v_mfma_f32_16x16x32_bf16: lane l holds rows n = 4 (l / 16) + i of column p =
 // l % 16).  That layout is at once the operand layout of S C^T with the sum
@@ -34,16 +34,33 @@
 namespace rssm {
 namespace {
 
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kCols = 128;        // x columns of a workgroup
-constexpr int kXs = kCols + 16;   // row strides of the LDS tiles in elements: no bank twice in a read
+constexpr int kCols = 16 * kWaves;  // x columns of a workgroup
+constexpr int kHeads = 4;           // heads of a workgroup at most
 constexpr float kLog2e = 1.4426950408889634f;
+
+// LDS tiles are [token][column] in bf16 without padding, in 16-byte granules.
+// B and x are read 4 rows at 16 neighbouring columns (the transposing read) and, B
+// less often, 16 rows at one column, 8 bytes a lane each: the granules of a row are
+// permuted by an exclusive or, and the halves of a granule swapped, so that the 16
+// lanes of either read meet each bank once.
+__device__ __forceinline__ int in_row(int row, int c) {  // byte of column c (a multiple of 4) in its row
+  const int g = 2 * (row & 3) | (row >> 2 & 1), half = row >> 3 & 1;
+  return ((c >> 3 ^ g) << 4) + (((c >> 2 & 1) ^ half) << 3);
+}
+// C is read as operands only: a granule holds a lane's operand of one 32-column
+// step, columns 32 k + 4 q .. + 3 and 32 k + 16 + 4 q .. + 3.
+__device__ __forceinline__ int in_row_c(int row, int c) {
+  return (((c >> 5 << 2 | (c >> 2 & 3)) ^ (row & 7)) << 4) + (c >> 4 & 1) * 8;
+}
 
 union Frag {  // eight bf16 of one lane: an operand of the 16x16x32 product
   s16x8 v;
@@ -55,7 +72,15 @@ __device__ __forceinline__ floatx4 mfma32(const Frag &a, const Frag &b, floatx4 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ s16x4 read_tr(const bf16_t *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
+__device__ __forceinline__ s16x4 read_tr(const char *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
+
+// A buffer of n bytes: loads past its end give zeros, stores past it do nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, size_t n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)n, 0x00020000);
+}
+__device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t b, int at, int plus) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, at, plus, 0));
+}
 
 // The upper halves of two words: b's in the upper half.
 __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
@@ -114,26 +139,36 @@ struct ScanPlan {
 // decay.  kFrom: segments start from the states that combine_k left.
 enum { kAll = 0, kOwn = 1, kFrom = 2 };
 
+// Compile-time shape of a kernel: R records, Y outputs, NK 32-column steps of the state.
 template <typename R, typename Y, int NK, int MODE>
-__global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void scan_k(ScanArgs a, ScanPlan plan) {
-  constexpr int IP = sizeof(R) == 4 ? 3 : 1;             // pieces of an input
-  constexpr int MP = sizeof(Y) == 4 ? 3 : 1;             // pieces of M and S
-  constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;       // blocks and tokens of a chunk
-  constexpr int KB = QB / 2;                             // 32-token steps
-  constexpr int NT = 2 * NK, Ns = 32 * NK + 8;
+struct Shape_ {
+  static constexpr bool OUT = MODE != kOwn;
+  static constexpr int IP = sizeof(R) == 4 ? 3 : 1;        // pieces of an input
+  static constexpr int MP = sizeof(Y) == 4 ? 3 : 1;        // pieces of M and S
+  static constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;  // blocks and tokens of a chunk
+  static constexpr int TILES = QB * (QB + 1) / 2;
+  static constexpr int RS = NK > 2 ? 256 : 128, XS = 2 * kCols;  // bytes of a row of B, C and of x
+  static constexpr int B0 = 0, C0 = B0 + IP * Q * RS, X0 = C0 + (OUT ? IP * Q * RS : 0), SC0 = X0 + IP * Q * XS;
+  static constexpr int SC = 5 * Q * 4;                           // per head: five values a token
+  static constexpr int M = TILES * kWave * (MP == 1 ? 8 : 16);   // per head: M
+  static constexpr int lds(int heads) { return SC0 + heads * (SC + (OUT ? M : 0)); }
+};
+
+template <typename R, typename Y, int NK, int MODE>
+__global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan) {
+  typedef Shape_<R, Y, NK, MODE> Z;
+  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
+  constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
   constexpr int V = 16 / (int)sizeof(R);                 // elements of a 16-byte load
   constexpr int NV = 32 * NK / V, XV = kCols / V;        // loads of a row
-  constexpr int LB = Q * NV / kThreads > 0 ? Q * NV / kThreads : 1, LX = Q * XV / kThreads;
-  constexpr bool OUT = MODE != kOwn;
-  constexpr int TILES = QB * (QB + 1) / 2;
-  __shared__ __attribute__((aligned(16))) bf16_t sB[IP][Q][Ns];
-  __shared__ __attribute__((aligned(16))) bf16_t sC[OUT ? IP : 1][OUT ? Q : 1][Ns];
-  __shared__ __attribute__((aligned(16))) bf16_t sX[IP][Q][kXs];
+  constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one load of the workgroup
+  constexpr int LB = Q > RB ? Q / RB : 1, LX = Q / RX;
+  static_assert(RX % 16 == 0 && RB % 16 == 0, "a thread's rows share their permutation");
+  constexpr bool OUT = Z::OUT;
   typedef typename MTile<MP>::type mtile;
-  __shared__ mtile sM[OUT ? kWaves : 1][OUT ? TILES : 1][kWave];            // per head of the workgroup
-  __shared__ __attribute__((aligned(16))) float sc[kWaves][5][kWave];     // per head and token, see below
+  extern __shared__ __attribute__((aligned(16))) char lds[];
 
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane % 16, q = lane / 16;
   // Unit u on XCD u % 8 (workgroup i runs on XCD i % 8): a unit's workgroups share an
   // L2, and items without work, which come at the end of each sequence, spread over the XCDs.
@@ -160,20 +195,22 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
   const int row = batch_row(a.p, seq, g == 0 && blk == 0 && tid == 0 && MODE != kOwn && t_first == 0);
   if (row < 0) return;
 
-  const int hi = wave / plan.wph;
   const int h0 = g * Hg + blk * plan.hw;                       // the workgroup's first head
   const int nh = min(plan.hw, Hg - blk * plan.hw);
-  const bool active = hi < nh;
-  const int h = h0 + (active ? hi : 0);
-  const int pt0 = (wave % plan.wph) * 2;
-  const int np = active ? min(2, P / 16 - pt0) : 0;            // this wave's 16-column tiles
-  const int xcol = (active ? hi : 0) * P + (np > 0 ? 16 * pt0 : 0);
+  const int hw_ = wave / plan.wph;
+  const bool active = hw_ < nh;                                // this wave has a tile of x columns
+  const int hi = active ? hw_ : 0, pt = active ? wave % plan.wph : 0;
+  const int h = h0 + hi;
+  const int xcol = hi * P + 16 * pt;
   const int ncols = nh * P;
   const float Al = a.A[h] * kLog2e;
+  float *const sc = reinterpret_cast<float *>(lds + Z::SC0);                               // [heads][5][Q]
+  mtile *const sM = reinterpret_cast<mtile *>(lds + Z::SC0 + plan.hw * Z::SC);             // [heads][TILES][64]
+  float *const my = sc + hi * 5 * Q;
 
-  // The state: S^T tile nt of column tile pt.
-  floatx4 S[NT][2];
-  const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt0 + r) * N + 4 * q;
+  // The state: S^T tile nt, rows n = 16 nt + 4 q + i, column p = r of the wave's tile.
+  floatx4 S[NT];
+  const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt + r) * N + 4 * q;
   const size_t states = (size_t)a.H * P * N;
   bool split = false;
   if constexpr (MODE == kFrom) split = len > plan.seg;
@@ -181,107 +218,104 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
   const float *from = nullptr;
   if constexpr (MODE != kOwn) from = split ? plan.state + item * states : known ? a.initial + row * states : nullptr;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int pt = 0; pt < 2; ++pt) {
-      S[nt][pt] = floatx4{0.f, 0.f, 0.f, 0.f};
-      if (from && pt < np && 16 * nt < N) {
-        const float4 v = ld4(from + tile0 + (size_t)16 * pt * N + 16 * nt);
-        S[nt][pt] = floatx4{v.x, v.y, v.z, v.w};
-      }
+  for (int nt = 0; nt < NT; ++nt) {
+    S[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    if (from && 16 * nt < N) {
+      const float4 v = ld4(from + tile0 + 16 * nt);
+      S[nt] = floatx4{v.x, v.y, v.z, v.w};
     }
+  }
 
-  // Global to registers, and registers to LDS.  Rows are uniform, a thread adds
-  // its place in them; whole chunks of full width need no checks.
+  // Global to registers through buffers that end with the chunk's last row: rows
+  // past it read as zeros, and so do the columns of threads without a place.
   uint4 pB[LB], pC[OUT ? LB : 1], pX[LX];
   const size_t rB = (size_t)a.G * N, rX = (size_t)a.H * P;
   const R *Bg = (const R *)a.Bm + (size_t)begin * rB + (size_t)g * N;
   const R *Cg = (const R *)a.Cm + (size_t)begin * rB + (size_t)g * N;
   const R *Xg = (const R *)a.x + (size_t)begin * rX + (size_t)h0 * P;
-  constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one load
+  const float *dtg = a.dt + (size_t)begin * a.H + h;
+  constexpr int kNowhere = 0x7fffff00;
   const int tB = tid / NV, cB = tid % NV * V, tX = tid / XV, cX = tid % XV * V;
-  const uint32_t oB = (uint32_t)(tB * rB + cB) * sizeof(R), oX = (uint32_t)(tX * rX + cX) * sizeof(R);
-  const bool full_width = N == 32 * NK && ncols == kCols;
-  auto load16 = [](const void *base, uint32_t off) {
-    return *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + off);
-  };
+  const bool hasB = RB <= Q || tB < Q;  // narrow states leave threads without a piece of B and C
+  const int oB = hasB && cB < N ? (int)((tB * rB + cB) * sizeof(R)) : kNowhere;
+  const int oX = cX < ncols ? (int)((tX * rX + cX) * sizeof(R)) : kNowhere;
+  const int odt = lane < Q ? lane * a.H * 4 : kNowhere;
+  float dtv = 0.f;
   auto fetch = [&](int t0) {
-    const R *Bt = Bg + t0 * rB, *Ct = Cg + t0 * rB, *Xt = Xg + t0 * rX;
-    if (full_width && t0 + Q <= t_end) {
+    const int rem = min(Q, t_end - t0);
+    const auto bB = buffer_of(Bg + t0 * rB, ((rem - 1) * rB + N) * sizeof(R));
+    const auto bX = buffer_of(Xg + t0 * rX, ((rem - 1) * rX + ncols) * sizeof(R));
 #pragma unroll
-      for (int i = 0; i < LB; ++i) {
-        pB[i] = load16(Bt + i * RB * rB, oB);
-        if constexpr (OUT) pC[i] = load16(Ct + i * RB * rB, oB);
-      }
+    for (int i = 0; i < LB; ++i) pB[i] = buffer_load16(bB, oB, (int)(i * RB * rB * sizeof(R)));
+    if constexpr (OUT) {
+      const auto bC = buffer_of(Cg + t0 * rB, ((rem - 1) * rB + N) * sizeof(R));
 #pragma unroll
-      for (int i = 0; i < LX; ++i) pX[i] = load16(Xt + i * RX * rX, oX);
-    } else {
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < LB; ++i) {
-        const bool in = t0 + i * RB + tB < t_end && cB < N;
-        pB[i] = in ? load16(Bt + i * RB * rB, oB) : zero;
-        if constexpr (OUT) pC[i] = in ? load16(Ct + i * RB * rB, oB) : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < LX; ++i)
-        pX[i] = t0 + i * RX + tX < t_end && cX < ncols ? load16(Xt + i * RX * rX, oX) : zero;
+      for (int i = 0; i < LB; ++i) pC[i] = buffer_load16(bC, oB, (int)(i * RB * rB * sizeof(R)));
     }
-  };
-  auto put = [&](uint4 v, bf16_t *at, int piece) {  // at: the first piece's place; piece: elements between pieces
-    if constexpr (IP == 1) {
-      *reinterpret_cast<uint4 *>(at) = v;
-    } else {
-      uint32_t lo[3], hi3[3];
-      pieces<3>(__uint_as_float(v.x), __uint_as_float(v.y), lo);
-      pieces<3>(__uint_as_float(v.z), __uint_as_float(v.w), hi3);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2 *>(at + k * piece) = make_uint2(lo[k], hi3[k]);
+    for (int i = 0; i < LX; ++i) pX[i] = buffer_load16(bX, oX, (int)(i * RX * rX * sizeof(R)));
+    dtv = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        buffer_of(dtg + (size_t)t0 * a.H, ((rem - 1) * (size_t)a.H + 1) * 4), odt, 0, 0));
+  };
+  const int wB = tB * RS + in_row(tB, cB), wC = tB * RS + in_row_c(tB, cB), wX = tX * XS + in_row(tX, cX);
+  auto put = [&](uint4 v, int tile, int at, int next, int piece) {  // next: the way from four columns to the next four
+    if constexpr (IP == 1) {
+      *reinterpret_cast<uint2 *>(lds + tile + at) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2 *>(lds + tile + (at ^ next)) = make_uint2(v.z, v.w);
+    } else {
+      uint32_t w0[3], w1[3];
+      pieces<3>(__uint_as_float(v.x), __uint_as_float(v.y), w0);
+      pieces<3>(__uint_as_float(v.z), __uint_as_float(v.w), w1);
+#pragma unroll
+      for (int u = 0; u < 3; ++u) *reinterpret_cast<uint2 *>(lds + tile + u * piece + at) = make_uint2(w0[u], w1[u]);
     }
   };
   auto spill = [&]() {
+    if (hasB) {
 #pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      put(pB[i], &sB[0][i * RB + tB][cB], Q * Ns);
-      if constexpr (OUT) put(pC[i], &sC[0][i * RB + tB][cB], Q * Ns);
+      for (int i = 0; i < LB; ++i) {
+        put(pB[i], Z::B0 + i * RB * RS, wB, 8, Q * RS);
+        if constexpr (OUT) put(pC[i], Z::C0 + i * RB * RS, wC, 16, Q * RS);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < LX; ++i) put(pX[i], &sX[0][i * RX + tX][cX], Q * kXs);
+    for (int i = 0; i < LX; ++i) put(pX[i], Z::X0 + i * RX * XS, wX, 8, Q * XS);
   };
-  const float *dtg = a.dt + (size_t)begin * a.H + h;
-  auto fetch_dt = [&](int t0) {
-    const int t = t0 + lane;
-    return lane < Q && t < t_end && active ? dtg[(size_t)t * a.H] : 0.f;
-  };
-
-  // Operand of 32 columns of a row-major tile: row r of block b, columns in the order of an accumulator pair.
-  auto rows = [&](const bf16_t *tile, int stride, int b, int k) {
+  // Operand of 32 columns (step k) of rows 16 b + r, in the order of an accumulator
+  // pair: columns 32 k + 4 q .. + 3, then 32 k + 16 + 4 q .. + 3.
+  const int oR = r * RS + in_row(r, 4 * q);
+  auto rows = [&](int tile, int b, int k) {
     Frag f;
-    const bf16_t *p = tile + (16 * b + r) * stride + 32 * k + 4 * q;
-    f.h[0] = *reinterpret_cast<const s16x4 *>(p);
-    f.h[1] = *reinterpret_cast<const s16x4 *>(p + 16);
+    const char *p = lds + tile + 16 * b * RS + 128 * (k / 2);
+    f.h[0] = *reinterpret_cast<const s16x4 *>(p + (oR ^ (k % 2 * 64)));
+    f.h[1] = *reinterpret_cast<const s16x4 *>(p + (oR ^ (k % 2 * 64 + 32)));
     return f;
   };
-  // Operand of 32 tokens: column c0 + r, tokens in the same order.
-  auto cols = [&](const bf16_t *tile, int stride, int c0, int k) {
+  const int oC = r * RS + in_row_c(r, 4 * q);
+  auto rows_c = [&](int tile, int b, int k) {
     Frag f;
-    const bf16_t *p = tile + (32 * k + 4 * q + r / 4) * stride + c0 + 4 * (r % 4);
+    f.v = *reinterpret_cast<const s16x8 *>(lds + tile + 16 * b * RS + 128 * (k / 2) + (oC ^ (k % 2 * 64)));
+    return f;
+  };
+  // Operand of 32 tokens (step k) of column 16 c + r, tokens in the same order.
+  const int tr = 4 * q + r / 4;
+  const int oT = tr * RS + in_row(tr, r % 4 * 4), oTx = tr * XS + in_row(tr, xcol + r % 4 * 4);
+  auto cols = [&](int tile, int c, int k) {
+    Frag f;
+    const char *p = lds + tile + 32 * k * RS + 128 * (c / 4) + (oT ^ (c % 4 * 32));
     f.h[0] = read_tr(p);
-    f.h[1] = read_tr(p + 16 * stride);
+    f.h[1] = read_tr(p + 16 * RS);
     return f;
   };
 
   float decay = 1.f;
   fetch(t_first);
-  float dtv = fetch_dt(t_first);
   for (int t0 = t_first; t0 < t_end; t0 += Q) {
     lds_barrier();  // every wave is done with the last chunk's tiles
     spill();
     const float dt = dtv;
-    if (t0 + Q < t_end) {
-      fetch(t0 + Q);
-      dtv = fetch_dt(t0 + Q);
-    }
+    if constexpr (!OUT)
+      if (t0 + Q < t_end) fetch(t0 + Q);
     // Decays: lane = token.
     double sum = dt;
     float suf = dt;
@@ -292,13 +326,13 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
     suf = row_shift<0x101>(suf);  // the tokens after this one
     const float pre = (float)sum;
     const float epre = __builtin_amdgcn_exp2f(Al * pre);
-    if (active && pt0 == 0) {
-      sc[hi][0][lane] = pre;
-      sc[hi][1][lane] = epre;
-      sc[hi][2][lane] = __builtin_amdgcn_exp2f(Al * suf) * dt;
+    if (active && pt == 0 && lane < Q) {
+      my[lane] = pre;
+      my[Q + lane] = epre;
+      my[2 * Q + lane] = __builtin_amdgcn_exp2f(Al * suf) * dt;
       if constexpr (OUT) {
-        sc[hi][3][lane] = dt;
-        sc[hi][4][lane] = (float)(sum - (double)pre);
+        my[3 * Q + lane] = dt;
+        my[4 * Q + lane] = (float)(sum - (double)pre);
       }
     }
     float E[QB];  // the blocks' decays
@@ -306,7 +340,7 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
     for (int b = 0; b < QB; ++b) E[b] = __uint_as_float(__builtin_amdgcn_readlane(bits(epre), 16 * b + 15));
     lds_barrier();
 
-    floatx4 Yt[QB][2];
+    floatx4 Yt[QB];
     if constexpr (OUT) {
       // G^T tiles (rows j, columns t), and M^T from them for each of the workgroup's heads.
       for (int i = wave; i < TILES; i += kWaves) {
@@ -318,7 +352,7 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
         for (int k = 0; k < NK; ++k) {
           Frag bf[IP], cf[IP];
 #pragma unroll
-          for (int u = 0; u < IP; ++u) bf[u] = rows(&sB[u][0][0], Ns, jb, k), cf[u] = rows(&sC[u][0][0], Ns, tb, k);
+          for (int u = 0; u < IP; ++u) bf[u] = rows(Z::B0 + u * Q * RS, jb, k), cf[u] = rows_c(Z::C0 + u * Q * RS, tb, k);
 #pragma unroll
           for (int u = IP - 1; u >= 0; --u)
 #pragma unroll
@@ -326,17 +360,16 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
         }
         for (int hd = 0; hd < nh; ++hd) {
           const float ah = a.A[h0 + hd] * kLog2e;
+          const float *s = sc + hd * 5 * Q;
           float m[4];
           if (jb < tb) {
-            float f = sc[hd][1][16 * tb + r];  // t's block up to t, and the whole blocks between
-            for (int b = jb + 1; b < tb; ++b) f *= sc[hd][1][16 * b + 15];
-            const float4 w = *reinterpret_cast<const float4 *>(&sc[hd][2][16 * jb + 4 * q]);
+            float f = s[Q + 16 * tb + r];  // t's block up to t, and the whole blocks between
+            for (int b = jb + 1; b < tb; ++b) f *= s[Q + 16 * b + 15];
+            const float4 w = ld4(s + 2 * Q + 16 * jb + 4 * q);
             m[0] = acc[0] * (f * w.x), m[1] = acc[1] * (f * w.y), m[2] = acc[2] * (f * w.z), m[3] = acc[3] * (f * w.w);
           } else {
-            const float p1 = sc[hd][0][16 * tb + r], l1 = sc[hd][4][16 * tb + r];
-            const float4 p4 = *reinterpret_cast<const float4 *>(&sc[hd][0][16 * jb + 4 * q]);
-            const float4 d4 = *reinterpret_cast<const float4 *>(&sc[hd][3][16 * jb + 4 * q]);
-            const float4 l4 = *reinterpret_cast<const float4 *>(&sc[hd][4][16 * jb + 4 * q]);
+            const float p1 = s[16 * tb + r], l1 = s[4 * Q + 16 * tb + r];
+            const float4 p4 = ld4(s + 16 * jb + 4 * q), d4 = ld4(s + 3 * Q + 16 * jb + 4 * q), l4 = ld4(s + 4 * Q + 16 * jb + 4 * q);
             const float pj[4] = {p4.x, p4.y, p4.z, p4.w}, dj[4] = {d4.x, d4.y, d4.z, d4.w};
             const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
@@ -345,70 +378,68 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
               m[e] = 4 * q + e <= r ? v : 0.f;
             }
           }
+          mtile *to = sM + (hd * TILES + i) * kWave + lane;
           if constexpr (MP == 1)
-            sM[hd][i][lane] = make_uint2(pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3]));
+            *to = make_uint2(pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3]));
           else
-            sM[hd][i][lane] = make_float4(m[0], m[1], m[2], m[3]);
+            *to = make_float4(m[0], m[1], m[2], m[3]);
         }
       }
       // S0 C^T, transposed: rows p, columns t.
 #pragma unroll
-      for (int tb = 0; tb < QB; ++tb)
-#pragma unroll
-        for (int pt = 0; pt < 2; ++pt) Yt[tb][pt] = floatx4{0.f, 0.f, 0.f, 0.f};
-      if (np > 0) {
+      for (int tb = 0; tb < QB; ++tb) Yt[tb] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (active) {
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-          Frag sp[2][MP];
+          Frag sp[MP];
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int i = 0; i < 4; ++i) {
+            const floatx4 &s = S[2 * k + i / 2];
+            uint32_t w[MP];
+            pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const floatx4 &s = S[2 * k + i / 2][pt];
-              uint32_t w[MP];
-              pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
+            for (int u = 0; u < MP; ++u) sp[u].w[i] = w[u];
+          }
 #pragma unroll
-              for (int u = 0; u < MP; ++u) sp[pt][u].w[i] = w[u];
-            }
+          for (int v = 0; v < IP; ++v) {
+            Frag cf[QB];
 #pragma unroll
-          for (int tb = 0; tb < QB; ++tb) {
-            Frag cf[IP];
+            for (int tb = 0; tb < QB; ++tb) cf[tb] = rows_c(Z::C0 + v * Q * RS, tb, k);
 #pragma unroll
-            for (int u = 0; u < IP; ++u) cf[u] = rows(&sC[u][0][0], Ns, tb, k);
+            for (int u = MP - 1; u >= 0; --u)
+              if (u + v < 3) {
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-              for (int u = MP - 1; u >= 0; --u)
-#pragma unroll
-                for (int v = 0; v < IP; ++v)
-                  if (u + v < 3) Yt[tb][pt] = mfma32(sp[pt][u], cf[v], Yt[tb][pt]);
+                for (int tb = 0; tb < QB; ++tb) Yt[tb] = mfma32(sp[u], cf[tb], Yt[tb]);
+              }
           }
         }
         float f = 1.f;
 #pragma unroll
         for (int tb = 0; tb < QB; ++tb) {
-          const float e = f * sc[hi][1][16 * tb + r];
-          Yt[tb][0] *= e;
-          Yt[tb][1] *= e;
+          Yt[tb] *= f * my[Q + 16 * tb + r];
           f *= E[tb];
         }
       }
       lds_barrier();  // M is complete
+      if (t0 + Q < t_end) fetch(t0 + Q);  // here: the registers are free from now on
     }
 
-    if (np > 0) {
-      Frag xf[KB][2][IP];
+    if (active) {
+      Frag xf[KB][IP];
 #pragma unroll
       for (int k = 0; k < KB; ++k)
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-          for (int u = 0; u < IP; ++u) xf[k][pt][u] = cols(&sX[u][0][0], kXs, xcol + (pt < np ? 16 * pt : 0), k);
+        for (int u = 0; u < IP; ++u) {
+          const char *p = lds + Z::X0 + u * Q * XS + 32 * k * XS + oTx;
+          xf[k][u].h[0] = read_tr(p);
+          xf[k][u].h[1] = read_tr(p + 16 * XS);
+        }
       if constexpr (OUT) {
+        const mtile *mt = sM + hi * TILES * kWave + lane;
 #pragma unroll
-        for (int tb = 0; tb < QB; ++tb) {
+        for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int k = 0; k <= tb / 2; ++k) {
+          for (int tb = 2 * k; tb < QB; ++tb) {
             Frag mf[MP];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -418,7 +449,7 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
                 for (int u = 0; u < MP; ++u) mf[u].h[half] = s16x4{0, 0, 0, 0};
                 continue;
               }
-              const mtile m = sM[hi][tb * (tb + 1) / 2 + jb][lane];
+              const mtile m = mt[(tb * (tb + 1) / 2 + jb) * kWave];
               if constexpr (MP == 1) {
                 mf[0].w[2 * half] = m.x, mf[0].w[2 * half + 1] = m.y;
               } else {
@@ -430,37 +461,38 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
               }
             }
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
+            for (int u = MP - 1; u >= 0; --u)
 #pragma unroll
-              for (int u = MP - 1; u >= 0; --u)
-#pragma unroll
-                for (int v = 0; v < IP; ++v)
-                  if (u + v < 3) Yt[tb][pt] = mfma32(xf[k][pt][v], mf[u], Yt[tb][pt]);
+              for (int v = 0; v < IP; ++v)
+                if (u + v < 3) Yt[tb] = mfma32(xf[k][v], mf[u], Yt[tb]);
           }
-        }
         // y: this lane holds four neighbouring channels of token 16 tb + r.
         const float D = a.D[h];
+        const int oD = r * XS + in_row(r, xcol + 4 * q);
+        const int rem = min(Q, t_end - t0);
+        const auto bY = buffer_of((Y *)a.y + (size_t)(begin + t0) * rX + (size_t)h * P + 16 * pt,
+                                  ((rem - 1) * rX + 16) * sizeof(Y));  // rows past the end are not written
+        const int oY = (int)((r * rX + 4 * q) * sizeof(Y));
 #pragma unroll
         for (int tb = 0; tb < QB; ++tb) {
-          const int t = t0 + 16 * tb + r;
-          if (t < t_end) {
+          float x4[4], o[4];
+          load_vec<bf16_t, 4>(reinterpret_cast<const bf16_t *>(lds + Z::X0 + (IP - 1) * Q * XS + 16 * tb * XS + oD), x4);
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
-              if (pt < np) {
-                float o[4];
-                float x4[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int u = IP - 2; u >= 0; --u) {
+            float v[4];
+            load_vec<bf16_t, 4>(reinterpret_cast<const bf16_t *>(lds + Z::X0 + u * Q * XS + 16 * tb * XS + oD), v);
 #pragma unroll
-                for (int u = IP - 1; u >= 0; --u) {
-                  float v[4];
-                  load_vec<bf16_t, 4>(&sX[u][16 * tb + r][xcol + 16 * pt + 4 * q], v);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) x4[i] += v[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = fmaf(D, x4[i], Yt[tb][pt][i]);
-                store_vec<Y, 4>((Y *)a.y + ((size_t)(begin + t) * a.H + h) * P + 16 * (pt0 + pt) + 4 * q, o);
-              }
+            for (int i = 0; i < 4; ++i) x4[i] += v[i];
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = fmaf(D, x4[i], Yt[tb][i]);
+          const int step = (int)(16 * tb * rX * sizeof(Y));
+          if constexpr (sizeof(Y) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, oY, step, 0);
+          else  // step in the vector offset: a 16-byte store with a scalar offset may send the registers'
+                // next values if an instruction rewrites them right behind it (seen: the last lanes of a row)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, oY + step, 0, 0);
         }
       }
       // The state after the chunk.
@@ -469,9 +501,7 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
       for (int b = 0; b < QB; ++b) all *= E[b];
       decay *= all;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int pt = 0; pt < 2; ++pt) S[nt][pt] *= all;
+      for (int nt = 0; nt < NT; ++nt) S[nt] *= all;
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
         float f1 = 1.f;
@@ -479,52 +509,45 @@ __global__ __launch_bounds__(kThreads, sizeof(R) == 4 && NK == 4 ? 1 : 2) void s
         for (int b = 0; b < QB; ++b)
           if (b > 2 * k + 1) f1 *= E[b];
         const float f0 = f1 * E[2 * k + 1];
-        const float4 w0 = *reinterpret_cast<const float4 *>(&sc[hi][2][32 * k + 4 * q]);
-        const float4 w1 = *reinterpret_cast<const float4 *>(&sc[hi][2][32 * k + 16 + 4 * q]);
+        const float4 w0 = ld4(my + 2 * Q + 32 * k + 4 * q), w1 = ld4(my + 2 * Q + 32 * k + 16 + 4 * q);
         const float w[8] = {f0 * w0.x, f0 * w0.y, f0 * w0.z, f0 * w0.w, f1 * w1.x, f1 * w1.y, f1 * w1.z, f1 * w1.w};
-        Frag xw[2][3];
+        Frag xw[3];
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
+        for (int i = 0; i < 4; ++i) {
+          float lo = __uint_as_float(xf[k][IP - 1].w[i] << 16), up = cut(__uint_as_float(xf[k][IP - 1].w[i]));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float lo = 0.f, hi2 = 0.f;
-#pragma unroll
-            for (int u = IP - 1; u >= 0; --u) {
-              lo += __uint_as_float(xf[k][pt][u].w[i] << 16);
-              hi2 += __uint_as_float(xf[k][pt][u].w[i] & 0xFFFF0000u);
-            }
-            uint32_t pw[3];
-            pieces<3>(lo * w[2 * i], hi2 * w[2 * i + 1], pw);
-#pragma unroll
-            for (int u = 0; u < 3; ++u) xw[pt][u].w[i] = pw[u];
+          for (int u = IP - 2; u >= 0; --u) {
+            lo += __uint_as_float(xf[k][u].w[i] << 16);
+            up += cut(__uint_as_float(xf[k][u].w[i]));
           }
+          uint32_t pw[3];
+          pieces<3>(lo * w[2 * i], up * w[2 * i + 1], pw);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Frag bf[IP];
+          for (int u = 0; u < 3; ++u) xw[u].w[i] = pw[u];
+        }
 #pragma unroll
-          for (int u = 0; u < IP; ++u) bf[u] = cols(&sB[u][0][0], Ns, 16 * nt, k);
+        for (int n0 = 0; n0 < NT; n0 += 2)  // two accumulators in turn
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int v = 0; v < IP; ++v) {
+            const Frag b0 = cols(Z::B0 + v * Q * RS, n0, k), b1 = cols(Z::B0 + v * Q * RS, n0 + 1, k);
 #pragma unroll
             for (int u = 2; u >= 0; --u)
-#pragma unroll
-              for (int v = 0; v < IP; ++v)
-                if (u + v < 3) S[nt][pt] = mfma32(bf[v], xw[pt][u], S[nt][pt]);
-        }
+              if (u + v < 3) {
+                S[n0] = mfma32(b0, xw[u], S[n0]);
+                S[n0 + 1] = mfma32(b1, xw[u], S[n0 + 1]);
+              }
+          }
       }
     }
   }
 
   float *to = MODE == kOwn ? plan.state + item * states : t_end == len ? a.state + row * states : nullptr;
-  if (to) {
+  if (to && active) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
-        if (pt < np && 16 * nt < N)
-          st4(to + tile0 + (size_t)16 * pt * N + 16 * nt, make_float4(S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]));
+      if (16 * nt < N) st4(to + tile0 + 16 * nt, make_float4(S[nt][0], S[nt][1], S[nt][2], S[nt][3]));
   }
-  if (MODE == kOwn && np > 0 && wave % plan.wph == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
+  if (MODE == kOwn && active && pt == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
 }
 
 // Where each segment of a split sequence starts: the segment before it decays
@@ -551,9 +574,10 @@ __global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan,
 
 ScanPlan make_plan(const ScanArgs &a) {
   ScanPlan p{};
-  p.wph = (a.P + 31) / 32;
-  p.hw = kWaves / p.wph;
   const int Hg = a.H / a.G;
+  p.wph = a.P / 16;
+  p.hw = kWaves / p.wph < kHeads ? kWaves / p.wph : kHeads;
+  if (p.hw > Hg) p.hw = Hg;
   p.nb = (Hg + p.hw - 1) / p.hw;
   const int per = a.G * p.nb;
   p.fnb = make_fastdiv((uint32_t)p.nb);
@@ -570,18 +594,25 @@ ScanPlan make_plan(const ScanArgs &a) {
 
 size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.items * a.H * 4 + 255) / 256 * 256; }
 
+template <typename R, typename Y, int NK, int MODE>
+void launch_part(const ScanArgs &a, const ScanPlan &p, dim3 grid, hipStream_t st) {
+  constexpr int most = 160 * 1024;
+  static_assert(Shape_<R, Y, NK, MODE>::lds(kHeads) <= most, "LDS of a workgroup");
+  hipLaunchKernelGGL((scan_k<R, Y, NK, MODE>), grid, dim3(kThreads), (Shape_<R, Y, NK, MODE>::lds(p.hw)), st, a, p);
+}
+
 template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
   const int64_t blocks = ((int64_t)p.items * a.G + kXcds - 1) / kXcds * kXcds * p.nb;
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffLL || (int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
-  const dim3 grid((uint32_t)blocks), block(kThreads);
+  const dim3 grid((uint32_t)blocks);
   if (!p.seg) {
-    hipLaunchKernelGGL((scan_k<R, Y, NK, kAll>), grid, block, 0, st, a, p);
+    launch_part<R, Y, NK, kAll>(a, p, grid, st);
   } else {
-    hipLaunchKernelGGL((scan_k<R, Y, NK, kOwn>), grid, block, 0, st, a, p);
-    hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), block, 0, st, a, p, make_fastdiv((uint32_t)per_seq));
-    hipLaunchKernelGGL((scan_k<R, Y, NK, kFrom>), grid, block, 0, st, a, p);
+    launch_part<R, Y, NK, kOwn>(a, p, grid, st);
+    hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
+    launch_part<R, Y, NK, kFrom>(a, p, grid, st);
   }
   return (int)hipGetLastError();
 }
