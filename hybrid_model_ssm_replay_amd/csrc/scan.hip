@@ -47,20 +47,19 @@ constexpr int kCols = 16 * kWaves;  // x columns of a workgroup
 constexpr int kHeads = 4;           // heads of a workgroup at most
 constexpr float kLog2e = 1.4426950408889634f;
 
-// LDS tiles are [token][column] in bf16 without padding, in 16-byte granules.
-// B and x are read 4 rows at 16 neighbouring columns (the transposing read) and, B
-// less often, 16 rows at one column, 8 bytes a lane each: the granules of a row are
-// permuted by an exclusive or, and the halves of a granule swapped, so that the 16
-// lanes of either read meet each bank once.
+// LDS tiles are rows of 256 bytes, a token each, in 16-byte granules of eight
+// bf16.  A read serves 256 bytes at a time, so its lanes' granules must differ in
+// their low four bits; the granules of a row are permuted by an exclusive or that
+// does that for the reads at hand (measured: no conflicts).
+constexpr int kRow = 256;
+// B and x: 4 rows at 16 neighbouring columns (the transposing read), and 16 rows
+// at one column; 32 lanes of 8 bytes at a time each.
 __device__ __forceinline__ int in_row(int row, int c) {  // byte of column c (a multiple of 4) in its row
-  const int g = 2 * (row & 3) | (row >> 2 & 1), half = row >> 3 & 1;
-  return ((c >> 3 ^ g) << 4) + (((c >> 2 & 1) ^ half) << 3);
+  return ((c >> 3 ^ (2 * (row & 7) | (row >> 3 & 1))) << 4) + (c >> 2 & 1) * 8;
 }
-// C is read as operands only: a granule holds a lane's operand of one 32-column
-// step, columns 32 k + 4 q .. + 3 and 32 k + 16 + 4 q .. + 3.
-__device__ __forceinline__ int in_row_c(int row, int c) {
-  return (((c >> 5 << 2 | (c >> 2 & 3)) ^ (row & 7)) << 4) + (c >> 4 & 1) * 8;
-}
+// C: a granule holds a lane's operand of one 32-column step k, columns 32 k + 4 q
+// .. + 3 and 32 k + 16 + 4 q .. + 3, and is read whole by 16 rows at a time.
+__device__ __forceinline__ int in_row_c(int row, int k, int q) { return ((4 * k + q) ^ (row & 15)) << 4; }
 
 union Frag {  // eight bf16 of one lane: an operand of the 16x16x32 product
   s16x8 v;
@@ -74,6 +73,19 @@ __device__ __forceinline__ floatx4 mfma32(const Frag &a, const Frag &b, floatx4 
 
 __device__ __forceinline__ s16x4 read_tr(const char *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
 
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+
+// A value all lanes share, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(bits(v)));
+}
+
+// v, but not known to the compiler to be what it was before.
+__device__ __forceinline__ int again(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // A buffer of n bytes: loads past its end give zeros, stores past it do nothing.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, size_t n) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)n, 0x00020000);
@@ -84,7 +96,6 @@ __device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t b, int at,
 
 // The upper halves of two words: b's in the upper half.
 __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
 __device__ __forceinline__ float cut(float v) { return __uint_as_float(bits(v) & 0xFFFF0000u); }
 
 // Two values as MP words of bf16 pairs: one piece rounds to nearest, three
@@ -101,6 +112,38 @@ __device__ __forceinline__ void pieces(float a, float b, uint32_t (&w)[MP]) {
     w[2] = upper(bits(a), bits(b));
   }
 }
+
+// Eight neighbouring elements of a record on their way to a granule of LDS: as
+// they are, or float32 cut in three bf16 pieces, a tile each.
+template <typename R>
+struct Granule {
+  uint4 v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, int plus) { v = buffer_load16(b, at, plus); }
+  __device__ __forceinline__ void load2(__amdgpu_buffer_rsrc_t b, int at0, int at1, int plus) {  // four and four
+    const i32x2 x = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(b, at0, plus, 0));
+    const i32x2 y = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(b, at1, plus, 0));
+    v = make_uint4(x[0], x[1], y[0], y[1]);
+  }
+  __device__ __forceinline__ void put(char *to, int) const { *reinterpret_cast<uint4 *>(to) = v; }
+};
+template <>
+struct Granule<float> {
+  uint4 v, w;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, int plus) { load2(b, at, at + 16, plus); }
+  __device__ __forceinline__ void load2(__amdgpu_buffer_rsrc_t b, int at0, int at1, int plus) {
+    v = buffer_load16(b, at0, plus);
+    w = buffer_load16(b, at1, plus);
+  }
+  __device__ __forceinline__ void put(char *to, int piece) const {
+    uint32_t a[3], b[3], c[3], d[3];
+    pieces<3>(__uint_as_float(v.x), __uint_as_float(v.y), a);
+    pieces<3>(__uint_as_float(v.z), __uint_as_float(v.w), b);
+    pieces<3>(__uint_as_float(w.x), __uint_as_float(w.y), c);
+    pieces<3>(__uint_as_float(w.z), __uint_as_float(w.w), d);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) *reinterpret_cast<uint4 *>(to + u * piece) = make_uint4(a[u], b[u], c[u], d[u]);
+  }
+};
 
 template <int CTRL>
 __device__ __forceinline__ float row_shift(float v) {  // within 16 lanes, zeros shifted in
@@ -147,7 +190,7 @@ struct Shape_ {
   static constexpr int MP = sizeof(Y) == 4 ? 3 : 1;        // pieces of M and S
   static constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;  // blocks and tokens of a chunk
   static constexpr int TILES = QB * (QB + 1) / 2;
-  static constexpr int RS = NK > 2 ? 256 : 128, XS = 2 * kCols;  // bytes of a row of B, C and of x
+  static constexpr int RS = kRow, XS = kRow;  // bytes of a row of B, C and of x
   static constexpr int B0 = 0, C0 = B0 + IP * Q * RS, X0 = C0 + (OUT ? IP * Q * RS : 0), SC0 = X0 + IP * Q * XS;
   static constexpr int SC = 5 * Q * 4;                           // per head: five values a token
   static constexpr int M = TILES * kWave * (MP == 1 ? 8 : 16);   // per head: M
@@ -159,9 +202,8 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   typedef Shape_<R, Y, NK, MODE> Z;
   constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
   constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
-  constexpr int V = 16 / (int)sizeof(R);                 // elements of a 16-byte load
-  constexpr int NV = 32 * NK / V, XV = kCols / V;        // loads of a row
-  constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one load of the workgroup
+  constexpr int NV = 4 * NK, XV = kCols / 8;             // granules of a row
+  constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one granule a thread
   constexpr int LB = Q > RB ? Q / RB : 1, LX = Q / RX;
   static_assert(RX % 16 == 0 && RB % 16 == 0, "a thread's rows share their permutation");
   constexpr bool OUT = Z::OUT;
@@ -203,7 +245,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   const int h = h0 + hi;
   const int xcol = hi * P + 16 * pt;
   const int ncols = nh * P;
-  const float Al = a.A[h] * kLog2e;
+  const float Al = uniform(a.A[h] * kLog2e), D = OUT ? uniform(a.D[h]) : 0.f;
   float *const sc = reinterpret_cast<float *>(lds + Z::SC0);                               // [heads][5][Q]
   mtile *const sM = reinterpret_cast<mtile *>(lds + Z::SC0 + plan.hw * Z::SC);             // [heads][TILES][64]
   float *const my = sc + hi * 5 * Q;
@@ -228,81 +270,76 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
 
   // Global to registers through buffers that end with the chunk's last row: rows
   // past it read as zeros, and so do the columns of threads without a place.
-  uint4 pB[LB], pC[OUT ? LB : 1], pX[LX];
+  typedef Granule<R> Gr;
+  Gr pB[LB], pC[OUT ? LB : 1], pX[LX];
   const size_t rB = (size_t)a.G * N, rX = (size_t)a.H * P;
   const R *Bg = (const R *)a.Bm + (size_t)begin * rB + (size_t)g * N;
   const R *Cg = (const R *)a.Cm + (size_t)begin * rB + (size_t)g * N;
   const R *Xg = (const R *)a.x + (size_t)begin * rX + (size_t)h0 * P;
   const float *dtg = a.dt + (size_t)begin * a.H + h;
   constexpr int kNowhere = 0x7fffff00;
-  const int tB = tid / NV, cB = tid % NV * V, tX = tid / XV, cX = tid % XV * V;
-  const bool hasB = RB <= Q || tB < Q;  // narrow states leave threads without a piece of B and C
-  const int oB = hasB && cB < N ? (int)((tB * rB + cB) * sizeof(R)) : kNowhere;
-  const int oX = cX < ncols ? (int)((tX * rX + cX) * sizeof(R)) : kNowhere;
-  const int odt = lane < Q ? lane * a.H * 4 : kNowhere;
   float dtv = 0.f;
+  // Places in global memory and LDS are computed anew from the thread's number at each
+  // use: a few operations, where 14 registers would otherwise push others into memory.
   auto fetch = [&](int t0) {
+    const int id = again(tid);
+    const int tB = id / NV, cB = id % NV * 8, tX = id / XV, cX = id % XV * 8;
+    const int cC = 32 * (id % NV / 4) + 4 * (id % 4);  // C's granules go by operands
+    const bool hasB = RB <= Q || tB < Q;               // narrow states leave threads without a piece of B and C
+    const int oB = hasB && cB < N ? (int)((tB * rB + cB) * sizeof(R)) : kNowhere;
+    const int oC = hasB && cC < N ? (int)((tB * rB + cC) * sizeof(R)) : kNowhere;
+    const int oC1 = NK > 1 || cC + 16 < N ? oC + 16 * (int)sizeof(R) : kNowhere;
+    const int oX = cX < ncols ? (int)((tX * rX + cX) * sizeof(R)) : kNowhere;
+    const int odt = id % kWave < Q ? id % kWave * a.H * 4 : kNowhere;
     const int rem = min(Q, t_end - t0);
+    dtv = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        buffer_of(dtg + (size_t)t0 * a.H, ((rem - 1) * (size_t)a.H + 1) * 4), odt, 0, 0));
     const auto bB = buffer_of(Bg + t0 * rB, ((rem - 1) * rB + N) * sizeof(R));
     const auto bX = buffer_of(Xg + t0 * rX, ((rem - 1) * rX + ncols) * sizeof(R));
 #pragma unroll
-    for (int i = 0; i < LB; ++i) pB[i] = buffer_load16(bB, oB, (int)(i * RB * rB * sizeof(R)));
+    for (int i = 0; i < LB; ++i) pB[i].load(bB, oB, (int)(i * RB * rB * sizeof(R)));
     if constexpr (OUT) {
       const auto bC = buffer_of(Cg + t0 * rB, ((rem - 1) * rB + N) * sizeof(R));
 #pragma unroll
-      for (int i = 0; i < LB; ++i) pC[i] = buffer_load16(bC, oB, (int)(i * RB * rB * sizeof(R)));
+      for (int i = 0; i < LB; ++i) pC[i].load2(bC, oC, oC1, (int)(i * RB * rB * sizeof(R)));
     }
 #pragma unroll
-    for (int i = 0; i < LX; ++i) pX[i] = buffer_load16(bX, oX, (int)(i * RX * rX * sizeof(R)));
-    dtv = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        buffer_of(dtg + (size_t)t0 * a.H, ((rem - 1) * (size_t)a.H + 1) * 4), odt, 0, 0));
-  };
-  const int wB = tB * RS + in_row(tB, cB), wC = tB * RS + in_row_c(tB, cB), wX = tX * XS + in_row(tX, cX);
-  auto put = [&](uint4 v, int tile, int at, int next, int piece) {  // next: the way from four columns to the next four
-    if constexpr (IP == 1) {
-      *reinterpret_cast<uint2 *>(lds + tile + at) = make_uint2(v.x, v.y);
-      *reinterpret_cast<uint2 *>(lds + tile + (at ^ next)) = make_uint2(v.z, v.w);
-    } else {
-      uint32_t w0[3], w1[3];
-      pieces<3>(__uint_as_float(v.x), __uint_as_float(v.y), w0);
-      pieces<3>(__uint_as_float(v.z), __uint_as_float(v.w), w1);
-#pragma unroll
-      for (int u = 0; u < 3; ++u) *reinterpret_cast<uint2 *>(lds + tile + u * piece + at) = make_uint2(w0[u], w1[u]);
-    }
+    for (int i = 0; i < LX; ++i) pX[i].load(bX, oX, (int)(i * RX * rX * sizeof(R)));
   };
   auto spill = [&]() {
-    if (hasB) {
+    const int id = again(tid);
+    const int tB = id / NV, tX = id / XV;
+    char *toB = lds + Z::B0 + tB * RS + in_row(tB, id % NV * 8), *toC = lds + Z::C0 + tB * RS + in_row_c(tB, id % NV / 4, id % 4);
+    char *toX = lds + Z::X0 + tX * XS + in_row(tX, id % XV * 8);
+    if (RB <= Q || tB < Q) {
 #pragma unroll
       for (int i = 0; i < LB; ++i) {
-        put(pB[i], Z::B0 + i * RB * RS, wB, 8, Q * RS);
-        if constexpr (OUT) put(pC[i], Z::C0 + i * RB * RS, wC, 16, Q * RS);
+        pB[i].put(toB + i * RB * RS, Q * RS);
+        if constexpr (OUT) pC[i].put(toC + i * RB * RS, Q * RS);
       }
     }
 #pragma unroll
-    for (int i = 0; i < LX; ++i) put(pX[i], Z::X0 + i * RX * XS, wX, 8, Q * XS);
+    for (int i = 0; i < LX; ++i) pX[i].put(toX + i * RX * XS, Q * XS);
   };
+
   // Operand of 32 columns (step k) of rows 16 b + r, in the order of an accumulator
   // pair: columns 32 k + 4 q .. + 3, then 32 k + 16 + 4 q .. + 3.
-  const int oR = r * RS + in_row(r, 4 * q);
-  auto rows = [&](int tile, int b, int k) {
+  auto rows = [&](int tile, int b, int k, int oR) {
     Frag f;
-    const char *p = lds + tile + 16 * b * RS + 128 * (k / 2);
-    f.h[0] = *reinterpret_cast<const s16x4 *>(p + (oR ^ (k % 2 * 64)));
-    f.h[1] = *reinterpret_cast<const s16x4 *>(p + (oR ^ (k % 2 * 64 + 32)));
+    const char *p = lds + tile + 16 * b * RS;
+    f.h[0] = *reinterpret_cast<const s16x4 *>(p + (oR ^ (k * 64)));
+    f.h[1] = *reinterpret_cast<const s16x4 *>(p + (oR ^ (k * 64 + 32)));
     return f;
   };
-  const int oC = r * RS + in_row_c(r, 4 * q);
-  auto rows_c = [&](int tile, int b, int k) {
+  auto rows_c = [&](int tile, int b, int k, int oC) {
     Frag f;
-    f.v = *reinterpret_cast<const s16x8 *>(lds + tile + 16 * b * RS + 128 * (k / 2) + (oC ^ (k % 2 * 64)));
+    f.v = *reinterpret_cast<const s16x8 *>(lds + tile + 16 * b * RS + (oC ^ (k * 64)));
     return f;
   };
   // Operand of 32 tokens (step k) of column 16 c + r, tokens in the same order.
-  const int tr = 4 * q + r / 4;
-  const int oT = tr * RS + in_row(tr, r % 4 * 4), oTx = tr * XS + in_row(tr, xcol + r % 4 * 4);
-  auto cols = [&](int tile, int c, int k) {
+  auto cols = [&](int tile, int c, int k, int oT) {
     Frag f;
-    const char *p = lds + tile + 32 * k * RS + 128 * (c / 4) + (oT ^ (c % 4 * 32));
+    const char *p = lds + tile + 32 * k * RS + (oT ^ (c * 32));
     f.h[0] = read_tr(p);
     f.h[1] = read_tr(p + 16 * RS);
     return f;
@@ -324,8 +361,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
     sum += row_shift<0x114>(sum), suf += row_shift<0x104>(suf);
     sum += row_shift<0x118>(sum), suf += row_shift<0x108>(suf);
     suf = row_shift<0x101>(suf);  // the tokens after this one
+    sum *= Al;  // as an exponent of 2
     const float pre = (float)sum;
-    const float epre = __builtin_amdgcn_exp2f(Al * pre);
+    const float epre = __builtin_amdgcn_exp2f(pre);
     if (active && pt == 0 && lane < Q) {
       my[lane] = pre;
       my[Q + lane] = epre;
@@ -342,6 +380,8 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
 
     floatx4 Yt[QB];
     if constexpr (OUT) {
+      const int la = again(lane), oR = la % 16 * RS + in_row(la % 16, la / 16 * 4);
+      const int oC = la % 16 * RS + in_row_c(la % 16, 0, la / 16);
       // G^T tiles (rows j, columns t), and M^T from them for each of the workgroup's heads.
       for (int i = wave; i < TILES; i += kWaves) {
         int tb = 0;
@@ -352,14 +392,13 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
         for (int k = 0; k < NK; ++k) {
           Frag bf[IP], cf[IP];
 #pragma unroll
-          for (int u = 0; u < IP; ++u) bf[u] = rows(Z::B0 + u * Q * RS, jb, k), cf[u] = rows_c(Z::C0 + u * Q * RS, tb, k);
+          for (int u = 0; u < IP; ++u) bf[u] = rows(Z::B0 + u * Q * RS, jb, k, oR), cf[u] = rows_c(Z::C0 + u * Q * RS, tb, k, oC);
 #pragma unroll
           for (int u = IP - 1; u >= 0; --u)
 #pragma unroll
             for (int v = IP - 1 - u; v >= 0; --v) acc = mfma32(bf[u], cf[v], acc);
         }
         for (int hd = 0; hd < nh; ++hd) {
-          const float ah = a.A[h0 + hd] * kLog2e;
           const float *s = sc + hd * 5 * Q;
           float m[4];
           if (jb < tb) {
@@ -374,7 +413,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
             const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float v = acc[e] * (__builtin_amdgcn_exp2f(ah * ((p1 - pj[e]) + (l1 - lj[e]))) * dj[e]);
+              const float v = acc[e] * (__builtin_amdgcn_exp2f((p1 - pj[e]) + (l1 - lj[e])) * dj[e]);
               m[e] = 4 * q + e <= r ? v : 0.f;
             }
           }
@@ -404,7 +443,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
           for (int v = 0; v < IP; ++v) {
             Frag cf[QB];
 #pragma unroll
-            for (int tb = 0; tb < QB; ++tb) cf[tb] = rows_c(Z::C0 + v * Q * RS, tb, k);
+            for (int tb = 0; tb < QB; ++tb) cf[tb] = rows_c(Z::C0 + v * Q * RS, tb, k, oC);
 #pragma unroll
             for (int u = MP - 1; u >= 0; --u)
               if (u + v < 3) {
@@ -425,6 +464,8 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
     }
 
     if (active) {
+      const int la = again(lane), tr = la / 16 * 4 + la % 16 / 4;
+      const int oT = tr * RS + in_row(tr, la % 4 * 4), oTx = tr * XS + in_row(tr, xcol + la % 4 * 4);
       Frag xf[KB][IP];
 #pragma unroll
       for (int k = 0; k < KB; ++k)
@@ -467,7 +508,6 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
                 if (u + v < 3) Yt[tb] = mfma32(xf[k][v], mf[u], Yt[tb]);
           }
         // y: this lane holds four neighbouring channels of token 16 tb + r.
-        const float D = a.D[h];
         const int oD = r * XS + in_row(r, xcol + 4 * q);
         const int rem = min(Q, t_end - t0);
         const auto bY = buffer_of((Y *)a.y + (size_t)(begin + t0) * rX + (size_t)h * P + 16 * pt,
@@ -529,7 +569,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
         for (int n0 = 0; n0 < NT; n0 += 2)  // two accumulators in turn
 #pragma unroll
           for (int v = 0; v < IP; ++v) {
-            const Frag b0 = cols(Z::B0 + v * Q * RS, n0, k), b1 = cols(Z::B0 + v * Q * RS, n0 + 1, k);
+            const Frag b0 = cols(Z::B0 + v * Q * RS, n0, k, oT), b1 = cols(Z::B0 + v * Q * RS, n0 + 1, k, oT);
 #pragma unroll
             for (int u = 2; u >= 0; --u)
               if (u + v < 3) {
