@@ -73,6 +73,8 @@ __device__ __forceinline__ floatx4 mfma32(const Frag &a, const Frag &b, floatx4 
 
 __device__ __forceinline__ s16x4 read_tr(const char *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
 
+__device__ __forceinline__ float upper(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float lower(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
 
 // A value all lanes share, in a scalar register.
@@ -94,22 +96,18 @@ __device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t b, int at,
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, at, plus, 0));
 }
 
-// The upper halves of two words: b's in the upper half.
-__device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-__device__ __forceinline__ float cut(float v) { return __uint_as_float(bits(v) & 0xFFFF0000u); }
-
-// Two values as MP words of bf16 pairs: one piece rounds to nearest, three
-// pieces cut (8 bits each: together the 24 bits of the value).
+// Two values as MP words of bf16 pairs: one piece rounds to nearest, three pieces
+// cut (8 bits each: together the 24 bits of the value).
 template <int MP>
 __device__ __forceinline__ void pieces(float a, float b, uint32_t (&w)[MP]) {
   if constexpr (MP == 1) {
     w[0] = pack_bf16(a, b);
   } else {
-    w[0] = upper(bits(a), bits(b));
-    a -= cut(a), b -= cut(b);
-    w[1] = upper(bits(a), bits(b));
-    a -= cut(a), b -= cut(b);
-    w[2] = upper(bits(a), bits(b));
+#pragma unroll
+    for (int u = 0; u < MP; ++u) {
+      w[u] = __builtin_amdgcn_perm(bits(b), bits(a), 0x07060302u);  // the upper halves, b's on top
+      if (u + 1 < MP) a -= upper(bits(a)), b -= upper(bits(b));
+    }
   }
 }
 
@@ -166,6 +164,17 @@ struct MTile<1> {
   typedef uint2 type;
 };
 
+// The lower triangle's tiles, diagonal ones in the middle: eight waves take tile w
+// and w + 8 of the ten, and a diagonal tile costs more.
+template <int QB>
+__device__ __forceinline__ int tile_row(int i) {
+  return (QB == 4 ? 0x3332103221ull >> 4 * i : 0x101ull >> 4 * i) & 15;
+}
+template <int QB>
+__device__ __forceinline__ int tile_col(int i) {
+  return (QB == 4 ? 0x2132100100ull >> 4 * i : 0x100ull >> 4 * i) & 15;
+}
+
 struct ScanPlan {
   int seg;        // tokens of a segment (a multiple of 64), or 0: sequences are not split
   int items;      // segments of all sequences
@@ -192,15 +201,16 @@ struct Shape_ {
   static constexpr int TILES = QB * (QB + 1) / 2;
   static constexpr int RS = kRow, XS = kRow;  // bytes of a row of B, C and of x
   static constexpr int B0 = 0, C0 = B0 + IP * Q * RS, X0 = C0 + (OUT ? IP * Q * RS : 0), SC0 = X0 + IP * Q * XS;
-  static constexpr int SC = 5 * Q * 4;                           // per head: five values a token
-  static constexpr int M = TILES * kWave * (MP == 1 ? 8 : 16);   // per head: M
+  static constexpr int SC = (5 * Q + 4) * 4;                     // per head: five values a token, and D
+  static constexpr int MT = TILES + (MP == 1 ? QB : 0);          // tiles of M, and what rounding left of the diagonal ones
+  static constexpr int M = MT * kWave * (MP == 1 ? 8 : 16);      // per head: M
   static constexpr int lds(int heads) { return SC0 + heads * (SC + (OUT ? M : 0)); }
 };
 
 template <typename R, typename Y, int NK, int MODE>
 __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan) {
   typedef Shape_<R, Y, NK, MODE> Z;
-  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
+  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, MT = Z::MT, RS = Z::RS, XS = Z::XS;
   constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
   constexpr int NV = 4 * NK, XV = kCols / 8;             // granules of a row
   constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one granule a thread
@@ -246,9 +256,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   const int xcol = hi * P + 16 * pt;
   const int ncols = nh * P;
   const float Al = uniform(a.A[h] * kLog2e), D = OUT ? uniform(a.D[h]) : 0.f;
-  float *const sc = reinterpret_cast<float *>(lds + Z::SC0);                               // [heads][5][Q]
+  float *const sc = reinterpret_cast<float *>(lds + Z::SC0);                               // [heads]{[5][Q], D}
   mtile *const sM = reinterpret_cast<mtile *>(lds + Z::SC0 + plan.hw * Z::SC);             // [heads][TILES][64]
-  float *const my = sc + hi * 5 * Q;
+  float *const my = sc + hi * (5 * Q + 4);
 
   // The state: S^T tile nt, rows n = 16 nt + 4 q + i, column p = r of the wave's tile.
   floatx4 S[NT];
@@ -345,6 +355,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
     return f;
   };
 
+  if (OUT && active && pt == 0 && lane == 0) my[5 * Q] = D;  // read after two barriers
   float decay = 1.f;
   fetch(t_first);
   for (int t0 = t_first; t0 < t_end; t0 += Q) {
@@ -383,10 +394,12 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
       const int la = again(lane), oR = la % 16 * RS + in_row(la % 16, la / 16 * 4);
       const int oC = la % 16 * RS + in_row_c(la % 16, 0, la / 16);
       // G^T tiles (rows j, columns t), and M^T from them for each of the workgroup's heads.
-      for (int i = wave; i < TILES; i += kWaves) {
-        int tb = 0;
-        while ((tb + 1) * (tb + 2) / 2 <= i) ++tb;
-        const int jb = i - tb * (tb + 1) / 2;
+      // A wave takes a tile, or a tile for one head where there are no more of those than waves.
+      const bool by_head = TILES * nh <= kWaves;
+      for (int i = wave; i < (by_head ? TILES * nh : TILES); i += kWaves) {
+        const int tile = by_head ? i % TILES : i;
+        // The dear diagonal tiles meet waves that get no second one.
+        const int tb = tile_row<QB>(tile), jb = tile_col<QB>(tile);
         floatx4 acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
@@ -398,8 +411,8 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
 #pragma unroll
             for (int v = IP - 1 - u; v >= 0; --v) acc = mfma32(bf[u], cf[v], acc);
         }
-        for (int hd = 0; hd < nh; ++hd) {
-          const float *s = sc + hd * 5 * Q;
+        for (int hd = by_head ? i / TILES : 0; hd < (by_head ? i / TILES + 1 : nh); ++hd) {
+          const float *s = sc + hd * (5 * Q + 4);
           float m[4];
           if (jb < tb) {
             float f = s[Q + 16 * tb + r];  // t's block up to t, and the whole blocks between
@@ -414,14 +427,20 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float v = acc[e] * (__builtin_amdgcn_exp2f((p1 - pj[e]) + (l1 - lj[e])) * dj[e]);
-              m[e] = 4 * q + e <= r ? v : 0.f;
+              m[e] = 4 * q + e < r ? v : 4 * q + e == r ? v + s[5 * Q] : 0.f;  // D x_t rides along
             }
           }
-          mtile *to = sM + (hd * TILES + i) * kWave + lane;
-          if constexpr (MP == 1)
-            *to = make_uint2(pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3]));
-          else
+          mtile *to = sM + (hd * MT + tb * (tb + 1) / 2 + jb) * kWave + lane;
+          if constexpr (MP == 1) {
+            const uint2 w = make_uint2(pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3]));
+            *to = w;
+            if (jb == tb) {
+              sM[(hd * MT + TILES + tb) * kWave + lane] = make_uint2(pack_bf16(m[0] - lower(w.x), m[1] - upper(w.x)),
+                                                                     pack_bf16(m[2] - lower(w.y), m[3] - upper(w.y)));
+            }
+          } else {
             *to = make_float4(m[0], m[1], m[2], m[3]);
+          }
         }
       }
       // S0 C^T, transposed: rows p, columns t.
@@ -476,7 +495,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
           xf[k][u].h[1] = read_tr(p + 16 * XS);
         }
       if constexpr (OUT) {
-        const mtile *mt = sM + hi * TILES * kWave + lane;
+        const mtile *mt = sM + hi * MT * kWave + lane;
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -506,26 +525,23 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
 #pragma unroll
               for (int v = 0; v < IP; ++v)
                 if (u + v < 3) Yt[tb] = mfma32(xf[k][v], mf[u], Yt[tb]);
+            if constexpr (MP == 1)
+              if (tb / 2 == k) {
+                const mtile m = mt[(TILES + tb) * kWave];
+                Frag lf;
+                lf.h[1 - tb % 2] = s16x4{0, 0, 0, 0};
+                lf.w[tb % 2 * 2] = m.x, lf.w[tb % 2 * 2 + 1] = m.y;
+                Yt[tb] = mfma32(xf[k][0], lf, Yt[tb]);
+              }
           }
         // y: this lane holds four neighbouring channels of token 16 tb + r.
-        const int oD = r * XS + in_row(r, xcol + 4 * q);
         const int rem = min(Q, t_end - t0);
         const auto bY = buffer_of((Y *)a.y + (size_t)(begin + t0) * rX + (size_t)h * P + 16 * pt,
                                   ((rem - 1) * rX + 16) * sizeof(Y));  // rows past the end are not written
         const int oY = (int)((r * rX + 4 * q) * sizeof(Y));
 #pragma unroll
         for (int tb = 0; tb < QB; ++tb) {
-          float x4[4], o[4];
-          load_vec<bf16_t, 4>(reinterpret_cast<const bf16_t *>(lds + Z::X0 + (IP - 1) * Q * XS + 16 * tb * XS + oD), x4);
-#pragma unroll
-          for (int u = IP - 2; u >= 0; --u) {
-            float v[4];
-            load_vec<bf16_t, 4>(reinterpret_cast<const bf16_t *>(lds + Z::X0 + u * Q * XS + 16 * tb * XS + oD), v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x4[i] += v[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = fmaf(D, x4[i], Yt[tb][i]);
+          const floatx4 o = Yt[tb];
           const int step = (int)(16 * tb * rX * sizeof(Y));
           if constexpr (sizeof(Y) == 2)
             __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, oY, step, 0);
@@ -554,12 +570,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
         Frag xw[3];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float lo = __uint_as_float(xf[k][IP - 1].w[i] << 16), up = cut(__uint_as_float(xf[k][IP - 1].w[i]));
+          float lo = lower(xf[k][IP - 1].w[i]), up = upper(xf[k][IP - 1].w[i]);
 #pragma unroll
-          for (int u = IP - 2; u >= 0; --u) {
-            lo += __uint_as_float(xf[k][u].w[i] << 16);
-            up += cut(__uint_as_float(xf[k][u].w[i]));
-          }
+          for (int u = IP - 2; u >= 0; --u) lo += lower(xf[k][u].w[i]), up += upper(xf[k][u].w[i]);
           uint32_t pw[3];
           pieces<3>(lo * w[2 * i], up * w[2 * i + 1], pw);
 #pragma unroll
