@@ -14,7 +14,7 @@
 // rounding left of it), so that the difference is good to float32 itself.
 //
 // A workgroup takes up to 128 columns of x (heads of one group, which share
-// B, C and G) of one sequence, and walks its chunks; a wave owns 16 columns of
+// B, C and G) of one sequence, and walks its chunks; a wave owns 32 columns of
 // one head with their whole state in registers (S^T as accumulators of
 // v_mfma_f32_16x16x32_bf16: lane l holds rows n = 4 (l / 16) + i of column p =
 // l % 16).  That layout is at once the operand layout of S C^T with the sum
@@ -41,9 +41,10 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kCols = 16 * kWaves;  // x columns of a workgroup
+constexpr int CT = 2;                    // 16-column tiles of a wave
+constexpr int kCols = 16 * CT * kWaves;  // x columns of a workgroup
 constexpr int kHeads = 4;           // heads of a workgroup at most
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -154,25 +155,18 @@ __device__ __forceinline__ double row_shift(double v) {
                                               __builtin_amdgcn_update_dpp(0, w.y, CTRL, 0xF, 0xF, true)));
 }
 
-// Four entries of M of one lane: rounded to bf16, or float32 to be cut in pieces when used.
-template <int MP>
-struct MTile {
-  typedef float4 type;
-};
-template <>
-struct MTile<1> {
-  typedef uint2 type;
-};
+// Tile i of the lower triangle, row by row.
+__device__ __forceinline__ int tile_row(int i) { return 0x3333222110ull >> 4 * i & 15; }
+__device__ __forceinline__ int tile_col(int i) { return 0x3210210100ull >> 4 * i & 15; }
 
-// The lower triangle's tiles, diagonal ones in the middle: eight waves take tile w
-// and w + 8 of the ten, and a diagonal tile costs more.
-template <int QB>
-__device__ __forceinline__ int tile_row(int i) {
-  return (QB == 4 ? 0x3332103221ull >> 4 * i : 0x101ull >> 4 * i) & 15;
-}
-template <int QB>
-__device__ __forceinline__ int tile_col(int i) {
-  return (QB == 4 ? 0x2132100100ull >> 4 * i : 0x100ull >> 4 * i) & 15;
+// Asks the compiler to issue N matrix products with V other vector operations behind each.
+template <int N, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+  }
 }
 
 struct ScanPlan {
@@ -201,33 +195,34 @@ struct Shape_ {
   static constexpr int TILES = QB * (QB + 1) / 2;
   static constexpr int RS = kRow, XS = kRow;  // bytes of a row of B, C and of x
   static constexpr int B0 = 0, C0 = B0 + IP * Q * RS, X0 = C0 + (OUT ? IP * Q * RS : 0), SC0 = X0 + IP * Q * XS;
-  static constexpr int SC = (5 * Q + 4) * 4;                     // per head: five values a token, and D
-  static constexpr int MT = TILES + (MP == 1 ? QB : 0);          // tiles of M, and what rounding left of the diagonal ones
-  static constexpr int M = MT * kWave * (MP == 1 ? 8 : 16);      // per head: M
-  static constexpr int lds(int heads) { return SC0 + heads * (SC + (OUT ? M : 0)); }
+  static constexpr int SC = 6 * Q * 4;  // per head: six values a token
+  static constexpr int G0 = SC0 + kHeads * SC;
+  static constexpr int LDS = G0 + (OUT ? TILES * kWave * 16 : 0);
 };
 
 template <typename R, typename Y, int NK, int MODE>
-__global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void scan_k(ScanArgs a, ScanPlan plan) {
   typedef Shape_<R, Y, NK, MODE> Z;
-  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, MT = Z::MT, RS = Z::RS, XS = Z::XS;
+  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
   constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
   constexpr int NV = 4 * NK, XV = kCols / 8;             // granules of a row
   constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one granule a thread
   constexpr int LB = Q > RB ? Q / RB : 1, LX = Q / RX;
   static_assert(RX % 16 == 0 && RB % 16 == 0, "a thread's rows share their permutation");
   constexpr bool OUT = Z::OUT;
-  typedef typename MTile<MP>::type mtile;
   extern __shared__ __attribute__((aligned(16))) char lds[];
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane % 16, q = lane / 16;
   // Unit u on XCD u % 8 (workgroup i runs on XCD i % 8): a unit's workgroups share an
-  // L2, and items without work, which come at the end of each sequence, spread over the XCDs.
+  // L2, and items without work, which come at the end of each sequence, spread over the
+  // XCDs.  An XCD takes another group in each item: a row of B holds all groups, 256
+  // bytes each, so one group for an XCD would keep two of its L2's sixteen channels
+  // busy and the others idle (kernel of a prompt of 8192 tokens: XXX us).
   const int k8 = blockIdx.x / kXcds, u8 = fdiv(k8, plan.fnb);
   const int unit = u8 * kXcds + blockIdx.x % kXcds, blk = k8 - u8 * plan.nb;
   if (unit >= plan.units) return;
-  const int item = fdiv(unit, plan.fG), g = unit - item * a.G;
+  const int item = fdiv(unit, plan.fG), g = fmod_(unit + item, plan.fG);
   const int Hg = a.H / a.G, P = a.P, N = a.N;
 
   int seq, begin, len, t_first = 0, t_end;
@@ -251,18 +246,18 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   const int nh = min(plan.hw, Hg - blk * plan.hw);
   const int hw_ = wave / plan.wph;
   const bool active = hw_ < nh;                                // this wave has a tile of x columns
-  const int hi = active ? hw_ : 0, pt = active ? wave % plan.wph : 0;
+  const int hi = active ? hw_ : 0, pt0 = active ? wave % plan.wph * CT : 0;
+  const int np = min(CT, P / 16 - pt0);                        // a head's last wave may have a tile less
   const int h = h0 + hi;
-  const int xcol = hi * P + 16 * pt;
+  const int xcol = hi * P + 16 * pt0;
   const int ncols = nh * P;
   const float Al = uniform(a.A[h] * kLog2e), D = OUT ? uniform(a.D[h]) : 0.f;
-  float *const sc = reinterpret_cast<float *>(lds + Z::SC0);                               // [heads]{[5][Q], D}
-  mtile *const sM = reinterpret_cast<mtile *>(lds + Z::SC0 + plan.hw * Z::SC);             // [heads][TILES][64]
-  float *const my = sc + hi * (5 * Q + 4);
+  float *const my = reinterpret_cast<float *>(lds + Z::SC0) + hi * 6 * Q;  // the head's values a token
+  float4 *const sG = reinterpret_cast<float4 *>(lds + Z::G0) + lane;
 
-  // The state: S^T tile nt, rows n = 16 nt + 4 q + i, column p = r of the wave's tile.
-  floatx4 S[NT];
-  const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt + r) * N + 4 * q;
+  // The state: S^T tile nt, rows n = 16 nt + 4 q + i, column p = r of each of the wave's tiles.
+  floatx4 S[NT][CT];
+  const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt0 + r) * N + 4 * q;
   const size_t states = (size_t)a.H * P * N;
   bool split = false;
   if constexpr (MODE == kFrom) split = len > plan.seg;
@@ -270,13 +265,15 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   const float *from = nullptr;
   if constexpr (MODE != kOwn) from = split ? plan.state + item * states : known ? a.initial + row * states : nullptr;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    S[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if (from && 16 * nt < N) {
-      const float4 v = ld4(from + tile0 + 16 * nt);
-      S[nt] = floatx4{v.x, v.y, v.z, v.w};
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int pt = 0; pt < CT; ++pt) {
+      S[nt][pt] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (from && 16 * nt < N && pt < np) {
+        const float4 v = ld4(from + tile0 + (size_t)16 * pt * N + 16 * nt);
+        S[nt][pt] = floatx4{v.x, v.y, v.z, v.w};
+      }
     }
-  }
 
   // Global to registers through buffers that end with the chunk's last row: rows
   // past it read as zeros, and so do the columns of threads without a place.
@@ -291,7 +288,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   float dtv = 0.f;
   // Places in global memory and LDS are computed anew from the thread's number at each
   // use: a few operations, where 14 registers would otherwise push others into memory.
-  auto fetch = [&](int t0) {
+  auto fetch = [&](int t0, bool bc, bool x_) {
     const int id = again(tid);
     const int tB = id / NV, cB = id % NV * 8, tX = id / XV, cX = id % XV * 8;
     const int cC = 32 * (id % NV / 4) + 4 * (id % 4);  // C's granules go by operands
@@ -301,20 +298,25 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
     const int oC1 = NK > 1 || cC + 16 < N ? oC + 16 * (int)sizeof(R) : kNowhere;
     const int oX = cX < ncols ? (int)((tX * rX + cX) * sizeof(R)) : kNowhere;
     const int odt = id % kWave < Q ? id % kWave * a.H * 4 : kNowhere;
-    const int rem = min(Q, t_end - t0);
-    dtv = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        buffer_of(dtg + (size_t)t0 * a.H, ((rem - 1) * (size_t)a.H + 1) * 4), odt, 0, 0));
-    const auto bB = buffer_of(Bg + t0 * rB, ((rem - 1) * rB + N) * sizeof(R));
-    const auto bX = buffer_of(Xg + t0 * rX, ((rem - 1) * rX + ncols) * sizeof(R));
+    const int rem = min(Q, t_end - t0);  // none left: empty buffers, which read nothing
+    auto size = [&](size_t row, int last) { return rem > 0 ? ((rem - 1) * row + last) * sizeof(R) : 0; };
+    if (bc) {
+      dtv = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          buffer_of(dtg + (size_t)t0 * a.H, rem > 0 ? ((rem - 1) * (size_t)a.H + 1) * 4 : 0), odt, 0, 0));
+      const auto bB = buffer_of(Bg + t0 * rB, size(rB, N));
 #pragma unroll
-    for (int i = 0; i < LB; ++i) pB[i].load(bB, oB, (int)(i * RB * rB * sizeof(R)));
-    if constexpr (OUT) {
-      const auto bC = buffer_of(Cg + t0 * rB, ((rem - 1) * rB + N) * sizeof(R));
+      for (int i = 0; i < LB; ++i) pB[i].load(bB, oB, (int)(i * RB * rB * sizeof(R)));
+      if constexpr (OUT) {
+        const auto bC = buffer_of(Cg + t0 * rB, size(rB, N));
 #pragma unroll
-      for (int i = 0; i < LB; ++i) pC[i].load2(bC, oC, oC1, (int)(i * RB * rB * sizeof(R)));
+        for (int i = 0; i < LB; ++i) pC[i].load2(bC, oC, oC1, (int)(i * RB * rB * sizeof(R)));
+      }
     }
+    if (x_) {
+      const auto bX = buffer_of(Xg + t0 * rX, size(rX, ncols));
 #pragma unroll
-    for (int i = 0; i < LX; ++i) pX[i].load(bX, oX, (int)(i * RX * rX * sizeof(R)));
+      for (int i = 0; i < LX; ++i) pX[i].load(bX, oX, (int)(i * RX * rX * sizeof(R)));
+    }
   };
   auto spill = [&]() {
     const int id = again(tid);
@@ -355,16 +357,11 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
     return f;
   };
 
-  if (OUT && active && pt == 0 && lane == 0) my[5 * Q] = D;  // read after two barriers
   float decay = 1.f;
-  fetch(t_first);
+  fetch(t_first, true, true);
   for (int t0 = t_first; t0 < t_end; t0 += Q) {
-    lds_barrier();  // every wave is done with the last chunk's tiles
-    spill();
-    const float dt = dtv;
-    if constexpr (!OUT)
-      if (t0 + Q < t_end) fetch(t0 + Q);
     // Decays: lane = token.
+    const float dt = dtv;
     double sum = dt;
     float suf = dt;
     sum += row_shift<0x111>(sum), suf += row_shift<0x101>(suf);
@@ -372,223 +369,285 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
     sum += row_shift<0x114>(sum), suf += row_shift<0x104>(suf);
     sum += row_shift<0x118>(sum), suf += row_shift<0x108>(suf);
     suf = row_shift<0x101>(suf);  // the tokens after this one
-    sum *= Al;  // as an exponent of 2
-    const float pre = (float)sum;
-    const float epre = __builtin_amdgcn_exp2f(pre);
-    if (active && pt == 0 && lane < Q) {
-      my[lane] = pre;
-      my[Q + lane] = epre;
-      my[2 * Q + lane] = __builtin_amdgcn_exp2f(Al * suf) * dt;
-      if constexpr (OUT) {
-        my[3 * Q + lane] = dt;
-        my[4 * Q + lane] = (float)(sum - (double)pre);
-      }
-    }
+    sum *= Al;                    // as an exponent of 2
+    const float pre = (float)sum, epre = __builtin_amdgcn_exp2f(pre), edt = __builtin_amdgcn_exp2f(Al * suf) * dt;
     float E[QB];  // the blocks' decays
 #pragma unroll
     for (int b = 0; b < QB; ++b) E[b] = __uint_as_float(__builtin_amdgcn_readlane(bits(epre), 16 * b + 15));
+    float all = 1.f, after = 1.f;  // the chunk's decay, and from the end of the lane's block to the chunk's
+#pragma unroll
+    for (int b = QB - 1; b >= 0; --b) {
+      after = lane / 16 == b ? all : after;
+      all *= E[b];
+    }
+    decay *= all;
+
+    lds_barrier();  // every wave is done with the last chunk's tiles
+    spill();
+    if (active && pt0 == 0 && lane < Q) {
+      my[lane] = edt * after;
+      if constexpr (OUT) {
+        my[Q + lane] = epre;
+        my[2 * Q + lane] = pre;
+        my[3 * Q + lane] = (float)(sum - (double)pre);
+        my[4 * Q + lane] = dt;
+        my[5 * Q + lane] = edt;
+      }
+    }
     lds_barrier();
 
-    floatx4 Yt[QB];
-    if constexpr (OUT) {
-      const int la = again(lane), oR = la % 16 * RS + in_row(la % 16, la / 16 * 4);
-      const int oC = la % 16 * RS + in_row_c(la % 16, 0, la / 16);
-      // G^T tiles (rows j, columns t), and M^T from them for each of the workgroup's heads.
-      // A wave takes a tile, or a tile for one head where there are no more of those than waves.
-      const bool by_head = TILES * nh <= kWaves;
-      for (int i = wave; i < (by_head ? TILES * nh : TILES); i += kWaves) {
-        const int tile = by_head ? i % TILES : i;
-        // The dear diagonal tiles meet waves that get no second one.
-        const int tb = tile_row<QB>(tile), jb = tile_col<QB>(tile);
-        floatx4 acc{0.f, 0.f, 0.f, 0.f};
+    // All of this is independent of the other waves: their tiles of G^T (rows j,
+    // columns t), S0 C^T transposed (rows p, columns t), and the state after the chunk.
+    floatx4 Yt[QB][CT];
+    const int la = again(lane), lr = la % 16, lq = la / 16;
+    const int tr = 4 * lq + lr / 4, oT = tr * RS + in_row(tr, lr % 4 * 4);
+    Frag xf[KB][CT][IP], xw[KB][CT][3];
+    float4 w4[KB][2];
+    // The weighted inputs, in three pieces: step k, column tile pt.
+    auto weigh = [&](int k, int pt) {
+      const float w[8] = {w4[k][0].x, w4[k][0].y, w4[k][0].z, w4[k][0].w, w4[k][1].x, w4[k][1].y, w4[k][1].z, w4[k][1].w};
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          Frag bf[IP], cf[IP];
+      for (int i = 0; i < 4; ++i) {
+        const Frag(&x)[IP] = xf[k][pt];
+        float lo = lower(x[IP - 1].w[i]), up = upper(x[IP - 1].w[i]);
 #pragma unroll
-          for (int u = 0; u < IP; ++u) bf[u] = rows(Z::B0 + u * Q * RS, jb, k, oR), cf[u] = rows_c(Z::C0 + u * Q * RS, tb, k, oC);
+        for (int u = IP - 2; u >= 0; --u) lo += lower(x[u].w[i]), up += upper(x[u].w[i]);
+        uint32_t pw[3];
+        pieces<3>(lo * w[2 * i], up * w[2 * i + 1], pw);
 #pragma unroll
-          for (int u = IP - 1; u >= 0; --u)
-#pragma unroll
-            for (int v = IP - 1 - u; v >= 0; --v) acc = mfma32(bf[u], cf[v], acc);
-        }
-        for (int hd = by_head ? i / TILES : 0; hd < (by_head ? i / TILES + 1 : nh); ++hd) {
-          const float *s = sc + hd * (5 * Q + 4);
-          float m[4];
-          if (jb < tb) {
-            float f = s[Q + 16 * tb + r];  // t's block up to t, and the whole blocks between
-            for (int b = jb + 1; b < tb; ++b) f *= s[Q + 16 * b + 15];
-            const float4 w = ld4(s + 2 * Q + 16 * jb + 4 * q);
-            m[0] = acc[0] * (f * w.x), m[1] = acc[1] * (f * w.y), m[2] = acc[2] * (f * w.z), m[3] = acc[3] * (f * w.w);
-          } else {
-            const float p1 = s[16 * tb + r], l1 = s[4 * Q + 16 * tb + r];
-            const float4 p4 = ld4(s + 16 * jb + 4 * q), d4 = ld4(s + 3 * Q + 16 * jb + 4 * q), l4 = ld4(s + 4 * Q + 16 * jb + 4 * q);
-            const float pj[4] = {p4.x, p4.y, p4.z, p4.w}, dj[4] = {d4.x, d4.y, d4.z, d4.w};
-            const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float v = acc[e] * (__builtin_amdgcn_exp2f((p1 - pj[e]) + (l1 - lj[e])) * dj[e]);
-              m[e] = 4 * q + e < r ? v : 4 * q + e == r ? v + s[5 * Q] : 0.f;  // D x_t rides along
-            }
-          }
-          mtile *to = sM + (hd * MT + tb * (tb + 1) / 2 + jb) * kWave + lane;
-          if constexpr (MP == 1) {
-            const uint2 w = make_uint2(pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3]));
-            *to = w;
-            if (jb == tb) {
-              sM[(hd * MT + TILES + tb) * kWave + lane] = make_uint2(pack_bf16(m[0] - lower(w.x), m[1] - upper(w.x)),
-                                                                     pack_bf16(m[2] - lower(w.y), m[3] - upper(w.y)));
-            }
-          } else {
-            *to = make_float4(m[0], m[1], m[2], m[3]);
-          }
-        }
+        for (int u = 0; u < 3; ++u) xw[k][pt][u].w[i] = pw[u];
       }
-      // S0 C^T, transposed: rows p, columns t.
+    };
+    auto load_x = [&]() {
 #pragma unroll
-      for (int tb = 0; tb < QB; ++tb) Yt[tb] = floatx4{0.f, 0.f, 0.f, 0.f};
-      if (active) {
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          Frag sp[MP];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const floatx4 &s = S[2 * k + i / 2];
-            uint32_t w[MP];
-            pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
-#pragma unroll
-            for (int u = 0; u < MP; ++u) sp[u].w[i] = w[u];
-          }
-#pragma unroll
-          for (int v = 0; v < IP; ++v) {
-            Frag cf[QB];
-#pragma unroll
-            for (int tb = 0; tb < QB; ++tb) cf[tb] = rows_c(Z::C0 + v * Q * RS, tb, k, oC);
-#pragma unroll
-            for (int u = MP - 1; u >= 0; --u)
-              if (u + v < 3) {
-#pragma unroll
-                for (int tb = 0; tb < QB; ++tb) Yt[tb] = mfma32(sp[u], cf[tb], Yt[tb]);
-              }
-          }
-        }
-        float f = 1.f;
-#pragma unroll
-        for (int tb = 0; tb < QB; ++tb) {
-          Yt[tb] *= f * my[Q + 16 * tb + r];
-          f *= E[tb];
-        }
-      }
-      lds_barrier();  // M is complete
-      if (t0 + Q < t_end) fetch(t0 + Q);  // here: the registers are free from now on
-    }
-
-    if (active) {
-      const int la = again(lane), tr = la / 16 * 4 + la % 16 / 4;
-      const int oT = tr * RS + in_row(tr, la % 4 * 4), oTx = tr * XS + in_row(tr, xcol + la % 4 * 4);
-      Frag xf[KB][IP];
-#pragma unroll
-      for (int k = 0; k < KB; ++k)
-#pragma unroll
-        for (int u = 0; u < IP; ++u) {
-          const char *p = lds + Z::X0 + u * Q * XS + 32 * k * XS + oTx;
-          xf[k][u].h[0] = read_tr(p);
-          xf[k][u].h[1] = read_tr(p + 16 * XS);
-        }
-      if constexpr (OUT) {
-        const mtile *mt = sM + hi * MT * kWave + lane;
+      for (int pt = 0; pt < CT; ++pt) {
+        const char *p = lds + Z::X0 + tr * XS + in_row(tr, xcol + (pt < np ? 16 * pt : 0) + lr % 4 * 4);
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int tb = 2 * k; tb < QB; ++tb) {
-            Frag mf[MP];
+          for (int u = 0; u < IP; ++u) {
+            xf[k][pt][u].h[0] = read_tr(p + (u * Q + 32 * k) * XS);
+            xf[k][pt][u].h[1] = read_tr(p + (u * Q + 32 * k + 16) * XS);
+          }
+      }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int jb = 2 * k + half;
-              if (jb > tb) {
+      for (int k = 0; k < KB; ++k) w4[k][0] = ld4(my + 32 * k + 4 * lq), w4[k][1] = ld4(my + 32 * k + 16 + 4 * lq);
+    };
+
+    if constexpr (OUT) {
+      const int oR = lr * RS + in_row(lr, 4 * lq), oC = lr * RS + in_row_c(lr, 0, lq);
+      constexpr int GT = (TILES + kWaves - 1) / kWaves;  // a wave's tiles; the last ones are computed twice over
+      Frag gb[GT][NK], gc[GT][NK];                       // the pieces v of both, one at a time
+      floatx4 acc[GT];
+      auto tile_of = [&](int g) { return min(g * kWaves + wave, TILES - 1); };
 #pragma unroll
-                for (int u = 0; u < MP; ++u) mf[u].h[half] = s16x4{0, 0, 0, 0};
-                continue;
-              }
-              const mtile m = mt[(tb * (tb + 1) / 2 + jb) * kWave];
-              if constexpr (MP == 1) {
-                mf[0].w[2 * half] = m.x, mf[0].w[2 * half + 1] = m.y;
-              } else {
-                uint32_t w0[MP], w1[MP];
-                pieces<MP>(m.x, m.y, w0);
-                pieces<MP>(m.z, m.w, w1);
+      for (int g = 0; g < GT; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
+      auto load_g = [&](int g, int u, int v) {
+        const int i = tile_of(g), tb = tile_row(i), jb = tile_col(i);
 #pragma unroll
-                for (int u = 0; u < MP; ++u) mf[u].w[2 * half] = w0[u], mf[u].w[2 * half + 1] = w1[u];
+        for (int k = 0; k < NK; ++k) {
+          gb[g][k] = rows(Z::B0 + u * Q * RS, jb, k, oR);
+          gc[g][k] = rows_c(Z::C0 + v * Q * RS, tb, k, oC);
+        }
+      };
+#pragma unroll
+      for (int u = IP - 1; u >= 0; --u)
+#pragma unroll
+        for (int v = IP - 1 - u; v >= 0; --v) {
+#pragma unroll
+          for (int g = 0; g < GT; ++g) load_g(g, u, v);
+          if (u == 0 && v == 0) load_x();
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int g = 0; g < GT; ++g) acc[g] = mfma32(gb[g][k], gc[g][k], acc[g]);
+        }
+      Frag sp[NK][CT][MP];
+      auto cut_state = [&](int k) {
+#pragma unroll
+        for (int pt = 0; pt < CT; ++pt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const floatx4 &s = S[2 * k + i / 2][pt];
+            uint32_t w[MP];
+            pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
+#pragma unroll
+            for (int u = 0; u < MP; ++u) sp[k][pt][u].w[i] = w[u];
+          }
+      };
+      Frag cf[2][QB];
+      auto load_c = [&](int at) {  // at: step k and piece v as k IP + v
+#pragma unroll
+        for (int tb = 0; tb < QB; ++tb) cf[at % 2][tb] = rows_c(Z::C0 + at % IP * Q * RS, tb, at / IP, oC);
+      };
+      load_c(0);
+      cut_state(0);
+#pragma unroll
+      for (int g = 0; g < GT; ++g) sG[tile_of(g) * kWave] = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+#pragma unroll
+      for (int tb = 0; tb < QB; ++tb)
+#pragma unroll
+        for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int at = 0; at < NK * IP; ++at) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int k = at / IP, v = at % IP;
+        if (at + 1 < NK * IP) load_c(at + 1);
+        if (v == IP - 1 && k + 1 < NK) cut_state(k + 1);
+        if (at < KB * CT) weigh(at / CT, at % CT);
+#pragma unroll
+        for (int u = MP - 1; u >= 0; --u)
+          if (u + v < 3) {
+#pragma unroll
+            for (int tb = 0; tb < QB; ++tb)
+#pragma unroll
+              for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(sp[k][pt][u], cf[at % 2][tb], Yt[tb][pt]);
+          }
+        interleave<QB * CT * (MP == 1 ? 1 : IP == 1 ? 3 : 2), MP == 1 ? 8 : 4>();
+      }
+#pragma unroll
+      for (int i = NK * IP; i < KB * CT; ++i) weigh(i / CT, i % CT);
+    } else {
+      load_x();
+#pragma unroll
+      for (int i = 0; i < KB * CT; ++i) weigh(i / CT, i % CT);
+    }
+    {
+      // Steps of two state tiles and one piece of B, their operands read one step ahead.
+      constexpr int STEPS = KB * NK * IP;
+      Frag bf[2][2];
+      auto load_b = [&](int at) {
+        const int k = at / (NK * IP), n0 = at / IP % NK * 2, v = at % IP;
+        bf[at % 2][0] = cols(Z::B0 + v * Q * RS, n0, k, oT);
+        bf[at % 2][1] = cols(Z::B0 + v * Q * RS, n0 + 1, k, oT);
+      };
+      load_b(0);
+#pragma unroll
+      for (int at = 0; at < STEPS; ++at) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int k = at / (NK * IP), n0 = at / IP % NK * 2, v = at % IP;
+        if (at + 1 < STEPS) load_b(at + 1);
+        if (k == 0 && v == 0) {
+#pragma unroll
+          for (int pt = 0; pt < CT; ++pt) S[n0][pt] *= all, S[n0 + 1][pt] *= all;
+        }
+#pragma unroll
+        for (int u = 2; u >= 0; --u)
+          if (u + v < 3) {
+#pragma unroll
+            for (int pt = 0; pt < CT; ++pt) {
+              S[n0][pt] = mfma32(bf[at % 2][0], xw[k][pt][u], S[n0][pt]);
+              S[n0 + 1][pt] = mfma32(bf[at % 2][1], xw[k][pt][u], S[n0 + 1][pt]);
+            }
+          }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    fetch(t0 + Q, true, !OUT);
+
+    if constexpr (OUT) {
+      // What M needs of block tb: the values of this lane's token in it, and of its own four tokens.
+      float et[2], p1[2], l1[2];
+      float4 g4[2][QB];
+      auto load_t = [&](int tb) {
+        et[tb % 2] = my[Q + 16 * tb + lr];
+        p1[tb % 2] = my[2 * Q + 16 * tb + lr], l1[tb % 2] = my[3 * Q + 16 * tb + lr];
+      };
+      auto load_gt = [&](int tb) {
+#pragma unroll
+        for (int jb = 0; jb <= tb; ++jb) g4[tb % 2][jb] = sG[(tb * (tb + 1) / 2 + jb) * kWave];
+      };
+      load_t(0);
+      lds_barrier();  // G is complete
+      load_gt(0);
+      float f = 1.f;
+#pragma unroll
+      for (int tb = 0; tb < QB; ++tb) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (tb == QB / 2) fetch(t0 + Q, false, true);
+        if (tb + 1 < QB) load_t(tb + 1), load_gt(tb + 1);
+        const int c = tb % 2;
+        const float4 p4 = ld4(my + 2 * Q + 16 * tb + 4 * lq), l4 = ld4(my + 3 * Q + 16 * tb + 4 * lq);
+        const float4 d4 = ld4(my + 4 * Q + 16 * tb + 4 * lq);
+        const float e = f * et[c];
+#pragma unroll
+        for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] *= e;
+        f *= E[tb];
+        // M^T from G^T, and x M^T.
+#pragma unroll
+        for (int k = 0; k <= tb / 2; ++k) {
+          Frag mf[MP], left;  // left: what rounding leaves of the diagonal tile
+          left.v = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int jb = 2 * k + half;
+            if (jb > tb) {
+#pragma unroll
+              for (int u = 0; u < MP; ++u) mf[u].h[half] = s16x4{0, 0, 0, 0};
+              continue;
+            }
+            const float4 gt = g4[c][jb];
+            float m[4];
+            if (jb < tb) {
+              float g = et[c];  // t's block up to t, and the whole blocks between
+#pragma unroll
+              for (int b = 0; b < QB; ++b)
+                if (b > jb && b < tb) g *= E[b];
+              const float4 wj = ld4(my + 5 * Q + 16 * jb + 4 * lq);
+              m[0] = gt.x * (g * wj.x), m[1] = gt.y * (g * wj.y), m[2] = gt.z * (g * wj.z), m[3] = gt.w * (g * wj.w);
+            } else {
+              const float gj[4] = {gt.x, gt.y, gt.z, gt.w}, pj[4] = {p4.x, p4.y, p4.z, p4.w};
+              const float lj[4] = {l4.x, l4.y, l4.z, l4.w}, dj[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = 4 * lq + i;
+                const float v = gj[i] * (__builtin_amdgcn_exp2f((p1[c] - pj[i]) + (l1[c] - lj[i])) * dj[i]);
+                m[i] = j < lr ? v : j == lr ? v + D : 0.f;  // D x_t rides along
               }
             }
 #pragma unroll
-            for (int u = MP - 1; u >= 0; --u)
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w[MP];
+              pieces<MP>(m[2 * i], m[2 * i + 1], w);
 #pragma unroll
-              for (int v = 0; v < IP; ++v)
-                if (u + v < 3) Yt[tb] = mfma32(xf[k][v], mf[u], Yt[tb]);
-            if constexpr (MP == 1)
-              if (tb / 2 == k) {
-                const mtile m = mt[(TILES + tb) * kWave];
-                Frag lf;
-                lf.h[1 - tb % 2] = s16x4{0, 0, 0, 0};
-                lf.w[tb % 2 * 2] = m.x, lf.w[tb % 2 * 2 + 1] = m.y;
-                Yt[tb] = mfma32(xf[k][0], lf, Yt[tb]);
-              }
+              for (int u = 0; u < MP; ++u) mf[u].w[2 * half + i] = w[u];
+              if (MP == 1 && jb == tb) left.w[2 * half + i] = pack_bf16(m[2 * i] - lower(w[0]), m[2 * i + 1] - upper(w[0]));
+            }
           }
-        // y: this lane holds four neighbouring channels of token 16 tb + r.
-        const int rem = min(Q, t_end - t0);
-        const auto bY = buffer_of((Y *)a.y + (size_t)(begin + t0) * rX + (size_t)h * P + 16 * pt,
-                                  ((rem - 1) * rX + 16) * sizeof(Y));  // rows past the end are not written
-        const int oY = (int)((r * rX + 4 * q) * sizeof(Y));
 #pragma unroll
-        for (int tb = 0; tb < QB; ++tb) {
-          const floatx4 o = Yt[tb];
-          const int step = (int)(16 * tb * rX * sizeof(Y));
-          if constexpr (sizeof(Y) == 2)
-            __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, oY, step, 0);
-          else  // step in the vector offset: a 16-byte store with a scalar offset may send the registers'
-                // next values if an instruction rewrites them right behind it (seen: the last lanes of a row)
-            __builtin_amdgcn_raw_buffer_store_b128(
-                i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, oY + step, 0, 0);
+          for (int u = MP - 1; u >= 0; --u)
+#pragma unroll
+            for (int v = 0; v < IP; ++v)
+              if (u + v < 3) {
+#pragma unroll
+                for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(xf[k][pt][v], mf[u], Yt[tb][pt]);
+              }
+          if (MP == 1 && tb / 2 == k) {
+#pragma unroll
+            for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(xf[k][pt][0], left, Yt[tb][pt]);
+          }
         }
       }
-      // The state after the chunk.
-      float all = 1.f;
+      // y: this lane holds four neighbouring channels of token 16 tb + r.
+      if (active) {
+        const int rem = min(Q, t_end - t0);
+        const auto bY = buffer_of((Y *)a.y + (size_t)(begin + t0) * rX + (size_t)h * P + 16 * pt0,
+                                  ((rem - 1) * rX + 16 * np) * sizeof(Y));  // rows past the end are not written
+        const int oY = (int)((lr * rX + 4 * lq) * sizeof(Y));
 #pragma unroll
-      for (int b = 0; b < QB; ++b) all *= E[b];
-      decay *= all;
+        for (int tb = 0; tb < QB; ++tb)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[nt] *= all;
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        float f1 = 1.f;
-#pragma unroll
-        for (int b = 0; b < QB; ++b)
-          if (b > 2 * k + 1) f1 *= E[b];
-        const float f0 = f1 * E[2 * k + 1];
-        const float4 w0 = ld4(my + 2 * Q + 32 * k + 4 * q), w1 = ld4(my + 2 * Q + 32 * k + 16 + 4 * q);
-        const float w[8] = {f0 * w0.x, f0 * w0.y, f0 * w0.z, f0 * w0.w, f1 * w1.x, f1 * w1.y, f1 * w1.z, f1 * w1.w};
-        Frag xw[3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float lo = lower(xf[k][IP - 1].w[i]), up = upper(xf[k][IP - 1].w[i]);
-#pragma unroll
-          for (int u = IP - 2; u >= 0; --u) lo += lower(xf[k][u].w[i]), up += upper(xf[k][u].w[i]);
-          uint32_t pw[3];
-          pieces<3>(lo * w[2 * i], up * w[2 * i + 1], pw);
-#pragma unroll
-          for (int u = 0; u < 3; ++u) xw[u].w[i] = pw[u];
-        }
-#pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += 2)  // two accumulators in turn
-#pragma unroll
-          for (int v = 0; v < IP; ++v) {
-            const Frag b0 = cols(Z::B0 + v * Q * RS, n0, k, oT), b1 = cols(Z::B0 + v * Q * RS, n0 + 1, k, oT);
-#pragma unroll
-            for (int u = 2; u >= 0; --u)
-              if (u + v < 3) {
-                S[n0] = mfma32(b0, xw[u], S[n0]);
-                S[n0 + 1] = mfma32(b1, xw[u], S[n0 + 1]);
-              }
+          for (int pt = 0; pt < CT; ++pt) {
+            if (pt >= np) continue;
+            const floatx4 o = Yt[tb][pt];
+            const int step = (int)(16 * tb * rX * sizeof(Y)), at = oY + 16 * pt * (int)sizeof(Y);
+            if constexpr (sizeof(Y) == 2)
+              __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, at, step, 0);
+            else  // step in the vector offset: a 16-byte store with a scalar offset may send the registers'
+                  // next values if an instruction rewrites them right behind it (seen: the last lanes of a row)
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, at + step, 0, 0);
           }
       }
     }
@@ -598,9 +657,12 @@ __global__ __launch_bounds__(kThreads, 4) void scan_k(ScanArgs a, ScanPlan plan)
   if (to && active) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      if (16 * nt < N) st4(to + tile0 + 16 * nt, make_float4(S[nt][0], S[nt][1], S[nt][2], S[nt][3]));
+#pragma unroll
+      for (int pt = 0; pt < CT; ++pt)
+        if (16 * nt < N && pt < np)
+          st4(to + tile0 + (size_t)16 * pt * N + 16 * nt, make_float4(S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]));
   }
-  if (MODE == kOwn && active && pt == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
+  if (MODE == kOwn && active && pt0 == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
 }
 
 // Where each segment of a split sequence starts: the segment before it decays
@@ -628,7 +690,7 @@ __global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan,
 ScanPlan make_plan(const ScanArgs &a) {
   ScanPlan p{};
   const int Hg = a.H / a.G;
-  p.wph = a.P / 16;
+  p.wph = (a.P / 16 + CT - 1) / CT;
   p.hw = kWaves / p.wph < kHeads ? kWaves / p.wph : kHeads;
   if (p.hw > Hg) p.hw = Hg;
   p.nb = (Hg + p.hw - 1) / p.hw;
@@ -649,9 +711,7 @@ size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.ite
 
 template <typename R, typename Y, int NK, int MODE>
 void launch_part(const ScanArgs &a, const ScanPlan &p, dim3 grid, hipStream_t st) {
-  constexpr int most = 160 * 1024;
-  static_assert(Shape_<R, Y, NK, MODE>::lds(kHeads) <= most, "LDS of a workgroup");
-  hipLaunchKernelGGL((scan_k<R, Y, NK, MODE>), grid, dim3(kThreads), (Shape_<R, Y, NK, MODE>::lds(p.hw)), st, a, p);
+  hipLaunchKernelGGL((scan_k<R, Y, NK, MODE>), grid, dim3(kThreads), (Shape_<R, Y, NK, MODE>::LDS), st, a, p);
 }
 
 template <typename R, typename Y, int NK>
