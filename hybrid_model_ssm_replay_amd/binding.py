@@ -119,16 +119,15 @@ _SIG = {
     "replay_snapshot_verify": (ctypes.c_int, [ctypes.POINTER(replay_config), _P, _P, ctypes.c_int32, _P, _P,
                                               ctypes.POINTER(replay_record), _P, _P]),
     "replay_snapshot_commit": (ctypes.c_int, [ctypes.POINTER(replay_config), _P, _P, ctypes.c_int32, _P]),
-    "replay_short_conv_step": (ctypes.c_int, [ctypes.POINTER(replay_short_conv), _P, ctypes.c_int64, ctypes.c_int64,
-                                              ctypes.c_int32, _P, _P, _P, _P]),
-    "replay_short_conv_prompt": (ctypes.c_int, [ctypes.POINTER(replay_short_conv), ctypes.POINTER(replay_prompt), _P,
-                                                ctypes.c_int64, _P, _P, _P, _P]),
-    "replay_scan_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(replay_config), ctypes.c_int32, ctypes.c_int32]),
-    "replay_scan_prompt": (ctypes.c_int, [ctypes.POINTER(replay_config), ctypes.POINTER(replay_prompt),
-                                          ctypes.POINTER(replay_record), _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
-    "replay_gated_norm": (ctypes.c_int, [ctypes.POINTER(replay_gated_norm_args), _P]),
+    # The operators around the recurrence take their structs by address: a ctypes
+    # structure, or the same bytes packed (a third of the time to make).
+    "replay_short_conv_step": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P]),
+    "replay_short_conv_prompt": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P]),
+    "replay_scan_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
+    "replay_scan_prompt": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
+    "replay_gated_norm": (ctypes.c_int, [_P, _P]),
     "replay_accept_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
-    "replay_accept_drafts": (ctypes.c_int, [ctypes.POINTER(replay_accept_args), _P, _P]),
+    "replay_accept_drafts": (ctypes.c_int, [_P, _P, _P]),
     "replay_hbm_probe": (ctypes.c_int, [_P, _P, ctypes.c_size_t, ctypes.c_int, _P]),
 }
 EXPORTS = tuple(_SIG)
@@ -270,40 +269,46 @@ def replay_hbm_probe(src: int, dst: int, nbytes: int, mode: int, stream: int) ->
     _check("replay_hbm_probe", load_library().replay_hbm_probe(src, dst, nbytes, mode, stream or None))
 
 
-def replay_short_conv_step(conv: replay_short_conv, x: int, seq_stride: int, row_stride: int, T: int, outs,
-                           stream: int) -> None:
-    _check("replay_short_conv_step",
-           load_library().replay_short_conv_step(ctypes.byref(conv), x or None, seq_stride, row_stride, T,
-                                                 *[o or None for o in outs], stream or None))
+def _by_address(st):
+    return st if isinstance(st, bytes) else ctypes.byref(st)
 
 
-def replay_short_conv_prompt(conv: replay_short_conv, prompt: replay_prompt, x: int, row_stride: int, outs,
-                             stream: int) -> None:
-    _check("replay_short_conv_prompt",
-           load_library().replay_short_conv_prompt(ctypes.byref(conv), ctypes.byref(prompt), x or None, row_stride,
-                                                   *[o or None for o in outs], stream or None))
+def replay_short_conv_step(conv, x: int, seq_stride: int, row_stride: int, T: int, outs, stream: int) -> None:
+    rc = (_lib or load_library()).replay_short_conv_step(_by_address(conv), x, seq_stride, row_stride, T, *outs, stream)
+    if rc:
+        _check("replay_short_conv_step", rc)
+
+
+def replay_short_conv_prompt(conv, prompt, x: int, row_stride: int, outs, stream: int) -> None:
+    rc = (_lib or load_library()).replay_short_conv_prompt(_by_address(conv), _by_address(prompt), x, row_stride, *outs,
+                                                           stream)
+    if rc:
+        _check("replay_short_conv_prompt", rc)
 
 
 def replay_scan_workspace_bytes(cfg, tokens: int, sequences: int) -> int:
-    return load_library().replay_scan_workspace_bytes(ctypes.byref(cfg), tokens, sequences)
+    return (_lib or load_library()).replay_scan_workspace_bytes(_by_address(cfg), tokens, sequences)
 
 
-def replay_scan_prompt(cfg, prompt: replay_prompt, rec: replay_record, A: int, D: int, initial: int, state: int, y: int,
-                       y_dtype: int, workspace: int, stream: int) -> None:
-    _check("replay_scan_prompt",
-           load_library().replay_scan_prompt(ctypes.byref(cfg), ctypes.byref(prompt), ctypes.byref(rec), A or None,
-                                             D or None, initial or None, state or None, y or None, y_dtype,
-                                             workspace or None, stream or None))
+def replay_scan_prompt(cfg, prompt, rec, A: int, D: int, initial: int, state: int, y: int, y_dtype: int, workspace: int,
+                       stream: int) -> None:
+    rc = (_lib or load_library()).replay_scan_prompt(_by_address(cfg), _by_address(prompt), _by_address(rec), A, D,
+                                                     initial, state, y, y_dtype, workspace, stream)
+    if rc:
+        _check("replay_scan_prompt", rc)
 
 
-def replay_gated_norm(args: replay_gated_norm_args, stream: int) -> None:
-    _check("replay_gated_norm", load_library().replay_gated_norm(ctypes.byref(args), stream or None))
+def replay_gated_norm(args, stream: int) -> None:
+    rc = (_lib or load_library()).replay_gated_norm(_by_address(args), stream)
+    if rc:
+        _check("replay_gated_norm", rc)
 
 
 def replay_accept_workspace_bytes(batch: int, vocab: int) -> int:
-    return load_library().replay_accept_workspace_bytes(batch, vocab)
+    return (_lib or load_library()).replay_accept_workspace_bytes(batch, vocab)
 
 
-def replay_accept_drafts(args: replay_accept_args, workspace: int, stream: int) -> None:
-    _check("replay_accept_drafts", load_library().replay_accept_drafts(ctypes.byref(args), workspace or None,
-                                                                       stream or None))
+def replay_accept_drafts(args, workspace: int, stream: int) -> None:
+    rc = (_lib or load_library()).replay_accept_drafts(_by_address(args), workspace, stream)
+    if rc:
+        _check("replay_accept_drafts", rc)

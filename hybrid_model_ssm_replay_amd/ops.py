@@ -10,85 +10,97 @@ kernels.  See include/replayssm.h for the definitions.
   the decode step continues from.
 * ``gated_norm``: the gated group norm behind the recurrence.
 * ``accept_drafts``: how many drafts to commit, and the token after them.
+
+The kernels of a decode step take a few microseconds, so what Python adds to a
+call counts: the checks are plain comparisons, and only a tensor that fails one
+is looked at again to say what is wrong with it.
 """
 from __future__ import annotations
+
+import struct
 
 import torch
 
 from . import binding as B
 
 _DT = {torch.float32: B.DT_F32, torch.bfloat16: B.DT_BF16}
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+# The library's structs as bytes, in the order of their fields (native alignment).
+_PROMPT = struct.Struct("@2i4P").pack
+_CONV = struct.Struct("@10i5P").pack
+_NORM = struct.Struct("@8ifi3q4P").pack
+_ACCEPT = struct.Struct("@6i4q7P").pack
+_CONFIG = struct.Struct("@10iQ2I").pack
+_RECORD = struct.Struct("@5P").pack
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
 
 
-def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _on_gpu(t, name, dtypes, shape=None, contiguous=True) -> torch.Tensor:
-    """t, if it is a device tensor of one of dtypes and of shape (None: any extent)."""
+def _refuse(t, name, dtypes, shape, dense=True):
+    """Raise what keeps t from being a device tensor of one of dtypes and of shape (None: any extent)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a device tensor of {' or '.join(str(d) for d in dtypes)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape))):
+    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
-    return t
+    raise ValueError(f"{name} must be contiguous" if dense else f"{name} must be dense along its last axis")
 
 
-def _rows_apart(t, name) -> None:
-    """The last axis is dense; the others may have any (non-negative) stride."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be dense along its last axis")
+def _check(t, name, dtype, shape, at):
+    """t is a contiguous tensor of dtype and shape on device `at`; its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == at:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != at:
+        raise ValueError(f"tensors are on several devices: {name} is on {t.device}")
+    _refuse(t, name, (dtype,), shape)
 
 
-def _same_device(*tensors) -> None:
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors are on several devices: {sorted(map(str, devices))}")
+def _vectors(t, name, dims):
+    """The first tensor of a call: float32 or bfloat16, dims axes, dense along the last; its device index."""
+    if (not isinstance(t, torch.Tensor) or t.dtype not in _DT or not t.is_cuda or t.dim() != dims
+            or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+        _refuse(t, name, tuple(_DT), (None,) * dims, False)
+    return t.get_device()
 
 
-def _ptr(t) -> int:
-    return t.data_ptr() if t is not None else 0
-
-
-def _prompt(tokens, seq_start, rows, resume, status) -> B.replay_prompt:
-    _on_gpu(seq_start, "seq_start", (torch.int32,), (None,))
+def _prompt(tokens, seq_start, rows, resume, status, at) -> tuple[bytes, int]:
+    if not isinstance(seq_start, torch.Tensor) or seq_start.dim() != 1 or seq_start.shape[0] < 2:
+        raise ValueError("seq_start must be int32 [sequences + 1], on the device")
     n = seq_start.shape[0] - 1
-    if n < 1:
-        raise ValueError("seq_start needs one entry more than there are sequences")
-    if rows is not None:
-        _on_gpu(rows, "rows", (torch.int32,), (n,))
+    start = _check(seq_start, "seq_start", _I32, (n + 1,), at)
     if resume is not None:
-        _on_gpu(resume, "resume", (torch.uint8, torch.bool), (n,))
-    if status is not None:
-        _on_gpu(status, "status", (torch.int32,))
-    return B.replay_prompt(tokens, n, seq_start.data_ptr(), _ptr(rows), _ptr(resume), _ptr(status))
+        resume = _check(resume, "resume", torch.bool if resume.dtype is torch.bool else torch.uint8, (n,), at)
+    return _PROMPT(tokens, n, start, _check(rows, "rows", _I32, (n,), at) if rows is not None else 0, resume or 0,
+                   _status(status, at)), n
 
 
-def _short_conv(x, weight, ring, pos, widths, bias, activation, status):
-    _on_gpu(x, "x", tuple(_DT), contiguous=False)
-    _rows_apart(x, "x")
+def _status(status, at) -> int:
+    return 0 if status is None else _check(status, "status", _I32, tuple(status.shape), at)
+
+
+def _short_conv(x, weight, ring, pos, widths, bias, activation, status, dims):
+    at = _vectors(x, "x", dims)
     C = x.shape[-1]
-    widths = tuple(int(w) for w in widths)
-    if not 1 <= len(widths) <= 3 or sum(widths) != C or min(widths) < 0:
-        raise ValueError(f"widths {widths} must be one to three extents that add up to {C} channels")
-    _on_gpu(weight, "weight", (torch.float32,), (C, None))
-    _on_gpu(ring, "ring", (x.dtype,), (None, None, C))
-    if bias is not None:
-        _on_gpu(bias, "bias", (torch.float32,), (C,))
-    if pos is not None:
-        _on_gpu(pos, "pos", (torch.int32,), (ring.shape[1],))
-    if status is not None:
-        _on_gpu(status, "status", (torch.int32,))
+    w3 = (*widths, 0, 0)[:3]
+    if not 1 <= len(widths) <= 3 or sum(w3) != C or min(w3) < 0:
+        raise ValueError(f"widths {tuple(widths)} must be one to three extents that add up to {C} channels")
     if activation not in ("silu", None):
         raise ValueError(f"unknown activation {activation!r}")
-    _same_device(x, weight, ring, bias, pos, status)
-    w3 = widths + (0,) * (3 - len(widths))
-    conv = B.replay_short_conv(C, weight.shape[1], ring.shape[0], ring.shape[1], _DT[x.dtype],
-                               1 if activation == "silu" else 0, w3, 0, weight.data_ptr(), _ptr(bias),
-                               ring.data_ptr(), _ptr(pos), _ptr(status))
-    outs = [torch.empty(x.shape[:-1] + (w,), dtype=x.dtype, device=x.device) for w in widths]
-    return conv, outs
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be float32 [channels, taps], on the device")
+    if not isinstance(ring, torch.Tensor) or ring.dim() != 3:
+        raise ValueError("ring must be [slots, batch, channels], on the device")
+    taps = weight.shape[1]
+    slots, batch, _ = ring.shape
+    conv = _CONV(C, taps, slots, batch, _DT[x.dtype], 1 if activation else 0, *w3, 0,
+                 _check(weight, "weight", _F32, (C, taps), at),
+                 0 if bias is None else _check(bias, "bias", _F32, (C,), at),
+                 _check(ring, "ring", x.dtype, (slots, batch, C), at),
+                 0 if pos is None else _check(pos, "pos", _I32, (batch,), at), _status(status, at))
+    lead = x.shape[:-1]
+    outs = [torch.empty((*lead, w), dtype=x.dtype, device=x.device) for w in widths]
+    return at, conv, batch, outs, ([o.data_ptr() for o in outs] + [0, 0])[:3]
 
 
 def short_conv_step(x, weight, ring, pos, widths, *, bias=None, activation="silu", status=None):
@@ -101,13 +113,10 @@ def short_conv_step(x, weight, ring, pos, widths, *, bias=None, activation="silu
     widths: how the channels are split into outputs.  Returns one contiguous
     [batch, T, width] tensor for each width.  Rejected drafts need no restore:
     the next call at the smaller pos writes over them."""
-    if isinstance(x, torch.Tensor) and x.dim() != 3:
-        raise ValueError("x must be [batch, T, channels]")
-    conv, outs = _short_conv(x, weight, ring, pos, widths, bias, activation, status)
-    if pos is None or x.shape[0] != ring.shape[1]:
-        raise ValueError(f"x has {x.shape[0]} rows, ring {ring.shape[1]}, and pos is needed")
-    B.replay_short_conv_step(conv, x.data_ptr(), x.stride(0), x.stride(1), x.shape[1],
-                             [_ptr(o) for o in outs] + [0] * (3 - len(outs)), _stream(x))
+    at, conv, batch, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 3)
+    if pos is None or x.shape[0] != batch:
+        raise ValueError(f"x has {x.shape[0]} rows, ring {batch}, and pos is needed")
+    B.replay_short_conv_step(conv, x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], to, _raw_stream(at))
     return outs
 
 
@@ -121,13 +130,9 @@ def short_conv_prompt(x, weight, ring, seq_start, widths, *, bias=None, activati
     history (None: no sequence does); pos as for a step (None: 0).  The ring's rows
     are left so that a step at pos continues the sequence.  Returns one contiguous
     [tokens, width] tensor for each width."""
-    if isinstance(x, torch.Tensor) and x.dim() != 2:
-        raise ValueError("x must be [tokens, channels]")
-    conv, outs = _short_conv(x, weight, ring, pos, widths, bias, activation, status)
-    prompt = _prompt(x.shape[0], seq_start, rows, resume, status)
-    _same_device(x, seq_start, rows, resume)
-    B.replay_short_conv_prompt(conv, prompt, x.data_ptr(), x.stride(0), [_ptr(o) for o in outs] + [0] * (3 - len(outs)),
-                               _stream(x))
+    at, conv, _, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 2)
+    prompt, _ = _prompt(x.shape[0], seq_start, rows, resume, status, at)
+    B.replay_short_conv_prompt(conv, prompt, x.data_ptr(), x.stride(0), to, _raw_stream(at))
     return outs
 
 
@@ -142,32 +147,31 @@ def scan_prompt(x, Bm, Cm, dt, A, D, seq_start, state, *, initial=None, rows=Non
     initial (same shape, may be ``state`` itself): where sequences start, all of
     them or those with resume nonzero; None: from zero.  out_dtype: float32
     (default) or, with bfloat16 inputs, bfloat16."""
-    _on_gpu(x, "x", tuple(_DT), (None, None, None))
+    at = _vectors(x, "x", 3)
     tokens, H, P = x.shape
-    _on_gpu(Bm, "Bm", (x.dtype,), (tokens, None, None))
+    dtype = x.dtype
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != 3:
+        raise ValueError("Bm must be [tokens, groups, state_dim], on the device")
     G, N = Bm.shape[1:]
-    _on_gpu(Cm, "Cm", (x.dtype,), (tokens, G, N))
-    _on_gpu(dt, "dt", (torch.float32,), (tokens, H))
-    _on_gpu(A, "A", (torch.float32,), (H,))
-    _on_gpu(D, "D", (torch.float32,), (H,))
-    _on_gpu(state, "state", (torch.float32,), (None, H, P, N))
-    if initial is not None:
-        _on_gpu(initial, "initial", (torch.float32,), tuple(state.shape))
-    elif resume is not None:
-        raise ValueError("resume needs initial")
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be float32 [batch, heads, head_dim, state_dim], on the device")
+    batch = state.shape[0]
+    out_dtype = _F32 if out_dtype is None else out_dtype
     if out_dtype not in _DT:
         raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
-    prompt = _prompt(tokens, seq_start, rows, resume, status)
-    _same_device(x, Bm, Cm, dt, A, D, state, initial, seq_start, rows, resume, status)
-    cfg = B.make_config(B.KIND_MAMBA2, state.shape[0], H, G, P, N, 1,
-                        flags=B.FLAG_BF16_RECORDS if x.dtype == torch.bfloat16 else 0)
+    if initial is None and resume is not None:
+        raise ValueError("resume needs initial")
+    rec = _RECORD(_check(x, "x", dtype, (tokens, H, P), at), _check(Bm, "Bm", dtype, (tokens, G, N), at),
+                  _check(Cm, "Cm", dtype, (tokens, G, N), at), _check(dt, "dt", _F32, (tokens, H), at), 0)
+    to = _check(state, "state", _F32, (batch, H, P, N), at)
+    start = 0 if initial is None else to if initial is state else _check(initial, "initial", _F32, (batch, H, P, N), at)
+    prompt, n = _prompt(tokens, seq_start, rows, resume, status, at)
+    cfg = _CONFIG(B.KIND_MAMBA2, batch, H, G, P, N, 1, 0, 0, 0, 0, B.FLAG_BF16_RECORDS if dtype is _BF16 else 0, 0)
+    nbytes = B.replay_scan_workspace_bytes(cfg, tokens, n)
     y = torch.empty((tokens, H, P), dtype=out_dtype, device=x.device)
-    nbytes = B.replay_scan_workspace_bytes(cfg, tokens, prompt.sequences)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-    rec = B.make_record(x.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), dt.data_ptr())
-    B.replay_scan_prompt(cfg, prompt, rec, A.data_ptr(), D.data_ptr(), _ptr(initial), state.data_ptr(), y.data_ptr(),
-                         _DT[out_dtype], _ptr(ws), _stream(x))
+    B.replay_scan_prompt(cfg, prompt, rec, _check(A, "A", _F32, (H,), at), _check(D, "D", _F32, (H,), at), start, to,
+                         y.data_ptr(), _DT[out_dtype], ws.data_ptr() if nbytes else 0, _raw_stream(at))
     return y
 
 
@@ -178,23 +182,22 @@ def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=Non
     float32 [channels], or [group] shared by the groups.  norm_first False: the
     norm of y silu(z); True: the norm of y, then the gate.  out_dtype: z's type
     if None."""
-    _on_gpu(y, "y", tuple(_DT), (None, None), contiguous=False)
-    _on_gpu(z, "z", tuple(_DT), tuple(y.shape), contiguous=False)
-    _rows_apart(y, "y")
-    _rows_apart(z, "z")
+    at = _vectors(y, "y", 2)
+    if _vectors(z, "z", 2) != at:
+        raise ValueError("tensors are on several devices")
     tokens, C = y.shape
-    _on_gpu(weight, "weight", (torch.float32,), (None,))
+    if z.shape != y.shape:
+        raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(y.shape)}")
     out_dtype = z.dtype if out_dtype is None else out_dtype
     if out_dtype not in _DT:
         raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
-    if group < 1 or C % group or weight.shape[0] not in (C, group):
-        raise ValueError(f"group {group} must divide {C} channels, and weight has {weight.shape[0]} of {C} or {group} values")
-    _same_device(y, z, weight)
+    wn = weight.shape[0] if isinstance(weight, torch.Tensor) and weight.dim() == 1 else -1
+    if group < 1 or C % group or (wn != C and wn != group):
+        raise ValueError(f"group {group} must divide {C} channels, and weight be [{C}] or [{group}]")
     out = torch.empty((tokens, C), dtype=out_dtype, device=y.device)
-    args = B.replay_gated_norm_args(tokens, C, group, weight.shape[0], _DT[y.dtype], _DT[z.dtype], _DT[out_dtype],
-                                    1 if norm_first else 0, eps, 0, y.stride(0), z.stride(0), C, y.data_ptr(),
-                                    z.data_ptr(), weight.data_ptr(), out.data_ptr())
-    B.replay_gated_norm(args, _stream(y))
+    B.replay_gated_norm(_NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0,
+                              eps, 0, y.stride(0), z.stride(0), C, y.data_ptr(), z.data_ptr(),
+                              _check(weight, "weight", _F32, (wn,), at), out.data_ptr()), _raw_stream(at))
     return out
 
 
@@ -208,26 +211,24 @@ def accept_drafts(tokens, target, uniforms, *, draft=None, lengths=None):
     [0, 1): T acceptance numbers and the sampling number; lengths int32 [batch]:
     drafts of each sequence (None: T).  Returns (accepted, next), int32 [batch];
     accepted goes to ``ReplayLayer.commit``."""
-    _on_gpu(tokens, "tokens", (torch.int32,), (None, None))
-    batch, T = tokens.shape
-    _on_gpu(target, "target", tuple(_DT), (batch, T + 1, None), contiguous=False)
-    V = target.shape[-1]
-    _rows_apart(target, "target")
+    at = _vectors(target, "target", 3)
+    batch, T, V = target.shape
+    T -= 1
+    if batch < 1 or V < 1 or T < 0:
+        raise ValueError("accept_drafts needs a sequence, a row of probabilities and a vocabulary")
+    ds, q, qt = (0, 0), 0, 0
     if draft is not None:
-        _on_gpu(draft, "draft", tuple(_DT), (batch, T, V), contiguous=False)
-        _rows_apart(draft, "draft")
-    _on_gpu(uniforms, "uniforms", (torch.float32,), (batch, T + 1))
-    if lengths is not None:
-        _on_gpu(lengths, "lengths", (torch.int32,), (batch,))
-    if batch < 1 or V < 1:
-        raise ValueError("accept_drafts needs a sequence and a vocabulary")
-    _same_device(tokens, target, uniforms, draft, lengths)
-    accepted, following = torch.empty((2, batch), dtype=torch.int32, device=tokens.device)
-    ws = torch.empty(B.replay_accept_workspace_bytes(batch, V), dtype=torch.uint8, device=tokens.device)
-    ds = (draft.stride(0), draft.stride(1)) if draft is not None else (0, 0)
-    args = B.replay_accept_args(batch, T, V, _DT[target.dtype], _DT[draft.dtype] if draft is not None else 0, 0,
-                                target.stride(0), target.stride(1), *ds, tokens.data_ptr(), _ptr(lengths),
-                                target.data_ptr(), _ptr(draft), uniforms.data_ptr(), accepted.data_ptr(),
-                                following.data_ptr())
-    B.replay_accept_drafts(args, ws.data_ptr(), _stream(tokens))
+        if _vectors(draft, "draft", 3) != at or draft.shape != (batch, T, V):
+            _refuse(draft, "draft", tuple(_DT), (batch, T, V))
+        ds, q, qt = draft.stride(), draft.data_ptr(), _DT[draft.dtype]
+    ts = target.stride()
+    device = target.device
+    accepted = torch.empty(batch, dtype=_I32, device=device)
+    following = torch.empty(batch, dtype=_I32, device=device)
+    ws = torch.empty(B.replay_accept_workspace_bytes(batch, V), dtype=torch.uint8, device=device)
+    args = _ACCEPT(batch, T, V, _DT[target.dtype], qt, 0, ts[0], ts[1], ds[0], ds[1],
+                   _check(tokens, "tokens", _I32, (batch, T), at),
+                   0 if lengths is None else _check(lengths, "lengths", _I32, (batch,), at), target.data_ptr(), q,
+                   _check(uniforms, "uniforms", _F32, (batch, T + 1), at), accepted.data_ptr(), following.data_ptr())
+    B.replay_accept_drafts(args, ws.data_ptr(), _raw_stream(at))
     return accepted, following

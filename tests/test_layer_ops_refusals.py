@@ -126,3 +126,20 @@ def test_python_wrappers_refuse_host_tensors(B):
         ops.gated_norm(f(5, 8), f(5, 8), f(8), 4)
     with pytest.raises(ValueError):
         ops.accept_drafts(torch.zeros(1, 2, dtype=torch.int32), f(1, 3, 9), f(1, 3))
+
+
+def test_packed_structs_have_the_librarys_sizes(B):
+    """The Python functions pass the structs as packed bytes: as long as the C ones, field by field as ctypes lays them out."""
+    import ctypes
+    import struct
+    lib = B.load_library()
+    codes = {ctypes.c_int32: "i", ctypes.c_uint32: "I", ctypes.c_int64: "q", ctypes.c_uint64: "Q", ctypes.c_float: "f",
+             ctypes.c_void_p: "P", ctypes.POINTER(ctypes.c_float): "P", ctypes.c_int32 * 3: "3i"}
+    from hybrid_model_ssm_replay_amd import ops
+    for which, st, pack in ((5, B.replay_prompt, ops._PROMPT), (6, B.replay_short_conv, ops._CONV),
+                            (7, B.replay_gated_norm_args, ops._NORM), (8, B.replay_accept_args, ops._ACCEPT),
+                            (0, B.replay_config, ops._CONFIG), (2, B.replay_record, ops._RECORD)):
+        fields = "@" + "".join(codes[t] for _, t in st._fields_)
+        assert struct.Struct(fields).size == pack.__self__.size == lib.replay_abi_sizeof(which)
+        n = len(struct.unpack(fields, bytes(struct.calcsize(fields))))
+        assert pack(*range(n)) == struct.pack(fields, *range(n))
