@@ -4,14 +4,18 @@
 //
 // A few operations per element: HBM bound.  A thread owns V neighbouring
 // channels (16 bytes) and walks along the tokens with the last K - 1 inputs in
-// registers, so each input is read once (a prompt tile re-reads K - 1 rows).
+// registers, so each input is read once (a prompt tile re-reads K - 1 rows).  It
+// issues the loads of several tokens (a prompt) or batch rows (a step) at a time:
+// that is what keeps enough bytes under way, and in a step it also shares the
+// weights, which are as large as a row's inputs and outputs together.
 #include "ops.h"
 
 namespace rssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 32;  // tokens of a prompt tile
+constexpr int kTile = 32;   // tokens of a prompt tile
+constexpr int kAhead = 8;   // tokens of a tile whose loads are under way together
 
 template <int V, int K>
 struct Taps {
@@ -61,39 +65,55 @@ __device__ __forceinline__ T *out_of(const ShortConvArgs &a, int c, int *width) 
   return reinterpret_cast<T *>(a.out[f]) + (c - (f == 0 ? 0 : f == 1 ? a.w[0] : a.w[0] + a.w[1]));
 }
 
-template <typename T, int V, int K>
+// ROWS batch rows a thread.
+template <typename T, int V, int K, int ROWS>
 __global__ __launch_bounds__(kThreads) void short_conv_step_k(ShortConvArgs a, FastDiv per_row) {
   const int blk = blockIdx.x;
-  const int b = fdiv(blk, per_row);
-  const int c = ((blk - b * (int)per_row.d) * kThreads + threadIdx.x) * V;
+  const int b0 = fdiv(blk, per_row) * ROWS;
+  const int c = ((blk - b0 / ROWS * (int)per_row.d) * kThreads + threadIdx.x) * V;
   if (c >= a.C) return;
-  const int pos = a.pos[b];
-  if (pos < 0) {
-    if (c == 0 && a.status) atomicOr(a.status, REPLAY_STATUS_BAD_POINTERS);
-    return;
-  }
   const size_t slot_elems = (size_t)a.batch * a.C;
-  T *ring = reinterpret_cast<T *>(a.ring) + (size_t)b * a.C + c;
-  int slot = pos % a.slots;
-  float h[K - 1][V];
+  const T *x = reinterpret_cast<const T *>(a.x) + c;
+  int slot[ROWS];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) {
-    int s = slot - (K - 1) + k;
-    if (s < 0) s += a.slots;
-    load_vec<T, V>(ring + s * slot_elems, h[k]);
+  for (int i = 0; i < ROWS; ++i) {
+    const int pos = b0 + i < a.batch ? a.pos[b0 + i] : -1;
+    if (pos < 0 && b0 + i < a.batch && c == 0 && a.status) atomicOr(a.status, REPLAY_STATUS_BAD_POINTERS);
+    slot[i] = pos < 0 ? -1 : pos % a.slots;  // -1: nothing to do
   }
+  float h[ROWS][K - 1][V], v[ROWS][V];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+    if (slot[i] >= 0) {
+      const T *ring = reinterpret_cast<const T *>(a.ring) + (size_t)(b0 + i) * a.C + c;
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) {
+        int s = slot[i] - (K - 1) + k;
+        if (s < 0) s += a.slots;
+        load_vec<T, V>(ring + s * slot_elems, h[i][k]);
+      }
+      load_vec<T, V>(x + (b0 + i) * a.seq_stride, v[i]);
+    }
   const Taps<V, K> taps = load_taps<V, K>(a, c);
-  const T *x = reinterpret_cast<const T *>(a.x) + b * a.seq_stride + c;
   int width;
-  T *out = out_of<T>(a, c, &width) + (size_t)b * a.T * width;
-  for (int t = 0; t < a.T; ++t) {
-    float v[V], y[V];
-    load_vec<T, V>(x + t * a.row_stride, v);
-    taps_out<V, K>(taps, h, v, a.silu, y);
-    store_vec<T, V>(out + (size_t)t * width, y);
-    store_vec<T, V>(ring + slot * slot_elems, v);
-    slot = slot + 1 == a.slots ? 0 : slot + 1;
-    push<V, K>(h, v);
+  T *out = out_of<T>(a, c, &width);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (slot[i] < 0) continue;
+    T *ring = reinterpret_cast<T *>(a.ring) + (size_t)(b0 + i) * a.C + c;
+    T *to = out + (size_t)(b0 + i) * a.T * width;
+    int s = slot[i];
+    for (int t = 0; t < a.T; ++t) {
+      float y[V], next[V];
+      if (t + 1 < a.T) load_vec<T, V>(x + (b0 + i) * a.seq_stride + (t + 1) * a.row_stride, next);
+      taps_out<V, K>(taps, h[i], v[i], a.silu, y);
+      store_vec<T, V>(to + (size_t)t * width, y);
+      store_vec<T, V>(ring + s * slot_elems, v[i]);
+      s = s + 1 == a.slots ? 0 : s + 1;
+      push<V, K>(h[i], v[i]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] = next[e];
+    }
   }
 }
 
@@ -157,12 +177,17 @@ __global__ __launch_bounds__(kThreads) void short_conv_prompt_k(ShortConvArgs a,
   int width;
   T *out = out_of<T>(a, c, &width) + (size_t)it.begin * width;
   const int t1 = min(it.len, t0 + kTile);
-  for (int t = t0; t < t1; ++t) {
-    float v[V], y[V];
-    load_vec<T, V>(x + (size_t)t * a.row_stride, v);
-    taps_out<V, K>(taps, h, v, a.silu, y);
-    store_vec<T, V>(out + (size_t)t * width, y);
-    push<V, K>(h, v);
+  for (int t = t0; t < t1; t += kAhead) {
+    float v[kAhead][V];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_vec<T, V>(x + (size_t)min(t + i, t1 - 1) * a.row_stride, v[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      float y[V];
+      taps_out<V, K>(taps, h, v[i], a.silu, y);
+      if (t + i < t1) store_vec<T, V>(out + (size_t)(t + i) * width, y);
+      push<V, K>(h, v[i]);
+    }
   }
 }
 
@@ -177,16 +202,25 @@ bool wide(const ShortConvArgs &a, int v) {
   return !(bits & 15u) && a.row_stride % v == 0 && a.seq_stride % v == 0;
 }
 
+template <typename T, int V, int K, int ROWS>
+void launch_step(const ShortConvArgs &a, int per, hipStream_t st) {
+  hipLaunchKernelGGL((short_conv_step_k<T, V, K, ROWS>), dim3((uint32_t)((a.batch + ROWS - 1) / ROWS * per)), dim3(kThreads), 0,
+                     st, a, make_fastdiv((uint32_t)per));
+}
+
 template <typename T, int V, int K>
 int launch(const ShortConvArgs &a, bool prompt, hipStream_t st) {
   const int per = (a.C + kThreads * V - 1) / (kThreads * V);
   const int64_t rows = prompt ? items_of(a.p.tokens, a.p.n, kTile) : a.batch;
   if (rows * per > 0x7fffffffLL) return (int)hipErrorInvalidValue;
-  const FastDiv f = make_fastdiv((uint32_t)per);
-  if (prompt)
-    hipLaunchKernelGGL((short_conv_prompt_k<T, V, K>), dim3((uint32_t)(rows * per)), dim3(kThreads), 0, st, a, f);
-  else
-    hipLaunchKernelGGL((short_conv_step_k<T, V, K>), dim3((uint32_t)(rows * per)), dim3(kThreads), 0, st, a, f);
+  if (prompt) {
+    hipLaunchKernelGGL((short_conv_prompt_k<T, V, K>), dim3((uint32_t)(rows * per)), dim3(kThreads), 0, st, a,
+                       make_fastdiv((uint32_t)per));
+  } else if (rows * per >= 2 * 4 * 256 / 2) {  // two rows a thread still leave two workgroups a CU
+    launch_step<T, V, K, 2>(a, per, st);
+  } else {
+    launch_step<T, V, K, 1>(a, per, st);
+  }
   return (int)hipGetLastError();
 }
 
