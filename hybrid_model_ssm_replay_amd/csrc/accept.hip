@@ -76,15 +76,44 @@ __device__ __forceinline__ Row row_of(const replay_accept_args &a, int b, int ac
 __device__ __forceinline__ double plain(float p) { return p > 0.f ? (double)p : 0.0; }
 __device__ __forceinline__ double residual(float p, float q) { return p > fmaxf(q, 0.f) ? (double)p - (double)fmaxf(q, 0.f) : 0.0; }
 
-__device__ __forceinline__ double sum64(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+// Moves of the low and high half of a double between lanes; lanes without a source get 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  const int2 w = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, w.x, CTRL, ROWS, 0xF, false),
+                                              __builtin_amdgcn_update_dpp(0, w.y, CTRL, ROWS, 0xF, false)));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {  // lane: the same for the whole wave
+  const int2 w = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(w.x, lane), __builtin_amdgcn_readlane(w.y, lane)));
+}
+// Inclusive prefix sum of a wave: within rows of 16 by shifts, then the last lane of a
+// row to the next row, and lane 31 to the upper half.
+__device__ __forceinline__ double scan64(double v) {
+  v += moved<0x111, 0xF>(v);
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);
+  v += moved<0x143, 0xC>(v);
   return v;
 }
+__device__ __forceinline__ double sum64(double v) { return lane_value(scan64(v), kWave - 1); }
 
-// TP, TQ: types; V: values of one load (8 where every row starts on 16 bytes, else 1);
-// HAS_Q: draft probabilities are given.
-template <typename TP, typename TQ, int V, bool HAS_Q>
+// The first lane whose running sum from `run` exceeds want, else the last with any
+// weight, else -1.  over: the first kind.  run becomes the sum before that lane, or
+// after all of them where there is none beyond want.
+__device__ __forceinline__ int find64(double w, double want, double &run, bool &over) {
+  const double s = run + scan64(w);
+  const uint64_t beyond = __ballot(w > 0.0 && s > want), any = __ballot(w > 0.0);
+  over = beyond != 0;
+  const int i = over ? __builtin_ctzll(beyond) : any ? 63 - __builtin_clzll(any) : -1;
+  run = over ? (i ? lane_value(s, i - 1) : run) : lane_value(s, kWave - 1);
+  return i;
+}
+
+// TP, TQ: types; HAS_Q: draft probabilities are given.
+template <typename TP, typename TQ, bool HAS_Q>
 __global__ __launch_bounds__(kThreads) void sums_k(replay_accept_args a, Slices sl) {
   __shared__ double part[2][kWaves];
   const int b = fdiv(blockIdx.x, sl.fn), slice = blockIdx.x - b * sl.n;
@@ -97,28 +126,10 @@ __global__ __launch_bounds__(kThreads) void sums_k(replay_accept_args a, Slices 
   double sr = 0.0, sp = 0.0;
   const int v0 = slice * sl.size, v1 = min(a.vocab, v0 + sl.size);
   for (int v = v0; v < v1; v += kStep) {
+    const int at0 = v + threadIdx.x * 8, there = v1 - at0;
     float pv[8], qv[8];
-    int at0, step;
-    if constexpr (V == 8) {
-      at0 = v + threadIdx.x * 8, step = 1;
-      if (at0 + 8 <= v1) {
-        load_vec<TP, 8>(p + at0, pv);
-        if (HAS_Q && row.less) load_vec<TQ, 8>(q + at0, qv);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          pv[i] = at0 + i < v1 ? ldr<TP>(p + at0 + i) : 0.f;
-          if (HAS_Q && row.less) qv[i] = at0 + i < v1 ? ldr<TQ>(q + at0 + i) : 0.f;
-        }
-      }
-    } else {
-      at0 = v + threadIdx.x, step = kThreads;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        pv[i] = at0 + i * kThreads < v1 ? ldr<TP>(p + at0 + i * kThreads) : 0.f;
-        if (HAS_Q && row.less) qv[i] = at0 + i * kThreads < v1 ? ldr<TQ>(q + at0 + i * kThreads) : 0.f;
-      }
-    }
+    load_part<TP, 8>(p + at0, there, pv);
+    if (HAS_Q && row.less) load_part<TQ, 8>(q + at0, there, qv);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double w = plain(pv[i]);
@@ -126,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void sums_k(replay_accept_args a, Slices 
       if (HAS_Q)
         sr += row.less ? residual(pv[i], qv[i]) : w;
       else
-        sr += at0 + i * step == row.x ? 0.0 : w;
+        sr += at0 + i == row.x ? 0.0 : w;
     }
   }
   sr = sum64(sr), sp = sum64(sp);
@@ -139,27 +150,6 @@ __global__ __launch_bounds__(kThreads) void sums_k(replay_accept_args a, Slices 
   }
 }
 
-__device__ __forceinline__ double scan64(double v, int lane) {  // inclusive prefix sum of a wave
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const double o = __shfl_up(v, d, kWave);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
-// The first of a wave's values whose running sum from `run` exceeds want, else the last
-// with any weight; -1 if none has.  run becomes the sum before it.
-__device__ __forceinline__ int find64(double w, double want, double &run, int lane) {
-  const double s = run + scan64(w, lane);
-  const uint64_t over = __ballot(w > 0.0 && s > want), any = __ballot(w > 0.0);
-  if (!any) return -1;
-  const int i = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll(any);
-  const double before = __shfl_up(s, 1, kWave);
-  run = i ? __shfl(before, i, kWave) : run;
-  return i;
-}
-
 constexpr int kRows = kStep / kWave;  // rows of 64 that the workgroup sums at a time
 
 __global__ __launch_bounds__(kThreads) void pick_k(replay_accept_args a, Slices sl) {
@@ -168,96 +158,119 @@ __global__ __launch_bounds__(kThreads) void pick_k(replay_accept_args a, Slices 
   const int acc = a.accepted[b], n = drafts_of(a, b);
   Row row = row_of(a, b, acc, n);
   const double2 *sums = sl.sums + (int64_t)b * sl.n;
-  // Every wave adds the slices up; the totals say whether the residual has any weight.
-  double tr = 0.0, tp = 0.0;
-  for (int i = lane; i < sl.n; i += kWave) tr += sums[i].x, tp += sums[i].y;
-  tr = sum64(tr), tp = sum64(tp);
-  if (!(tr > 0.0)) row.less = false, row.x = -1, tr = tp;
-  const bool by_p = !(row.less || row.x >= 0);
-  if (!(tr > 0.0)) {  // also where p has a NaN sum: none, since NaN has no weight
+  const double u = (double)a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts];
+  // Every wave adds the slices up, a lane a run of neighbours; the totals say whether
+  // the residual has any weight.
+  const int per = (sl.n + kWave - 1) / kWave;
+  double wr = 0.0, wp = 0.0;
+  for (int i = lane * per; i < min(sl.n, (lane + 1) * per); ++i) wr += sums[i].x, wp += sums[i].y;
+  double total = sum64(wr);
+  const bool by_p = !(total > 0.0) || !row.less;
+  if (by_p) row.less = false, row.x = -1, total = sum64(wp);
+  if (!(total > 0.0)) {
     if (threadIdx.x == 0) a.next[b] = -1;
     return;
   }
-  const double want = (double)a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts] * tr;
-  // The slice: in turns of 64, keeping the last with weight in case rounding leaves none beyond want.
-  int slice = -1;
-  double run = 0.0, base = 0.0;
-  for (int i0 = 0; i0 < sl.n; i0 += kWave) {
-    const double2 s2 = i0 + lane < sl.n ? sums[i0 + lane] : make_double2(0.0, 0.0);
-    const double w = by_p ? s2.y : s2.x;
-    const double s = run + scan64(w, lane);
-    const uint64_t over = __ballot(w > 0.0 && s > want), any = __ballot(w > 0.0);
-    if (any) {
-      const int i = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll(any);
-      const double before = __shfl_up(s, 1, kWave);
-      slice = i0 + i;
-      base = i ? __shfl(before, i, kWave) : run;
-    }
-    if (over) break;
-    run = __shfl(s, kWave - 1, kWave);
+  const double want = u * total;
+  // The lane's run, the slice in it, the rows of 64 of the slice, the lane.  Where
+  // rounding leaves nothing beyond want, the last with any weight.
+  double run = 0.0;
+  bool over;
+  const int l = find64(by_p ? wp : wr, want, run, over);
+  if (!over) {  // the sum before that lane
+    const double s = scan64(by_p ? wp : wr);
+    run = l ? lane_value(s, l - 1) : 0.0;
   }
-  // The rows of 64 of the slice, kRows at a time, then the lane.
+  int slice = -1;
+  double base = run;
+  for (int i = l * per; i < min(sl.n, (l + 1) * per); ++i) {
+    const double w = by_p ? sums[i].y : sums[i].x;
+    if (w > 0.0) {
+      slice = i, base = run;
+      if (run + w > want) break;
+    }
+    run += w;
+  }
   const int v0 = slice * sl.size, v1 = min(a.vocab, v0 + sl.size);
-  auto weight = [&](int v) -> double {
-    if (v >= v1 || v == row.x) return 0.0;
-    const float p = at(a.target, a.target_dtype, row.p + v);
-    return row.less && a.draft ? residual(p, at(a.draft, a.draft_dtype, row.q + v)) : plain(p);
+  constexpr int MINE = kRows / kWaves;  // rows of a wave
+  // All loads of a turn are under way together: no branch stands between them.
+  auto values = [&](const void *p, int dtype, int64_t at, int v, float (&w)[MINE]) {
+    const int last = v1 - 1;
+    if (dtype == REPLAY_DT_BF16) {
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) w[i] = ldr<bf16_t>((const bf16_t *)p + at + min(v + i * kWave, last));
+    } else {
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) w[i] = ldr<float>((const float *)p + at + min(v + i * kWave, last));
+    }
   };
   int token = -1;
   for (int v = v0; v < v1; v += kStep) {
-    double w[kRows / kWaves];
+    const int mine = v + wave * MINE * kWave + lane;
+    float pw[MINE], qw[MINE] = {};
+    values(a.target, a.target_dtype, row.p, mine, pw);
+    if (row.less && a.draft) values(a.draft, a.draft_dtype, row.q, mine, qw);
+    double w[MINE];
 #pragma unroll
-    for (int i = 0; i < kRows / kWaves; ++i) w[i] = weight(v + (wave * (kRows / kWaves) + i) * kWave + lane);
+    for (int i = 0; i < MINE; ++i) {
+      const int vi = mine + i * kWave;
+      w[i] = vi >= v1 || vi == row.x ? 0.0 : residual(pw[i], qw[i]);  // without q: p itself
+    }
     __syncthreads();  // the last turn's rows are read
 #pragma unroll
-    for (int i = 0; i < kRows / kWaves; ++i) {
-      const double s = sum64(w[i]);
-      if (lane == 0) rows[wave * (kRows / kWaves) + i] = s;
+    for (int i = 0; i < MINE; ++i) {
+      const double s = scan64(w[i]);
+      if (lane == kWave - 1) rows[wave * MINE + i] = s;
     }
     __syncthreads();
-    const double rw = lane < kRows ? rows[lane] : 0.0;
-    const double s = base + scan64(rw, lane);
-    const uint64_t over = __ballot(rw > 0.0 && s > want), any = __ballot(rw > 0.0);
-    if (any) {
-      const int i = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll(any);
-      const double before = __shfl_up(s, 1, kWave);
-      double from = i ? __shfl(before, i, kWave) : base;
-      const int lane_at = find64(weight(v + i * kWave + lane), want, from, lane);
-      if (lane_at >= 0) token = v + i * kWave + lane_at;
+    const double rw = lane < kRows ? rows[lane] : 0.0, start = base;
+    const int i = find64(rw, want, base, over);
+    if (i >= 0 && i / MINE == wave) {
+      double from = over ? base : start + (i ? lane_value(scan64(rw), i - 1) : 0.0);
+      bool hit;
+      double wi = 0.0;
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) wi = k == i % MINE ? w[k] : wi;
+      const int at_lane = find64(wi, want, from, hit);
+      if (at_lane >= 0) token = v + i * kWave + at_lane;
     }
     if (over) break;  // the same for every wave
-    base = __shfl(s, kWave - 1, kWave);
   }
-  if (threadIdx.x == 0) a.next[b] = token;
+  // The wave whose rows held it; of several turns' last ones, the latest.
+  __shared__ int found[kWaves];
+  if (lane == 0) found[wave] = token;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kWaves; ++i) token = max(token, found[i]);
+    a.next[b] = token;
+  }
 }
 
-// Slices of 2048 values, longer where there would be more than 4096 workgroups: those fill the card.
+// Slices of 2048 values, longer where there would be more than 2048 workgroups: those
+// fill the card at once (128 sequences of 50021: XXX us against XXX with 2048 values).
 Slices slices_of(int batch, int vocab) {
   Slices s{};
   s.size = kStep;
-  while ((int64_t)batch * ((vocab + (int64_t)s.size - 1) / s.size) > 4096 && s.size < vocab) s.size *= 2;
+  while ((int64_t)batch * ((vocab + (int64_t)s.size - 1) / s.size) > 2048 && s.size < vocab) s.size *= 2;
   s.n = (int)((vocab + (int64_t)s.size - 1) / s.size);
   s.fn = make_fastdiv((uint32_t)s.n);
   return s;
 }
 
 template <typename TP, typename TQ, bool HAS_Q>
-void launch_sums(const replay_accept_args &a, const Slices &s, bool wide, hipStream_t st) {
+void launch_sums(const replay_accept_args &a, const Slices &s, hipStream_t st) {
   const dim3 grid((uint32_t)a.batch * s.n), block(kThreads);
-  if (wide)
-    hipLaunchKernelGGL((sums_k<TP, TQ, 8, HAS_Q>), grid, block, 0, st, a, s);
-  else
-    hipLaunchKernelGGL((sums_k<TP, TQ, 1, HAS_Q>), grid, block, 0, st, a, s);
+  hipLaunchKernelGGL((sums_k<TP, TQ, HAS_Q>), grid, block, 0, st, a, s);
 }
 
 template <typename TP>
-void launch_q(const replay_accept_args &a, const Slices &s, bool wide, hipStream_t st) {
+void launch_q(const replay_accept_args &a, const Slices &s, hipStream_t st) {
   if (!a.draft)
-    launch_sums<TP, float, false>(a, s, wide, st);
+    launch_sums<TP, float, false>(a, s, st);
   else if (a.draft_dtype == REPLAY_DT_BF16)
-    launch_sums<TP, bf16_t, true>(a, s, wide, st);
+    launch_sums<TP, bf16_t, true>(a, s, st);
   else
-    launch_sums<TP, float, true>(a, s, wide, st);
+    launch_sums<TP, float, true>(a, s, st);
 }
 
 }  // namespace
@@ -271,12 +284,10 @@ int launch_accept(const replay_accept_args &a, void *workspace, hipStream_t st) 
   Slices s = slices_of(a.batch, a.vocab);
   if ((int64_t)a.batch * s.n > 0x7fffffffLL) return (int)hipErrorInvalidValue;
   s.sums = (double2 *)workspace;
-  const bool wide = !(((uintptr_t)a.target | (uintptr_t)a.draft) & 15u) &&
-                    !((a.target_seq_stride | a.target_row_stride | a.draft_seq_stride | a.draft_row_stride) & 7);
   if (a.target_dtype == REPLAY_DT_BF16)
-    launch_q<bf16_t>(a, s, wide, st);
+    launch_q<bf16_t>(a, s, st);
   else
-    launch_q<float>(a, s, wide, st);
+    launch_q<float>(a, s, st);
   hipLaunchKernelGGL(pick_k, dim3(a.batch), dim3(kThreads), 0, st, a, s);
   return (int)hipGetLastError();
 }

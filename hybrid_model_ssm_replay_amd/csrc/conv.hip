@@ -27,9 +27,10 @@ __device__ __forceinline__ Taps<V, K> load_taps(const ShortConvArgs &a, int c) {
   Taps<V, K> t;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
+    const int cv = min(c + v, a.C - 1);
 #pragma unroll
-    for (int k = 0; k < K; ++k) t.w[k][v] = a.weight[(size_t)(c + v) * K + k];
-    t.b[v] = a.bias ? a.bias[c + v] : 0.f;
+    for (int k = 0; k < K; ++k) t.w[k][v] = a.weight[(size_t)cv * K + k];
+    t.b[v] = a.bias ? a.bias[cv] : 0.f;
   }
   return t;
 }
@@ -57,21 +58,79 @@ __device__ __forceinline__ void push(float (&h)[K - 1][V], const float (&x)[V]) 
   for (int v = 0; v < V; ++v) h[K - 2][v] = x[v];
 }
 
-// Where channel c of output row r goes, and the distance between rows.
-template <typename T>
-__device__ __forceinline__ T *out_of(const ShortConvArgs &a, int c, int *width) {
-  const int f = c < a.w[0] ? 0 : c < a.w[0] + a.w[1] ? 1 : 2;
-  *width = a.w[f];
-  return reinterpret_cast<T *>(a.out[f]) + (c - (f == 0 ? 0 : f == 1 ? a.w[0] : a.w[0] + a.w[1]));
-}
+// Where channels c .. c + V - 1 go: element (row, v) at base + row width + v, all in
+// one field, or each in its own.
+template <typename T, int V>
+struct Out {
+  T *base;
+  int width, n;        // n of the V channels exist
+  bool one;            // in one field
+  int c;
 
-// ROWS batch rows a thread.
-template <typename T, int V, int K, int ROWS>
-__global__ __launch_bounds__(kThreads) void short_conv_step_k(ShortConvArgs a, FastDiv per_row) {
-  const int blk = blockIdx.x;
-  const int b0 = fdiv(blk, per_row) * ROWS;
-  const int c = ((blk - b0 / ROWS * (int)per_row.d) * kThreads + threadIdx.x) * V;
-  if (c >= a.C) return;
+  __device__ __forceinline__ static int field(const ShortConvArgs &a, int c) { return c < a.w[0] ? 0 : c < a.w[0] + a.w[1] ? 1 : 2; }
+  __device__ __forceinline__ Out(const ShortConvArgs &a, int c0) : c(c0) {
+    n = min(V, a.C - c0);
+    const int f = field(a, c0);
+    one = field(a, c0 + n - 1) == f;
+    width = a.w[f];
+    base = reinterpret_cast<T *>(a.out[f]) + (c0 - (f == 0 ? 0 : f == 1 ? a.w[0] : a.w[0] + a.w[1]));
+  }
+  __device__ __forceinline__ void store(const ShortConvArgs &a, size_t row, const float (&y)[V]) const {
+    if (one) {
+      store_part<T, V>(base + row * width, n, y);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < n) {
+          const int f = field(a, c + v);
+          const float y1[1] = {y[v]};
+          store_vec<T, 1>(reinterpret_cast<T *>(a.out[f]) + row * a.w[f] + (c + v - (f == 0 ? 0 : f == 1 ? a.w[0] : a.w[0] + a.w[1])), y1);
+        }
+    }
+  }
+};
+
+// V elements as they lie in memory: what a thread holds of loads under way.
+template <typename T, int V, bool WHOLE>
+struct Held {
+  typename Elems<T, V>::words w;
+  __device__ __forceinline__ void load(const T *p, int n) {
+    if constexpr (WHOLE) {
+      w = *reinterpret_cast<const typename Elems<T, V>::loose *>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t u = i < n ? (sizeof(T) == 4 ? __float_as_uint(ldr<T>(p + i)) : __float_as_uint(ldr<T>(p + i)) >> 16) : 0u;
+        if constexpr (sizeof(T) == 4)
+          w[i] = u;
+        else
+          w[i / 2] = i % 2 ? w[i / 2] | u << 16 : u;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T *p, int n) const {
+    if constexpr (WHOLE) {
+      *reinterpret_cast<typename Elems<T, V>::loose *>(p) = w;
+    } else {
+      float v[V];
+      get(v);
+      store_part<T, V>(p, n, v);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (sizeof(T) == 4)
+        v[i] = __uint_as_float(w[i]);
+      else
+        v[i] = i % 2 ? __uint_as_float(w[i / 2] & 0xFFFF0000u) : __uint_as_float(w[i / 2] << 16);
+    }
+  }
+};
+
+// ROWS batch rows a thread.  WHOLE: its V channels exist and are in one field.
+template <typename T, int V, int K, int ROWS, bool WHOLE>
+__device__ __forceinline__ void step_body(const ShortConvArgs &a, const Out<T, V> &out, int c, int b0) {
   const size_t slot_elems = (size_t)a.batch * a.C;
   const T *x = reinterpret_cast<const T *>(a.x) + c;
   int slot[ROWS];
@@ -81,53 +140,65 @@ __global__ __launch_bounds__(kThreads) void short_conv_step_k(ShortConvArgs a, F
     if (pos < 0 && b0 + i < a.batch && c == 0 && a.status) atomicOr(a.status, REPLAY_STATUS_BAD_POINTERS);
     slot[i] = pos < 0 ? -1 : pos % a.slots;  // -1: nothing to do
   }
-  float h[ROWS][K - 1][V], v[ROWS][V];
+  Held<T, V, WHOLE> old[ROWS][K - 1], in[ROWS];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i)
-    if (slot[i] >= 0) {
-      const T *ring = reinterpret_cast<const T *>(a.ring) + (size_t)(b0 + i) * a.C + c;
+  for (int i = 0; i < ROWS; ++i) {
+    if (slot[i] < 0) continue;
+    const T *ring = reinterpret_cast<const T *>(a.ring) + (size_t)(b0 + i) * a.C + c;
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k) {
-        int s = slot[i] - (K - 1) + k;
-        if (s < 0) s += a.slots;
-        load_vec<T, V>(ring + s * slot_elems, h[i][k]);
-      }
-      load_vec<T, V>(x + (b0 + i) * a.seq_stride, v[i]);
+    for (int k = 0; k < K - 1; ++k) {
+      int s = slot[i] - (K - 1) + k;
+      if (s < 0) s += a.slots;
+      old[i][k].load(ring + s * slot_elems, out.n);
     }
+    in[i].load(x + (b0 + i) * a.seq_stride, out.n);
+  }
   const Taps<V, K> taps = load_taps<V, K>(a, c);
-  int width;
-  T *out = out_of<T>(a, c, &width);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     if (slot[i] < 0) continue;
     T *ring = reinterpret_cast<T *>(a.ring) + (size_t)(b0 + i) * a.C + c;
-    T *to = out + (size_t)(b0 + i) * a.T * width;
+    float h[K - 1][V];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) old[i][k].get(h[k]);
     int s = slot[i];
     for (int t = 0; t < a.T; ++t) {
-      float y[V], next[V];
-      if (t + 1 < a.T) load_vec<T, V>(x + (b0 + i) * a.seq_stride + (t + 1) * a.row_stride, next);
-      taps_out<V, K>(taps, h[i], v[i], a.silu, y);
-      store_vec<T, V>(to + (size_t)t * width, y);
-      store_vec<T, V>(ring + s * slot_elems, v[i]);
+      Held<T, V, WHOLE> next = in[i];
+      if (t + 1 < a.T) next.load(x + (b0 + i) * a.seq_stride + (t + 1) * a.row_stride, out.n);
+      float v[V], y[V];
+      in[i].get(v);
+      taps_out<V, K>(taps, h, v, a.silu, y);
+      if constexpr (WHOLE)
+        store_vec<T, V>(out.base + ((size_t)(b0 + i) * a.T + t) * out.width, y);
+      else
+        out.store(a, (size_t)(b0 + i) * a.T + t, y);
+      in[i].store(ring + s * slot_elems, out.n);
       s = s + 1 == a.slots ? 0 : s + 1;
-      push<V, K>(h[i], v[i]);
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] = next[e];
+      push<V, K>(h, v);
+      in[i] = next;
     }
   }
 }
 
-template <typename T, int V, int K>
-__global__ __launch_bounds__(kThreads) void short_conv_prompt_k(ShortConvArgs a, FastDiv per_item) {
-  const int item = fdiv(blockIdx.x, per_item);
-  const int c = ((blockIdx.x - item * (int)per_item.d) * kThreads + threadIdx.x) * V;
-  const Item it = find_item(a.p, item, kTile);
+template <typename T, int V, int K, int ROWS>
+__global__ __launch_bounds__(kThreads) void short_conv_step_k(ShortConvArgs a, FastDiv per_row) {
+  const int blk = blockIdx.x, set = fdiv(blk, per_row);
+  const int c = ((blk - set * (int)per_row.d) * kThreads + threadIdx.x) * V;
+  if (c >= a.C) return;
+  const Out<T, V> out(a, c);
+  if (out.n == V && out.one)
+    step_body<T, V, K, ROWS, true>(a, out, c, set * ROWS);
+  else
+    step_body<T, V, K, ROWS, false>(a, out, c, set * ROWS);
+}
+
+template <typename T, int V, int K, bool WHOLE>
+__device__ __forceinline__ void prompt_body(const ShortConvArgs &a, const Out<T, V> &out, int c, const Item &it, int row) {
   const int t0 = it.index * kTile;
-  if (c >= a.C || it.index < 0 || (t0 >= it.len && it.index > 0)) return;
-  const int row = batch_row(a.p, it.seq, it.index == 0 && c == 0);
-  if (row < 0) return;
   const T *x = reinterpret_cast<const T *>(a.x) + (size_t)it.begin * a.row_stride + c;
-  float h[K - 1][V];
+  const int t1 = min(it.len, t0 + kTile);
+  constexpr int AHEAD = WHOLE ? kAhead : 1;  // the few threads at a border take no registers from the others
+  Held<T, V, WHOLE> in[AHEAD], old[K - 1];
   if (t0 == 0) {
     // The first tile also replaces the ring's history by the sequence's last
     // inputs: the same thread reads the old slots before it writes them.
@@ -144,62 +215,66 @@ __global__ __launch_bounds__(kThreads) void short_conv_prompt_k(ShortConvArgs a,
     for (int k = 0; k < K - 1; ++k) {
       int s = slot - (K - 1) + k;
       if (s < 0) s += a.slots;
-      if (known) {
-        load_vec<T, V>(ring + s * slot_elems, h[k]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[k][v] = 0.f;
-      }
+      if (known)
+        old[k].load(ring + s * slot_elems, out.n);
+      else
+        old[k].w = typename Elems<T, V>::words{};
     }
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
       int s = slot - (K - 1) + k;
       if (s < 0) s += a.slots;
       const int t = it.len - (K - 1) + k;  // negative: that far into the old history
-      float v[V];
+      Held<T, V, WHOLE> last;
       if (t >= 0) {
-        load_vec<T, V>(x + (size_t)t * a.row_stride, v);
+        last.load(x + (size_t)t * a.row_stride, out.n);
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.f;
-#pragma unroll
         for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = j == K - 1 + t ? h[j][i] : v[i];
+          if (j == K - 1 + t) last = old[j];
       }
-      store_vec<T, V>(ring + s * slot_elems, v);
+      last.store(ring + s * slot_elems, out.n);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) load_vec<T, V>(x + (size_t)(t0 - (K - 1) + k) * a.row_stride, h[k]);
+    for (int k = 0; k < K - 1; ++k) old[k].load(x + (size_t)(t0 - (K - 1) + k) * a.row_stride, out.n);
   }
   const Taps<V, K> taps = load_taps<V, K>(a, c);
-  int width;
-  T *out = out_of<T>(a, c, &width) + (size_t)it.begin * width;
-  const int t1 = min(it.len, t0 + kTile);
-  for (int t = t0; t < t1; t += kAhead) {
-    float v[kAhead][V];
+  float h[K - 1][V];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_vec<T, V>(x + (size_t)min(t + i, t1 - 1) * a.row_stride, v[i]);
+  for (int k = 0; k < K - 1; ++k) old[k].get(h[k]);
+  for (int t = t0; t < t1; t += AHEAD) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      float y[V];
-      taps_out<V, K>(taps, h, v[i], a.silu, y);
-      if (t + i < t1) store_vec<T, V>(out + (size_t)(t + i) * width, y);
-      push<V, K>(h, v[i]);
+    for (int i = 0; i < AHEAD; ++i) in[i].load(x + (size_t)min(t + i, t1 - 1) * a.row_stride, out.n);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      float v[V], y[V];
+      in[i].get(v);
+      taps_out<V, K>(taps, h, v, a.silu, y);
+      if (t + i < t1) {
+        if constexpr (WHOLE)
+          store_vec<T, V>(out.base + ((size_t)it.begin + t + i) * out.width, y);
+        else
+          out.store(a, (size_t)it.begin + t + i, y);
+      }
+      push<V, K>(h, v);
     }
   }
 }
 
-// Sixteen bytes a thread where every row, field and pointer allows it.
-template <typename T>
-bool wide(const ShortConvArgs &a, int v) {
-  uintptr_t bits = (uintptr_t)a.x | (uintptr_t)a.ring;
-  for (int i = 0; i < 3; ++i) {
-    if (a.w[i] % v) return false;
-    if (a.w[i]) bits |= (uintptr_t)a.out[i];
-  }
-  return !(bits & 15u) && a.row_stride % v == 0 && a.seq_stride % v == 0;
+template <typename T, int V, int K>
+__global__ __launch_bounds__(kThreads) void short_conv_prompt_k(ShortConvArgs a, FastDiv per_item) {
+  const int item = fdiv(blockIdx.x, per_item);
+  const int c = ((blockIdx.x - item * (int)per_item.d) * kThreads + threadIdx.x) * V;
+  const Item it = find_item(a.p, item, kTile);
+  if (c >= a.C || it.index < 0 || (it.index * kTile >= it.len && it.index > 0)) return;
+  const int row = batch_row(a.p, it.seq, it.index == 0 && c == 0);
+  if (row < 0) return;
+  const Out<T, V> out(a, c);
+  if (out.n == V && out.one)
+    prompt_body<T, V, K, true>(a, out, c, it, row);
+  else
+    prompt_body<T, V, K, false>(a, out, c, it, row);
 }
 
 template <typename T, int V, int K, int ROWS>
@@ -227,14 +302,9 @@ int launch(const ShortConvArgs &a, bool prompt, hipStream_t st) {
 template <typename T>
 int dispatch(const ShortConvArgs &a, bool prompt, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(T);
-  if (wide<T>(a, W)) {
-    if (a.K == 2) return launch<T, W, 2>(a, prompt, st);
-    if (a.K == 3) return launch<T, W, 3>(a, prompt, st);
-    return launch<T, W, 4>(a, prompt, st);
-  }
-  if (a.K == 2) return launch<T, 1, 2>(a, prompt, st);
-  if (a.K == 3) return launch<T, 1, 3>(a, prompt, st);
-  return launch<T, 1, 4>(a, prompt, st);
+  if (a.K == 2) return launch<T, W, 2>(a, prompt, st);
+  if (a.K == 3) return launch<T, W, 3>(a, prompt, st);
+  return launch<T, W, 4>(a, prompt, st);
 }
 
 int any(const ShortConvArgs &a, bool prompt, hipStream_t st) {

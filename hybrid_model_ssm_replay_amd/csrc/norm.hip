@@ -39,12 +39,12 @@ __global__ __launch_bounds__(kThreads) void gated_norm_k(replay_gated_norm_args 
   const int c0 = group_there ? g * a.group : 0;
   const float inv = 1.f / (float)a.group;
   float w[IT][8];
-  bool in[IT];
+  int in[IT];  // how many of the lane's eight values there are
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int c = (i * LANES + lane) * 8;
-    in[i] = group_there && c < a.group;
-    if (in[i]) load_vec<float, 8>(a.weight + (a.weight_len == a.channels ? c0 : 0) + c, w[i]);
+    in[i] = group_there ? a.group - c : 0;
+    if (in[i] > 0) load_part<float, 8>(a.weight + (a.weight_len == a.channels ? c0 : 0) + c, in[i], w[i]);
   }
   for (int t = t0; t < t1; ++t) {
     const TY *y = (const TY *)a.y + t * a.y_stride + c0 + lane * 8;
@@ -55,9 +55,9 @@ __global__ __launch_bounds__(kThreads) void gated_norm_k(replay_gated_norm_args 
       float zv[8];
 #pragma unroll
       for (int v = 0; v < 8; ++v) h[i][v] = 0.f, zv[v] = 0.f;
-      if (in[i]) {
-        load_vec<TY, 8>(y + i * LANES * 8, h[i]);
-        load_vec<TZ, 8>(z + i * LANES * 8, zv);
+      if (in[i] > 0) {
+        load_part<TY, 8>(y + i * LANES * 8, in[i], h[i]);
+        load_part<TZ, 8>(z + i * LANES * 8, in[i], zv);
       }
 #pragma unroll
       for (int v = 0; v < 8; ++v) {
@@ -71,46 +71,46 @@ __global__ __launch_bounds__(kThreads) void gated_norm_k(replay_gated_norm_args 
     TO *out = (TO *)a.out + t * a.out_stride + c0 + lane * 8;
 #pragma unroll
     for (int i = 0; i < IT; ++i)
-      if (in[i]) {
+      if (in[i] > 0) {
 #pragma unroll
         for (int v = 0; v < 8; ++v) h[i][v] *= r * w[i][v];
-        store_vec<TO, 8>(out + i * LANES * 8, h[i]);
+        store_part<TO, 8>(out + i * LANES * 8, in[i], h[i]);
       }
   }
 }
 
-// Any group, any alignment: one wave a group of one token, two passes.
-template <typename TY, typename TZ, typename TO, int V>
-__global__ __launch_bounds__(kThreads) void gated_norm_any_k(replay_gated_norm_args a, FastDiv groups, int items) {
-  const int lane = threadIdx.x % kWave;
-  const int64_t i64 = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-  if (i64 >= items) return;
-  const int t = fdiv((int)i64, groups), g = (int)i64 - t * (int)groups.d;
-  const int c0 = g * a.group;
+// Longer groups: one workgroup a group of one token, two passes.
+template <typename TY, typename TZ, typename TO>
+__global__ __launch_bounds__(kThreads) void gated_norm_long_k(replay_gated_norm_args a, FastDiv groups) {
+  __shared__ float part[kWaves];
+  const int t = fdiv(blockIdx.x, groups), c0 = (blockIdx.x - t * (int)groups.d) * a.group;
   const TY *y = (const TY *)a.y + t * a.y_stride + c0;
   const TZ *z = (const TZ *)a.z + t * a.z_stride + c0;
   const float *w = a.weight + (a.weight_len == a.channels ? c0 : 0);
   TO *out = (TO *)a.out + t * a.out_stride + c0;
   float ss = 0.f;
-  for (int c = lane * V; c < a.group; c += kWave * V) {
-    float yv[V], zv[V];
-    load_vec<TY, V>(y + c, yv);
-    load_vec<TZ, V>(z + c, zv);
+  for (int c = threadIdx.x * 8; c < a.group; c += kThreads * 8) {
+    float yv[8], zv[8];
+    load_part<TY, 8>(y + c, a.group - c, yv);
+    load_part<TZ, 8>(z + c, a.group - c, zv);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < 8; ++v) {
       const float h = a.norm_first ? yv[v] : yv[v] * silu(zv[v]);
       ss = fmaf(h, h, ss);
     }
   }
-  const float r = rsqrtf(sum64(ss) / (float)a.group + a.eps);
-  for (int c = lane * V; c < a.group; c += kWave * V) {
-    float yv[V], zv[V], wv[V], o[V];
-    load_vec<TY, V>(y + c, yv);
-    load_vec<TZ, V>(z + c, zv);
-    load_vec<float, V>(w + c, wv);
+  ss = sum64(ss);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = ss;
+  __syncthreads();
+  const float r = rsqrtf((part[0] + part[1] + part[2] + part[3]) / (float)a.group + a.eps);
+  for (int c = threadIdx.x * 8; c < a.group; c += kThreads * 8) {
+    float yv[8], zv[8], wv[8];
+    load_part<TY, 8>(y + c, a.group - c, yv);
+    load_part<TZ, 8>(z + c, a.group - c, zv);
+    load_part<float, 8>(w + c, a.group - c, wv);
 #pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = yv[v] * silu(zv[v]) * r * wv[v];
-    store_vec<TO, V>(out + c, o);
+    for (int v = 0; v < 8; ++v) yv[v] = yv[v] * silu(zv[v]) * (r * wv[v]);
+    store_part<TO, 8>(out + c, a.group - c, yv);
   }
 }
 
@@ -128,25 +128,14 @@ int launch_fast(const replay_gated_norm_args &a, hipStream_t st) {
 
 template <typename TY, typename TZ, typename TO>
 int launch(const replay_gated_norm_args &a, hipStream_t st) {
-  const uintptr_t bits = (uintptr_t)a.y | (uintptr_t)a.z | (uintptr_t)a.out | (uintptr_t)a.weight;
-  const int64_t steps = a.group | a.y_stride | a.z_stride | a.out_stride;
-  if (!(bits & 15u) && steps % 8 == 0) {
-    if (a.group <= 128) return launch_fast<TY, TZ, TO, 16, 1>(a, st);
-    if (a.group <= 256) return launch_fast<TY, TZ, TO, 32, 1>(a, st);
-    if (a.group <= 512) return launch_fast<TY, TZ, TO, 64, 1>(a, st);
-    if (a.group <= 1024) return launch_fast<TY, TZ, TO, 64, 2>(a, st);
-    if (a.group <= 2048) return launch_fast<TY, TZ, TO, 64, 4>(a, st);
-  }
+  if (a.group <= 128) return launch_fast<TY, TZ, TO, 16, 1>(a, st);
+  if (a.group <= 256) return launch_fast<TY, TZ, TO, 32, 1>(a, st);
+  if (a.group <= 512) return launch_fast<TY, TZ, TO, 64, 1>(a, st);
+  if (a.group <= 1024) return launch_fast<TY, TZ, TO, 64, 2>(a, st);
+  if (a.group <= 2048) return launch_fast<TY, TZ, TO, 64, 4>(a, st);
   const int groups = a.channels / a.group;
-  const int items = a.tokens * groups;
-  const dim3 grid((items + kWaves - 1) / kWaves), block(kThreads);
-  const FastDiv f = make_fastdiv((uint32_t)groups);
-  if (!(bits & 15u) && steps % 8 == 0)
-    hipLaunchKernelGGL((gated_norm_any_k<TY, TZ, TO, 8>), grid, block, 0, st, a, f, items);
-  else if (!(bits & 7u) && steps % 2 == 0)  // pairs
-    hipLaunchKernelGGL((gated_norm_any_k<TY, TZ, TO, 2>), grid, block, 0, st, a, f, items);
-  else
-    hipLaunchKernelGGL((gated_norm_any_k<TY, TZ, TO, 1>), grid, block, 0, st, a, f, items);
+  hipLaunchKernelGGL((gated_norm_long_k<TY, TZ, TO>), dim3((uint32_t)(a.tokens * groups)), dim3(kThreads), 0, st, a,
+                     make_fastdiv((uint32_t)groups));
   return (int)hipGetLastError();
 }
 

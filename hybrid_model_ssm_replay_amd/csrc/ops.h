@@ -9,38 +9,30 @@ namespace rssm {
 
 // ---- element types ------------------------------------------------------------
 // V consecutive elements of type T (float, or bf16_t: the upper half of a
-// float32) as float32.  V > 1 is one aligned access of V sizeof(T) bytes (two
-// for eight floats); the caller has checked the alignment.
+// float32) as float32.  The pointer is aligned to its element only: global memory
+// takes 16-byte accesses at any address, whole lines of a wave at nearly full speed.
+template <typename T, int V>
+struct Elems {
+  typedef uint32_t words __attribute__((ext_vector_type(sizeof(T) * V / 4)));
+  typedef words loose __attribute__((aligned(sizeof(T))));
+};
 template <typename T, int V>
 __device__ __forceinline__ void load_vec(const T *p, float (&v)[V]) {
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (V % 4 == 0) {
+  if constexpr (sizeof(T) * V < 8) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 w = *reinterpret_cast<const float4 *>(p + i);
-        v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = p[i];
-    }
+    for (int i = 0; i < V; ++i) v[i] = ldr<T>(p + i);
   } else {
-    if constexpr (V % 2 == 0) {
-      typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-      const words w = *reinterpret_cast<const words *>(p);
+    constexpr int S = sizeof(T) * V > 16 ? V / 2 : V;  // 16 bytes at a time
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        uint32_t u;
-        if constexpr (V == 2)
-          u = *reinterpret_cast<const uint32_t *>(&w);
+    for (int o = 0; o < V; o += S) {
+      const typename Elems<T, S>::words w = *reinterpret_cast<const typename Elems<T, S>::loose *>(p + o);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        if constexpr (sizeof(T) == 4)
+          v[o + i] = __uint_as_float(w[i]);
         else
-          u = w[i / 2];
-        v[i] = __uint_as_float(u << 16);
-        v[i + 1] = __uint_as_float(u & 0xFFFF0000u);
+          v[o + i] = i % 2 ? __uint_as_float(w[i / 2] & 0xFFFF0000u) : __uint_as_float(w[i / 2] << 16);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __uint_as_float((uint32_t)p[i] << 16);
     }
   }
 }
@@ -56,30 +48,55 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // The store that goes with load_vec; bf16 rounds to nearest even (half a step,
-// 2^-9 of the value at most 2^-8): the array's type asks for it.
+// at most 2^-8 of the value): the array's type asks for it.
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (V % 4 == 0) {
+  if constexpr (sizeof(T) * V < 8) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) p[i] = v[i];
-    }
-  } else if constexpr (V % 2 == 0) {
-    if constexpr (V == 2) {
-      *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
-    } else {
-      typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-      words w;
-#pragma unroll
-      for (int i = 0; i < V; i += 2) w[i / 2] = pack_bf16(v[i], v[i + 1]);
-      *reinterpret_cast<words *>(p) = w;
+    for (int i = 0; i < V; ++i) {
+      if constexpr (sizeof(T) == 4)
+        p[i] = v[i];
+      else
+        p[i] = (bf16_t)pack_bf16(v[i], 0.f);
     }
   } else {
+    constexpr int S = sizeof(T) * V > 16 ? V / 2 : V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = (bf16_t)pack_bf16(v[i], 0.f);
+    for (int o = 0; o < V; o += S) {
+      typename Elems<T, S>::words w;
+#pragma unroll
+      for (int i = 0; i < S * (int)sizeof(T) / 4; ++i) {
+        if constexpr (sizeof(T) == 4)
+          w[i] = __float_as_uint(v[o + i]);
+        else
+          w[i] = pack_bf16(v[o + 2 * i], v[o + 2 * i + 1]);
+      }
+      *reinterpret_cast<typename Elems<T, S>::loose *>(p + o) = w;
+    }
+  }
+}
+
+// The first n of V elements; the others are zero, or not written.
+template <typename T, int V>
+__device__ __forceinline__ void load_part(const T *p, int n, float (&v)[V]) {
+  if (n >= V) {
+    load_vec<T, V>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < n ? ldr<T>(p + i) : 0.f;
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_part(T *p, int n, const float (&v)[V]) {
+  if (n >= V) {
+    store_vec<T, V>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        const float one[1] = {v[i]};
+        store_vec<T, 1>(p + i, one);
+      }
   }
 }
 
