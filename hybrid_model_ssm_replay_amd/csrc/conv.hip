@@ -14,26 +14,55 @@ namespace rssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 32;   // tokens of a prompt tile
-constexpr int kAhead = 8;   // tokens of a tile whose loads are under way together
+constexpr int kAhead = 4;  // tokens of a tile whose loads are under way while as many are computed
 
 template <int V, int K>
 struct Taps {
   float w[K][V], b[V];
 };
 
+// The workgroup's taps go through LDS: a thread's own lie 16 V K bytes from its
+// neighbour's, so reading them directly would touch eight times the lines (a step
+// of 256 rows: XXX us so, XXX directly).  Granules of 16 bytes are permuted so that
+// neither side meets a bank twice.  Every thread of the workgroup takes part.
 template <int V, int K>
-__device__ __forceinline__ Taps<V, K> load_taps(const ShortConvArgs &a, int c) {
-  Taps<V, K> t;
+struct TapsLds {
+  static constexpr int kGranules = kThreads * V * K / 4;
+  float4 at[kGranules];
+  __device__ __forceinline__ static int place(int e) { return e ^ (e >> 3 & 15); }
+  // c0: the workgroup's first channel.
+  __device__ __forceinline__ void stage(const ShortConvArgs &a, int c0) {
+    const float *w = a.weight + (size_t)c0 * K;
+    const int64_t n = (int64_t)(a.C - c0) * K;  // values there are
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int cv = min(c + v, a.C - 1);
-#pragma unroll
-    for (int k = 0; k < K; ++k) t.w[k][v] = a.weight[(size_t)cv * K + k];
-    t.b[v] = a.bias ? a.bias[cv] : 0.f;
+    for (int i = 0; i < kGranules / kThreads; ++i) {
+      const int e = i * kThreads + threadIdx.x;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (4 * e + 4 <= n)
+        v = ld4(w + 4 * e);
+      else if (4 * e < n)
+        v = make_float4(w[4 * e], 4 * e + 1 < n ? w[4 * e + 1] : 0.f, 4 * e + 2 < n ? w[4 * e + 2] : 0.f, 0.f);
+      at[place(e)] = v;
+    }
   }
-  return t;
-}
+  __device__ __forceinline__ Taps<V, K> get(const ShortConvArgs &a, int c, int n) const {
+    Taps<V, K> t;
+    float f[V * K];
+#pragma unroll
+    for (int i = 0; i < V * K / 4; ++i) {
+      const float4 v = at[place(threadIdx.x * (V * K / 4) + i)];
+      f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) t.w[k][v] = f[v * K + k];
+      t.b[v] = 0.f;
+    }
+    if (a.bias) load_part<float, V>(a.bias + c, n, t.b);
+    return t;
+  }
+};
 
 template <int V, int K>
 __device__ __forceinline__ void taps_out(const Taps<V, K> &t, const float (&h)[K - 1][V], const float (&x)[V], int silu_on,
@@ -130,7 +159,7 @@ struct Held {
 
 // ROWS batch rows a thread.  WHOLE: its V channels exist and are in one field.
 template <typename T, int V, int K, int ROWS, bool WHOLE>
-__device__ __forceinline__ void step_body(const ShortConvArgs &a, const Out<T, V> &out, int c, int b0) {
+__device__ __forceinline__ void step_body(const ShortConvArgs &a, const TapsLds<V, K> &lds, const Out<T, V> &out, int c, int b0) {
   const size_t slot_elems = (size_t)a.batch * a.C;
   const T *x = reinterpret_cast<const T *>(a.x) + c;
   int slot[ROWS];
@@ -153,7 +182,7 @@ __device__ __forceinline__ void step_body(const ShortConvArgs &a, const Out<T, V
     }
     in[i].load(x + (b0 + i) * a.seq_stride, out.n);
   }
-  const Taps<V, K> taps = load_taps<V, K>(a, c);
+  const Taps<V, K> taps = lds.get(a, c, out.n);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     if (slot[i] < 0) continue;
@@ -183,22 +212,25 @@ __device__ __forceinline__ void step_body(const ShortConvArgs &a, const Out<T, V
 template <typename T, int V, int K, int ROWS>
 __global__ __launch_bounds__(kThreads) void short_conv_step_k(ShortConvArgs a, FastDiv per_row) {
   const int blk = blockIdx.x, set = fdiv(blk, per_row);
-  const int c = ((blk - set * (int)per_row.d) * kThreads + threadIdx.x) * V;
+  const int c0 = (blk - set * (int)per_row.d) * kThreads * V, c = c0 + threadIdx.x * V;
+  __shared__ TapsLds<V, K> lds;
+  lds.stage(a, c0);
+  __syncthreads();
   if (c >= a.C) return;
   const Out<T, V> out(a, c);
   if (out.n == V && out.one)
-    step_body<T, V, K, ROWS, true>(a, out, c, set * ROWS);
+    step_body<T, V, K, ROWS, true>(a, lds, out, c, set * ROWS);
   else
-    step_body<T, V, K, ROWS, false>(a, out, c, set * ROWS);
+    step_body<T, V, K, ROWS, false>(a, lds, out, c, set * ROWS);
 }
 
 template <typename T, int V, int K, bool WHOLE>
-__device__ __forceinline__ void prompt_body(const ShortConvArgs &a, const Out<T, V> &out, int c, const Item &it, int row) {
-  const int t0 = it.index * kTile;
+__device__ __forceinline__ void prompt_body(const ShortConvArgs &a, const TapsLds<V, K> &lds, const Out<T, V> &out, int c, const Item &it, int row) {
+  const int t0 = it.index * a.T;
   const T *x = reinterpret_cast<const T *>(a.x) + (size_t)it.begin * a.row_stride + c;
-  const int t1 = min(it.len, t0 + kTile);
+  const int t1 = min(it.len, t0 + a.T);
   constexpr int AHEAD = WHOLE ? kAhead : 1;  // the few threads at a border take no registers from the others
-  Held<T, V, WHOLE> in[AHEAD], old[K - 1];
+  Held<T, V, WHOLE> in[2][AHEAD], old[K - 1];
   if (t0 == 0) {
     // The first tile also replaces the ring's history by the sequence's last
     // inputs: the same thread reads the old slots before it writes them.
@@ -239,17 +271,21 @@ __device__ __forceinline__ void prompt_body(const ShortConvArgs &a, const Out<T,
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) old[k].load(x + (size_t)(t0 - (K - 1) + k) * a.row_stride, out.n);
   }
-  const Taps<V, K> taps = load_taps<V, K>(a, c);
+  if (t0 >= t1) return;  // an empty sequence had only its ring to do
+  auto fetch = [&](int t, int half) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) in[half][i].load(x + (size_t)min(t + i, t1 - 1) * a.row_stride, out.n);
+  };
+  fetch(t0, 0);
+  const Taps<V, K> taps = lds.get(a, c, out.n);
   float h[K - 1][V];
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) old[k].get(h[k]);
-  for (int t = t0; t < t1; t += AHEAD) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) in[i].load(x + (size_t)min(t + i, t1 - 1) * a.row_stride, out.n);
+  auto emit = [&](int t, int half) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       float v[V], y[V];
-      in[i].get(v);
+      in[half][i].get(v);
       taps_out<V, K>(taps, h, v, a.silu, y);
       if (t + i < t1) {
         if constexpr (WHOLE)
@@ -259,22 +295,33 @@ __device__ __forceinline__ void prompt_body(const ShortConvArgs &a, const Out<T,
       }
       push<V, K>(h, v);
     }
+  };
+  // The loads of the next AHEAD tokens are under way while these are computed.
+  for (int t = t0; t < t1; t += 2 * AHEAD) {
+    fetch(t + AHEAD, 1);
+    emit(t, 0);
+    fetch(t + 2 * AHEAD, 0);
+    emit(t + AHEAD, 1);
   }
 }
 
 template <typename T, int V, int K>
-__global__ __launch_bounds__(kThreads) void short_conv_prompt_k(ShortConvArgs a, FastDiv per_item) {
+__global__ __launch_bounds__(kThreads, 4) void short_conv_prompt_k(ShortConvArgs a, FastDiv per_item) {
   const int item = fdiv(blockIdx.x, per_item);
-  const int c = ((blockIdx.x - item * (int)per_item.d) * kThreads + threadIdx.x) * V;
-  const Item it = find_item(a.p, item, kTile);
-  if (c >= a.C || it.index < 0 || (it.index * kTile >= it.len && it.index > 0)) return;
+  const int c0 = (blockIdx.x - item * (int)per_item.d) * kThreads * V, c = c0 + threadIdx.x * V;
+  const Item it = find_item(a.p, item, a.T);
+  if (it.index < 0 || (it.index * a.T >= it.len && it.index > 0)) return;
   const int row = batch_row(a.p, it.seq, it.index == 0 && c == 0);
   if (row < 0) return;
+  __shared__ TapsLds<V, K> lds;
+  lds.stage(a, c0);
+  __syncthreads();
+  if (c >= a.C) return;
   const Out<T, V> out(a, c);
   if (out.n == V && out.one)
-    prompt_body<T, V, K, true>(a, out, c, it, row);
+    prompt_body<T, V, K, true>(a, lds, out, c, it, row);
   else
-    prompt_body<T, V, K, false>(a, out, c, it, row);
+    prompt_body<T, V, K, false>(a, lds, out, c, it, row);
 }
 
 template <typename T, int V, int K, int ROWS>
@@ -283,15 +330,24 @@ void launch_step(const ShortConvArgs &a, int per, hipStream_t st) {
                      st, a, make_fastdiv((uint32_t)per));
 }
 
+// Tokens of a prompt tile: the fewest, in steps of 8, whose workgroups the card
+// holds at once (four of 128 registers a CU), so that none waits for a second round.
+int tile_of(const ShortConvArgs &a, int per) {
+  const int64_t items = 4 * 256 / per - a.p.n;
+  const int64_t t = items > 0 ? (a.p.tokens + items - 1) / items : 1 << 20;
+  return (int)(t < 16 ? 16 : t > 128 ? 128 : (t + 7) / 8 * 8);
+}
+
 template <typename T, int V, int K>
-int launch(const ShortConvArgs &a, bool prompt, hipStream_t st) {
+int launch(ShortConvArgs a, bool prompt, hipStream_t st) {
   const int per = (a.C + kThreads * V - 1) / (kThreads * V);
-  const int64_t rows = prompt ? items_of(a.p.tokens, a.p.n, kTile) : a.batch;
+  if (prompt) a.T = tile_of(a, per);
+  const int64_t rows = prompt ? items_of(a.p.tokens, a.p.n, a.T) : a.batch;
   if (rows * per > 0x7fffffffLL) return (int)hipErrorInvalidValue;
   if (prompt) {
     hipLaunchKernelGGL((short_conv_prompt_k<T, V, K>), dim3((uint32_t)(rows * per)), dim3(kThreads), 0, st, a,
                        make_fastdiv((uint32_t)per));
-  } else if (rows * per >= 2 * 4 * 256 / 2) {  // two rows a thread still leave two workgroups a CU
+  } else if (rows * per >= 1024) {  // two rows a thread still leave two workgroups a CU
     launch_step<T, V, K, 2>(a, per, st);
   } else {
     launch_step<T, V, K, 1>(a, per, st);

@@ -157,7 +157,7 @@ struct ShortConvArgs {
   int32_t *status;
   const void *x;
   int64_t seq_stride, row_stride;
-  int T;       // step: tokens a row
+  int T;       // step: tokens a row; prompt: tokens of a tile
   Packed p;    // prompt
   void *out[3];
 };
