@@ -43,9 +43,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int CT = 2;                    // 16-column tiles of a wave
-constexpr int kCols = 16 * CT * kWaves;  // x columns of a workgroup
-constexpr int kHeads = 4;           // heads of a workgroup at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 // LDS tiles are rows of 256 bytes, a token each, in 16-byte granules of eight
@@ -57,6 +54,11 @@ constexpr int kRow = 256;
 // at one column; 32 lanes of 8 bytes at a time each.
 __device__ __forceinline__ int in_row(int row, int c) {  // byte of column c (a multiple of 4) in its row
   return ((c >> 3 ^ (2 * (row & 7) | (row >> 3 & 1))) << 4) + (c >> 2 & 1) * 8;
+}
+// x in rows of 128 bytes, two of which meet the banks that one of 256 does: the transposing read only.
+template <int BYTES>
+__device__ __forceinline__ int in_row_x(int row, int c) {
+  return BYTES == kRow ? in_row(row, c) : ((c >> 3 ^ (row & 6)) << 4) + (c >> 2 & 1) * 8;
 }
 // C: a granule holds a lane's operand of one 32-column step k, columns 32 k + 4 q
 // .. + 3 and 32 k + 16 + 4 q .. + 3, and is read whole by 16 rows at a time.
@@ -172,10 +174,12 @@ __device__ __forceinline__ void interleave() {
 struct ScanPlan {
   int seg;        // tokens of a segment (a multiple of 64), or 0: sequences are not split
   int items;      // segments of all sequences
-  int hw, wph;    // heads of a workgroup, waves of a head
+  int ct;         // 16-column tiles of a wave
+  int hw, wph;    // heads of a workgroup, waves of a head in it
+  int parts;      // workgroups a head's columns are spread over (then hw is 1)
   int nb;         // workgroups of a group
   int units;      // items x groups: the workgroups of a unit share B and C
-  FastDiv fnb, fG;
+  FastDiv fnb, fG, fparts;
   float *state;   // [items][H][P N]: a segment's own state, then its start
   float *decay;   // [items][H]
 };
@@ -185,24 +189,31 @@ struct ScanPlan {
 // decay.  kFrom: segments start from the states that combine_k left.
 enum { kAll = 0, kOwn = 1, kFrom = 2 };
 
-// Compile-time shape of a kernel: R records, Y outputs, NK 32-column steps of the state.
-template <typename R, typename Y, int NK, int MODE>
+// Compile-time shape of a kernel: R records, Y outputs, NK 32-column steps of the
+// state, CT 16-column tiles of x a wave.
+template <typename R, typename Y, int NK, int CT, int MODE>
 struct Shape_ {
+  static constexpr int COLS = 16 * CT * kWaves;            // x columns of a workgroup
   static constexpr bool OUT = MODE != kOwn;
   static constexpr int IP = sizeof(R) == 4 ? 3 : 1;        // pieces of an input
   static constexpr int MP = sizeof(Y) == 4 ? 3 : 1;        // pieces of M and S
   static constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;  // blocks and tokens of a chunk
   static constexpr int TILES = QB * (QB + 1) / 2;
-  static constexpr int RS = kRow, XS = kRow;  // bytes of a row of B, C and of x
+  static constexpr int RS = kRow, XS = 2 * COLS;           // bytes of a row of B and C, and of x
   static constexpr int B0 = 0, C0 = B0 + IP * Q * RS, X0 = C0 + (OUT ? IP * Q * RS : 0), SC0 = X0 + IP * Q * XS;
   static constexpr int SC = 6 * Q * 4;  // per head: six values a token
-  static constexpr int G0 = SC0 + kHeads * SC;
-  static constexpr int LDS = G0 + (OUT ? TILES * kWave * 16 : 0);
+  static constexpr int G0 = SC0, SC1 = G0 + (OUT ? TILES * kWave * 16 : 0);
+  static constexpr int lds(int heads) { return SC1 + heads * SC; }
+  // Waves a SIMD: as many as the tiles of one and the registers of the other allow.
+  static constexpr int WAVES = CT == 2 ? 2 : OUT ? 3 : 4;
 };
 
-template <typename R, typename Y, int NK, int MODE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void scan_k(ScanArgs a, ScanPlan plan) {
-  typedef Shape_<R, Y, NK, MODE> Z;
+template <typename R, typename Y, int NK, int CT, int MODE>
+__global__ __launch_bounds__(kThreads)
+__attribute__((amdgpu_waves_per_eu(Shape_<R, Y, NK, CT, MODE>::WAVES, Shape_<R, Y, NK, CT, MODE>::WAVES)))
+void scan_k(ScanArgs a, ScanPlan plan) {
+  typedef Shape_<R, Y, NK, CT, MODE> Z;
+  constexpr int kCols = Z::COLS;
   constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
   constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
   constexpr int NV = 4 * NK, XV = kCols / 8;             // granules of a row
@@ -242,17 +253,21 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const int row = batch_row(a.p, seq, g == 0 && blk == 0 && tid == 0 && MODE != kOwn && t_first == 0);
   if (row < 0) return;
 
-  const int h0 = g * Hg + blk * plan.hw;                       // the workgroup's first head
-  const int nh = min(plan.hw, Hg - blk * plan.hw);
-  const int hw_ = wave / plan.wph;
-  const bool active = hw_ < nh;                                // this wave has a tile of x columns
-  const int hi = active ? hw_ : 0, pt0 = active ? wave % plan.wph * CT : 0;
+  // The workgroup's heads, or its part of one head's columns.
+  const int bh = fdiv(blk, plan.fparts), part = blk - bh * plan.parts;
+  const int h0 = g * Hg + bh * plan.hw;                        // the first head
+  const int nh = min(plan.hw, Hg - bh * plan.hw);
+  const int hw_ = wave / plan.wph, pw = wave - hw_ * plan.wph;
+  const int c0 = part * plan.wph * 16 * CT;                    // the head's first column here
+  const bool active = hw_ < nh && c0 + 16 * CT * pw < P;       // this wave has tiles of x columns
+  const int hi = active ? hw_ : 0, pt0 = active ? c0 / 16 + pw * CT : c0 / 16;
   const int np = min(CT, P / 16 - pt0);                        // a head's last wave may have a tile less
   const int h = h0 + hi;
-  const int xcol = hi * P + 16 * pt0;
-  const int ncols = nh * P;
+  const int xcol = hi * P + 16 * pt0 - c0;
+  const int ncols = plan.parts > 1 ? min(plan.wph * 16 * CT, P - c0) : nh * P;
+  const bool first = active && pw == 0;                        // the head's first wave here
   const float Al = uniform(a.A[h] * kLog2e), D = OUT ? uniform(a.D[h]) : 0.f;
-  float *const my = reinterpret_cast<float *>(lds + Z::SC0) + hi * 6 * Q;  // the head's values a token
+  float *const my = reinterpret_cast<float *>(lds + Z::SC1) + hi * 6 * Q;  // the head's values a token
   float4 *const sG = reinterpret_cast<float4 *>(lds + Z::G0) + lane;
 
   // The state: S^T tile nt, rows n = 16 nt + 4 q + i, column p = r of each of the wave's tiles.
@@ -282,7 +297,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   const size_t rB = (size_t)a.G * N, rX = (size_t)a.H * P;
   const R *Bg = (const R *)a.Bm + (size_t)begin * rB + (size_t)g * N;
   const R *Cg = (const R *)a.Cm + (size_t)begin * rB + (size_t)g * N;
-  const R *Xg = (const R *)a.x + (size_t)begin * rX + (size_t)h0 * P;
+  const R *Xg = (const R *)a.x + (size_t)begin * rX + (size_t)h0 * P + c0;
   const float *dtg = a.dt + (size_t)begin * a.H + h;
   constexpr int kNowhere = 0x7fffff00;
   float dtv = 0.f;
@@ -322,7 +337,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const int id = again(tid);
     const int tB = id / NV, tX = id / XV;
     char *toB = lds + Z::B0 + tB * RS + in_row(tB, id % NV * 8), *toC = lds + Z::C0 + tB * RS + in_row_c(tB, id % NV / 4, id % 4);
-    char *toX = lds + Z::X0 + tX * XS + in_row(tX, id % XV * 8);
+    char *toX = lds + Z::X0 + tX * XS + in_row_x<XS>(tX, id % XV * 8);
     if (RB <= Q || tB < Q) {
 #pragma unroll
       for (int i = 0; i < LB; ++i) {
@@ -384,7 +399,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
     lds_barrier();  // every wave is done with the last chunk's tiles
     spill();
-    if (active && pt0 == 0 && lane < Q) {
+    if (first && lane < Q) {
       my[lane] = edt * after;
       if constexpr (OUT) {
         my[Q + lane] = epre;
@@ -421,7 +436,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     auto load_x = [&]() {
 #pragma unroll
       for (int pt = 0; pt < CT; ++pt) {
-        const char *p = lds + Z::X0 + tr * XS + in_row(tr, xcol + (pt < np ? 16 * pt : 0) + lr % 4 * 4);
+        const char *p = lds + Z::X0 + tr * XS + in_row_x<XS>(tr, xcol + (pt < np ? 16 * pt : 0) + lr % 4 * 4);
 #pragma unroll
         for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -662,7 +677,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (16 * nt < N && pt < np)
           st4(to + tile0 + (size_t)16 * pt * N + 16 * nt, make_float4(S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]));
   }
-  if (MODE == kOwn && active && pt0 == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
+  if (MODE == kOwn && first && part == 0 && lane == 0) plan.decay[(size_t)item * a.H + h] = decay;
 }
 
 // Where each segment of a split sequence starts: the segment before it decays
@@ -687,20 +702,27 @@ __global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan,
   }
 }
 
-ScanPlan make_plan(const ScanArgs &a) {
-  ScanPlan p{};
-  const int Hg = a.H / a.G;
-  p.wph = (a.P / 16 + CT - 1) / CT;
-  p.hw = kWaves / p.wph < kHeads ? kWaves / p.wph : kHeads;
-  if (p.hw > Hg) p.hw = Hg;
-  p.nb = (Hg + p.hw - 1) / p.hw;
-  const int per = a.G * p.nb;
+// The workgroups of an item with ct tiles a wave.
+void set_tiles(const ScanArgs &a, ScanPlan &p, int ct) {
+  const int Hg = a.H / a.G, waves = (a.P / 16 + ct - 1) / ct;  // of a head
+  p.ct = ct;
+  p.parts = (waves + kWaves - 1) / kWaves;
+  p.wph = (waves + p.parts - 1) / p.parts;
+  p.hw = kWaves / p.wph < Hg ? kWaves / p.wph : Hg;
+  p.nb = (Hg + p.hw - 1) / p.hw * p.parts;
   p.fnb = make_fastdiv((uint32_t)p.nb);
   p.fG = make_fastdiv((uint32_t)a.G);
+  p.fparts = make_fastdiv((uint32_t)p.parts);
+}
+
+ScanPlan make_plan(const ScanArgs &a) {
+  ScanPlan p{};
+  set_tiles(a, p, 2);
+  const int per = a.G * p.nb;
   // Split sequences along the length when there are too few to fill the card.
   const int want = (512 + per - 1) / per;
   const int seg = ((a.p.tokens + want - 1) / want + 63) / 64 * 64;
-  p.seg = a.p.n >= want || seg >= a.p.tokens ? 0 : seg < 256 ? 256 : seg;
+  p.seg = a.p.n >= want || seg >= a.p.tokens ? 0 : seg < 128 ? 128 : seg;
   if (p.seg >= a.p.tokens) p.seg = 0;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
   p.units = p.items * a.G;
@@ -710,24 +732,30 @@ ScanPlan make_plan(const ScanArgs &a) {
 size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.items * a.H * 4 + 255) / 256 * 256; }
 
 template <typename R, typename Y, int NK, int MODE>
-void launch_part(const ScanArgs &a, const ScanPlan &p, dim3 grid, hipStream_t st) {
-  hipLaunchKernelGGL((scan_k<R, Y, NK, MODE>), grid, dim3(kThreads), (Shape_<R, Y, NK, MODE>::LDS), st, a, p);
+int launch_part(const ScanArgs &a, ScanPlan p, int ct, hipStream_t st) {
+  set_tiles(a, p, ct);
+  const int64_t blocks = ((int64_t)p.units + kXcds - 1) / kXcds * kXcds * p.nb;
+  if (blocks > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  const dim3 grid((uint32_t)blocks), block(kThreads);
+  if (ct == 1)
+    hipLaunchKernelGGL((scan_k<R, Y, NK, 1, MODE>), grid, block, (Shape_<R, Y, NK, 1, MODE>::lds(p.hw)), st, a, p);
+  else
+    hipLaunchKernelGGL((scan_k<R, Y, NK, 2, MODE>), grid, block, (Shape_<R, Y, NK, 2, MODE>::lds(p.hw)), st, a, p);
+  return (int)hipGetLastError();
 }
 
 template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
-  const int64_t blocks = ((int64_t)p.items * a.G + kXcds - 1) / kXcds * kXcds * p.nb;
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffLL || (int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
-  const dim3 grid((uint32_t)blocks);
-  if (!p.seg) {
-    launch_part<R, Y, NK, kAll>(a, p, grid, st);
-  } else {
-    launch_part<R, Y, NK, kOwn>(a, p, grid, st);
-    hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
-    launch_part<R, Y, NK, kFrom>(a, p, grid, st);
-  }
-  return (int)hipGetLastError();
+  if ((int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  // Own states of float32 records: half the columns leave LDS for four workgroups a CU
+  // (2048 tokens of 64 heads: 100 us a pass against 109).
+  const int ct = 2, ct_own = sizeof(R) == 4 ? 1 : 2;
+  if (!p.seg) return launch_part<R, Y, NK, kAll>(a, p, ct, st);
+  const int e = launch_part<R, Y, NK, kOwn>(a, p, ct_own, st);
+  if (e) return e;
+  hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
+  return launch_part<R, Y, NK, kFrom>(a, p, ct, st);
 }
 
 template <typename R, typename Y>
