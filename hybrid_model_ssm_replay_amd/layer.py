@@ -11,6 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
+from . import ops
 
 _FIELDS = {B.KIND_MAMBA2: ("x", "B", "C", "dt"), B.KIND_GDN: ("q", "k", "v", "alpha", "beta")}
 _VECTOR_FIELDS = ("x", "B", "C", "q", "k", "v")  # bf16 with FLAG_BF16_RECORDS; the scalars stay float32
@@ -173,6 +174,47 @@ class ReplayLayer:
         out = torch.empty(self.shapes.batch, dtype=torch.int32, device=self.ckpt.device)
         B.replay_record_slots(self.ctx, out.data_ptr(), _stream())
         return out
+
+    def prefill(self, rec: dict, seq_start: torch.Tensor, rows: torch.Tensor | None = None,
+                resume: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+        """Run packed prompts (Mamba-2): y for every token, [tokens, heads, head_dim];
+        the layer's next step of a prompted sequence continues behind its last token.
+
+        rec: x [tokens, heads, head_dim], B and C [tokens, groups, state_dim], dt
+        [tokens, heads]; seq_start, rows, resume, out_dtype as for ``ops.scan_prompt``,
+        whose resumed sequences continue from their state here, the records of their
+        window included.  The windows of prompted sequences are emptied; the others
+        are left alone, except for drafts still pending, which are discarded as by a
+        step.  Positions do not move.  The state is computed in float32 and stored in
+        the layer's formats; where the checkpoint itself is in a lower one, prompts
+        are for the whole batch (rows None) and resume is not possible."""
+        s = self.shapes
+        if s.kind != B.KIND_MAMBA2:
+            raise ValueError("prompts are for Mamba-2 layers")
+        if not isinstance(seq_start, torch.Tensor) or seq_start.dim() != 1 or seq_start.shape[0] < 2:
+            raise ValueError("seq_start must be int32 [sequences + 1], on the device")
+        n = seq_start.shape[0] - 1
+        if n > s.batch:
+            raise ValueError(f"{n} prompts for {s.batch} sequences")
+        if rows is not None and not (rows.is_cuda and rows.dtype == torch.int32 and tuple(rows.shape) == (n,)):
+            raise ValueError("rows must be an int32 device tensor [sequences]")
+        if rec["x"].dtype is not s.vec_dtype:
+            raise ValueError(f"x must be {s.vec_dtype}, the type of the layer's records")
+        f32 = self.cfg.ckpt_fmt == B.FMT_F32
+        if not f32 and (resume is not None or rows is not None or n != s.batch):
+            raise ValueError("with a checkpoint below float32, prompts are for the whole batch, in order, and from zero")
+        at = torch.arange(s.batch, device=self.ckpt.device)
+        mask = at < n if rows is None else (at[:, None] == rows[None, :]).any(1)
+        self.flush(None if rows is None and n == s.batch else mask.to(torch.uint8))
+        in_place = f32 and self.read_copy is None
+        state = self.checkpoint if in_place else self.checkpoint.clone() if f32 else torch.empty(
+            (s.batch, s.heads, s.head_dim, s.state_dim), dtype=torch.float32, device=self.ckpt.device)
+        y = ops.scan_prompt(rec["x"], rec["B"], rec["C"], rec["dt"], self.A, self.D, seq_start, state,
+                            initial=None if resume is None else state, rows=rows, resume=resume, out_dtype=out_dtype,
+                            status=self.status_word)
+        if not in_place:
+            self.set_state(state)
+        return y
 
     def step(self, rec: dict, y: torch.Tensor | None = None) -> torch.Tensor:
         lead = (self.shapes.batch,)
