@@ -226,10 +226,8 @@ void scan_k(ScanArgs a, ScanPlan plan) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane % 16, q = lane / 16;
   // Unit u on XCD u % 8 (workgroup i runs on XCD i % 8): a unit's workgroups share an
-  // L2, and items without work, which come at the end of each sequence, spread over the
-  // XCDs.  An XCD takes another group in each item: a row of B holds all groups, 256
-  // bytes each, so one group for an XCD would keep two of its L2's sixteen channels
-  // busy and the others idle (kernel of a prompt of 8192 tokens: XXX us).
+  // L2.  Items without work come at the end of each sequence, so an XCD takes another
+  // group in each item.
   const int k8 = blockIdx.x / kXcds, u8 = fdiv(k8, plan.fnb);
   const int unit = u8 * kXcds + blockIdx.x % kXcds, blk = k8 - u8 * plan.nb;
   if (unit >= plan.units) return;
@@ -375,6 +373,15 @@ void scan_k(ScanArgs a, ScanPlan plan) {
   float decay = 1.f;
   fetch(t_first, true, true);
   for (int t0 = t_first; t0 < t_end; t0 += Q) {
+    // Two workgroups share a SIMD, and the older one's instructions go first: it would end
+    // early and leave the other alone for the last quarter, so they take turns of two
+    // chunks.  The stretch of M is a chain of dependent steps and goes before both
+    // (prompts of 16384 tokens: 415 us; turns alone 424, M alone 413, neither 442; of 8192:
+    // 203, 205, 206, 209).
+    if ((t0 / Q / 2 + (blockIdx.x >= gridDim.x / 2)) & 1)
+      __builtin_amdgcn_s_setprio(1);
+    else
+      __builtin_amdgcn_s_setprio(0);
     // Decays: lane = token.
     const float dt = dtv;
     double sum = dt;
@@ -559,6 +566,7 @@ void scan_k(ScanArgs a, ScanPlan plan) {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (OUT) __builtin_amdgcn_s_setprio(2);
     fetch(t0 + Q, true, !OUT);
 
     if constexpr (OUT) {
