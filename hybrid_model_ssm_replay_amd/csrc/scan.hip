@@ -178,6 +178,7 @@ struct ScanPlan {
   int hw, wph;    // heads of a workgroup, waves of a head in it
   int parts;      // workgroups a head's columns are spread over (then hw is 1)
   int nb;         // workgroups of a group
+  int adds;       // segments add up the own states before them themselves; 0: combine_k does
   int units;      // items x groups: the workgroups of a unit share B and C
   FastDiv fnb, fG, fparts;
   float *state;   // [items][H][P N]: a segment's own state, then its start
@@ -226,15 +227,14 @@ void scan_k(ScanArgs a, ScanPlan plan) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane % 16, q = lane / 16;
   // Unit u on XCD u % 8 (workgroup i runs on XCD i % 8): a unit's workgroups share an
-  // L2.  Items without work come at the end of each sequence, so an XCD takes another
-  // group in each item.
+  // L2, and with eight groups (or a multiple) so do a group's segments and their states.
   const int k8 = blockIdx.x / kXcds, u8 = fdiv(k8, plan.fnb);
   const int unit = u8 * kXcds + blockIdx.x % kXcds, blk = k8 - u8 * plan.nb;
   if (unit >= plan.units) return;
-  const int item = fdiv(unit, plan.fG), g = fmod_(unit + item, plan.fG);
+  const int item = fdiv(unit, plan.fG), g = unit - item * a.G;
   const int Hg = a.H / a.G, P = a.P, N = a.N;
 
-  int seq, begin, len, t_first = 0, t_end;
+  int seq, begin, len, t_first = 0, t_end, before = 0;  // before: own states to add up first
   if constexpr (MODE == kAll) {
     seq = item;
     begin = clamp_start(a.p, seq);
@@ -245,6 +245,7 @@ void scan_k(ScanArgs a, ScanPlan plan) {
     seq = it.seq, begin = it.begin, len = it.len;
     t_first = it.index * plan.seg;
     if (it.index < 0 || (it.index > 0 && t_first >= len)) return;
+    if (MODE == kFrom && plan.adds) before = it.index;
     t_end = min(len, t_first + plan.seg);
     if (MODE == kOwn && t_end == len) return;  // nothing starts from the last segment's state
   }
@@ -273,7 +274,7 @@ void scan_k(ScanArgs a, ScanPlan plan) {
   const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt0 + r) * N + 4 * q;
   const size_t states = (size_t)a.H * P * N;
   bool split = false;
-  if constexpr (MODE == kFrom) split = len > plan.seg;
+  if constexpr (MODE == kFrom) split = len > plan.seg && !plan.adds;
   const bool known = a.initial && (!a.p.resume || a.p.resume[seq]);
   const float *from = nullptr;
   if constexpr (MODE != kOwn) from = split ? plan.state + item * states : known ? a.initial + row * states : nullptr;
@@ -287,6 +288,22 @@ void scan_k(ScanArgs a, ScanPlan plan) {
         S[nt][pt] = floatx4{v.x, v.y, v.z, v.w};
       }
     }
+
+  if constexpr (MODE == kFrom) {
+    for (int j = item - before; j < item; ++j) {
+      const float d = plan.decay[(size_t)j * a.H + h];
+      const float *own = plan.state + j * states + tile0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pt = 0; pt < CT; ++pt)
+          if (16 * nt < N && pt < np) {
+            const float4 v = ld4(own + (size_t)16 * pt * N + 16 * nt);
+            floatx4 &s = S[nt][pt];
+            s = floatx4{fmaf(s[0], d, v.x), fmaf(s[1], d, v.y), fmaf(s[2], d, v.z), fmaf(s[3], d, v.w)};
+          }
+    }
+  }
 
   // Global to registers through buffers that end with the chunk's last row: rows
   // past it read as zeros, and so do the columns of threads without a place.
@@ -732,6 +749,10 @@ ScanPlan make_plan(const ScanArgs &a) {
   const int seg = ((a.p.tokens + want - 1) / want + 63) / 64 * 64;
   p.seg = a.p.n >= want || seg >= a.p.tokens ? 0 : seg < 128 ? 128 : seg;
   if (p.seg >= a.p.tokens) p.seg = 0;
+  // A few segments add up the own states before them as they start, without another launch
+  // (300 tokens of 128 heads, three segments: 28 us against 37); more would keep the last
+  // one waiting (8192 tokens, eight segments: 212 us against 201).
+  p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 4;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
   p.units = p.items * a.G;
   return p;
@@ -762,7 +783,8 @@ int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
   if (!p.seg) return launch_part<R, Y, NK, kAll>(a, p, ct, st);
   const int e = launch_part<R, Y, NK, kOwn>(a, p, ct_own, st);
   if (e) return e;
-  hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
+  if (!p.adds)
+    hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
   return launch_part<R, Y, NK, kFrom>(a, p, ct, st);
 }
 
