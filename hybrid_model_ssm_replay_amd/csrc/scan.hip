@@ -706,7 +706,11 @@ void scan_k(ScanArgs a, ScanPlan plan) {
 }
 
 // Where each segment of a split sequence starts: the segment before it decays
-// that one's start and adds its own state.  One thread, four state elements.
+// that one's start and adds its own state.  One thread, four state elements.  HBM bound
+// (8192 tokens of 128 heads, 59 MB: 10.6 us); with many segments the loads' latency
+// counts, so four are under way together (4096 tokens of 16 heads: a pass of 56 us, one
+// by one 59).
+constexpr int kAhead = 4;
 __global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan, FastDiv blocks) {
   const int seq = fdiv(blockIdx.x, blocks);
   const int begin = clamp_start(a.p, seq), len = clamp_start(a.p, seq + 1) - begin;
@@ -718,12 +722,24 @@ __global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan,
   const size_t states = (size_t)a.H * PN;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.initial && (!a.p.resume || a.p.resume[seq])) run = ld4(a.initial + row * states + e);
-  for (int i = 0; i < n; ++i) {
-    float *at = plan.state + (item0 + i) * states + e;
-    const float d = i + 1 < n ? plan.decay[(size_t)(item0 + i) * a.H + h] : 0.f;
-    const float4 own = i + 1 < n ? ld4(at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    st4(at, run);
-    run = make_float4(fmaf(run.x, d, own.x), fmaf(run.y, d, own.y), fmaf(run.z, d, own.z), fmaf(run.w, d, own.w));
+  float *const at = plan.state + item0 * states + e;
+  const float *const decay = plan.decay + (size_t)item0 * a.H + h;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float4 own[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = min(i0 + i, n - 2);  // the last segment has no own state
+      own[i] = ld4(at + j * states);
+      d[i] = decay[(size_t)j * a.H];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= n) break;
+      st4(at + (i0 + i) * states, run);
+      run = make_float4(fmaf(run.x, d[i], own[i].x), fmaf(run.y, d[i], own[i].y), fmaf(run.z, d[i], own[i].z),
+                        fmaf(run.w, d[i], own[i].w));
+    }
   }
 }
 
@@ -750,12 +766,15 @@ ScanPlan make_plan(const ScanArgs &a) {
   // tokens of five sequences: 99 us against 104, 4096 of nine: 93 against 99).
   const int want = (512 + per - 1) / per, whole = max(want - a.p.n / 2, 1);
   const int seg = ((a.p.tokens + whole - 1) / whole + 63) / 64 * 64;
-  p.seg = a.p.n >= want || seg >= a.p.tokens ? 0 : seg < 128 ? 128 : seg;
+  // Below 128 tokens a segment costs more than it saves, and up to 256 tokens so do two
+  // launches (150 tokens of 128 heads: 21 us whole, 25 split; 300: 30 and 28).
+  p.seg = a.p.n >= want || seg >= a.p.tokens || a.p.tokens <= 256 ? 0 : seg < 128 ? 128 : seg;
   if (p.seg >= a.p.tokens) p.seg = 0;
-  // A few segments add up the own states before them as they start, without another launch
-  // (300 tokens of 128 heads, three segments: 28 us against 37); more would keep the last
-  // one waiting (8192 tokens, eight segments: 212 us against 201).
-  p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 4;
+  // A few segments add up the own states before them as they start, without combine_k's
+  // launch (300 tokens of 128 heads, three segments: 28 us against 37; 5000 of six
+  // sequences, at most six: 144 against 155); more would keep the last one waiting (8192
+  // tokens, eight: 212 against 201).
+  p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 6;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
   p.units = p.items * a.G;
   return p;
