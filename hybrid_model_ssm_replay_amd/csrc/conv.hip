@@ -8,6 +8,8 @@
 // issues the loads of several tokens (a prompt) or batch rows (a step) at a time:
 // that is what keeps enough bytes under way, and in a step it also shares the
 // weights, which are as large as a row's inputs and outputs together.
+// With 10240 channels, 4 taps, bf16: a prompt of 8192 tokens moves 336 MB in 72 us (4.7
+// TB/s; a large copy reaches 5.1), a step of 256 rows 31 MB in 11 us.
 #include "ops.h"
 
 namespace rssm {
@@ -23,7 +25,7 @@ struct Taps {
 
 // The workgroup's taps go through LDS: a thread's own lie 16 V K bytes from its
 // neighbour's, so reading them directly would touch eight times the lines (a step
-// of 256 rows: XXX us so, XXX directly).  Granules of 16 bytes are permuted so that
+// of 256 rows: 12.1 us so, 14.5 directly).  Granules of 16 bytes are permuted so that
 // neither side meets a bank twice.  Every thread of the workgroup takes part.
 template <int V, int K>
 struct TapsLds {
@@ -330,24 +332,21 @@ void launch_step(const ShortConvArgs &a, int per, hipStream_t st) {
                      st, a, make_fastdiv((uint32_t)per));
 }
 
-// Tokens of a prompt tile: the fewest, in steps of 8, whose workgroups the card
-// holds at once (four of 128 registers a CU), so that none waits for a second round.
-int tile_of(const ShortConvArgs &a, int per) {
-  const int64_t items = 4 * 256 / per - a.p.n;
-  const int64_t t = items > 0 ? (a.p.tokens + items - 1) / items : 1 << 20;
-  return (int)(t < 16 ? 16 : t > 128 ? 128 : (t + 7) / 8 * 8);
-}
+// Tokens of a prompt tile: short enough for many workgroups, so that those of uneven
+// sequences end together; a tile reads K - 1 of its predecessor's rows once more, mostly
+// from L2 (16384 tokens of 10240 channels, bf16: 142 us with 12 to 24, 156 with 64).
+constexpr int kTile = 24;
 
 template <typename T, int V, int K>
 int launch(ShortConvArgs a, bool prompt, hipStream_t st) {
   const int per = (a.C + kThreads * V - 1) / (kThreads * V);
-  if (prompt) a.T = tile_of(a, per);
+  if (prompt) a.T = kTile;
   const int64_t rows = prompt ? items_of(a.p.tokens, a.p.n, a.T) : a.batch;
   if (rows * per > 0x7fffffffLL) return (int)hipErrorInvalidValue;
   if (prompt) {
     hipLaunchKernelGGL((short_conv_prompt_k<T, V, K>), dim3((uint32_t)(rows * per)), dim3(kThreads), 0, st, a,
                        make_fastdiv((uint32_t)per));
-  } else if (rows * per >= 1024) {  // two rows a thread still leave two workgroups a CU
+  } else if (rows * per >= 1024) {  // two rows a thread still leave two workgroups a CU (256 rows: 11.0 us, one by one 12.4)
     launch_step<T, V, K, 2>(a, per, st);
   } else {
     launch_step<T, V, K, 1>(a, per, st);

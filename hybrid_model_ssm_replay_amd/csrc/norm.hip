@@ -8,6 +8,8 @@
 // eight) while the squares are added up: one pass over the data.  Groups of up to
 // 128 values share a wave four at a time, longer ones have a wave; a wave takes
 // several tokens of one group, which share the weights in its registers.
+// 8192 tokens of 8192 channels, bf16: 403 MB in 79 us, as fast as a large copy (5.1
+// TB/s).  256 tokens with float32 y: 17 MB in 4.6 us, bound by the launch's start and end.
 #include "ops.h"
 
 namespace rssm {
@@ -79,7 +81,8 @@ __global__ __launch_bounds__(kThreads) void gated_norm_k(replay_gated_norm_args 
   }
 }
 
-// Longer groups: one workgroup a group of one token, two passes.
+// Longer groups: one workgroup a group of one token, two passes (the second reads what
+// the first left in L2).
 template <typename TY, typename TZ, typename TO>
 __global__ __launch_bounds__(kThreads) void gated_norm_long_k(replay_gated_norm_args a, FastDiv groups) {
   __shared__ float part[kWaves];
@@ -118,8 +121,10 @@ template <typename TY, typename TZ, typename TO, int LANES, int IT>
 int launch_fast(const replay_gated_norm_args &a, hipStream_t st) {
   constexpr int PER = kWave / LANES;
   const int groups = a.channels / a.group, sets = (groups + PER - 1) / PER;
-  // Four tokens a wave once that still leaves sixteen waves a CU.
-  const int tok = (int64_t)a.tokens * sets >= 4 * 16 * 256 ? 4 : 1;
+  // Two tokens a wave share its weights once that leaves 32 waves a CU (8192 channels in
+  // groups of 1024, bf16: 4096 tokens 34 us, one by one 35, by fours 36; 1024 tokens one
+  // by one 12.2, by twos 12.5).
+  const int tok = (int64_t)a.tokens * sets >= 2 * 32 * 256 ? 2 : 1;
   const int64_t items = (int64_t)((a.tokens + tok - 1) / tok) * sets;
   hipLaunchKernelGGL((gated_norm_k<TY, TZ, TO, LANES, IT>), dim3((uint32_t)((items + kWaves - 1) / kWaves)), dim3(kThreads), 0,
                      st, a, sets, make_fastdiv((uint32_t)sets), tok);

@@ -11,11 +11,12 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool dtype_ok(int d) { return d == REPLAY_DT_F32 || d == REPLAY_DT_BF16; }
 size_t elem_size(int d) { return d == REPLAY_DT_BF16 ? 2 : 4; }
 bool elem_aligned(const void *p, int d) { return ((uintptr_t)p & (elem_size(d) - 1)) == 0; }
+constexpr int kMost = 1 << 30;  // tokens, sequences, vocabulary: indexes a little past them still fit 32 bits
 int hip_status(int e) { return e == 0 ? REPLAY_OK : REPLAY_EHIP; }
 
 bool prompt_ok(const replay_prompt *p, int batch) {
-  return p && p->tokens >= 0 && p->sequences >= 1 && p->sequences <= batch && p->seq_start &&
-         (int64_t)p->tokens + p->sequences <= 0x7fffffffLL;
+  return p && p->tokens >= 0 && p->tokens <= kMost && p->sequences >= 1 && p->sequences <= batch &&
+         p->sequences <= kMost && p->seq_start;
 }
 
 Packed packed_of(const replay_prompt &p, int batch) {
@@ -92,7 +93,7 @@ int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt 
 }
 
 size_t replay_scan_workspace_bytes(const replay_config *cfg, int32_t tokens, int32_t sequences) {
-  if (!scan_cfg_ok(cfg) || tokens < 0 || sequences < 1 || sequences > cfg->batch) return 0;
+  if (!scan_cfg_ok(cfg) || tokens < 0 || tokens > kMost || sequences < 1 || sequences > cfg->batch || sequences > kMost) return 0;
   return scan_workspace(scan_args(*cfg, tokens, sequences));
 }
 
@@ -132,11 +133,11 @@ int replay_gated_norm(const replay_gated_norm_args *a, void *stream) {
 }
 
 size_t replay_accept_workspace_bytes(int32_t batch, int32_t vocab) {
-  return batch < 1 || vocab < 1 ? 0 : accept_workspace(batch, vocab);
+  return batch < 1 || vocab < 1 || vocab > kMost ? 0 : accept_workspace(batch, vocab);
 }
 
 int replay_accept_drafts(const replay_accept_args *a, void *workspace, void *stream) {
-  if (!a || a->batch < 1 || a->vocab < 1 || a->drafts < 0 || a->drafts > (1 << 20) || a->reserved) return REPLAY_EINVAL;
+  if (!a || a->batch < 1 || a->vocab < 1 || a->vocab > kMost || a->drafts < 0 || a->drafts > (1 << 20) || a->reserved) return REPLAY_EINVAL;
   if (!dtype_ok(a->target_dtype) || !a->target || !elem_aligned(a->target, a->target_dtype)) return REPLAY_EINVAL;
   if (a->draft && (!dtype_ok(a->draft_dtype) || !elem_aligned(a->draft, a->draft_dtype))) return REPLAY_EINVAL;
   if ((a->drafts && !a->tokens) || !a->uniforms || !a->accepted || !a->next) return REPLAY_EINVAL;

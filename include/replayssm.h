@@ -346,8 +346,8 @@ int replay_record_slots(const replay_ctx *ctx, int32_t *slots, void *stream);
 #define REPLAY_DT_BF16 1
 
 /* Sequences of several prompts, packed one after the other.
- *   tokens     rows of the packed arrays (0 allowed).
- *   sequences  prompts in this call, 1..batch.
+ *   tokens     rows of the packed arrays, 0..2^30.
+ *   sequences  prompts in this call, 1..batch, at most 2^30.
  *   seq_start  device int32 [sequences + 1], non-decreasing, within 0..tokens:
  *              sequence i is rows seq_start[i] .. seq_start[i + 1] - 1 (it may
  *              be empty).  Values are clamped into that range, never followed
@@ -487,7 +487,7 @@ int replay_gated_norm(const replay_gated_norm_args *args, void *stream);
 typedef struct replay_accept_args {
   int32_t batch;
   int32_t drafts; /* 0 .. 2^20: 0 draws from p_0 */
-  int32_t vocab;
+  int32_t vocab;  /* 1 .. 2^30 */
   int32_t target_dtype;
   int32_t draft_dtype;
   int32_t reserved;

@@ -128,6 +128,20 @@ def test_python_wrappers_refuse_host_tensors(B):
         ops.accept_drafts(torch.zeros(1, 2, dtype=torch.int32), f(1, 3, 9), f(1, 3))
 
 
+def test_extents_past_32_bit_indexes_are_refused(B):
+    """2^30 tokens, sequences or words of a vocabulary is the most: offsets a little past it still fit."""
+    most = 1 << 30
+    for tokens, n in ((most + 1, 1), (5, most + 1)):
+        p = B.replay_prompt(tokens, n, P16, 0, 0, 0)
+        _refused(B, lambda: B.replay_short_conv_prompt(_conv(B, batch=n), p, P16, 48, [P16] * 3, 0))
+        cfg = B.make_config(0, n, 1, 1, 16, 16, 1)
+        _refused(B, lambda: B.replay_scan_prompt(cfg, p, B.make_record(P16, P16, P16, P16), P16, P16, 0, P16, P16, B.DT_F32, P16, 0))
+        assert B.replay_scan_workspace_bytes(cfg, tokens, n) == 0
+    assert B.replay_accept_workspace_bytes(1, most) > 0 and B.replay_accept_workspace_bytes(1, most + 1) == 0
+    args = B.replay_accept_args(1, 1, most + 1, 0, 0, 0, 0, 0, 0, 0, P16, 0, P16, 0, P16, P16, P16)
+    _refused(B, lambda: B.replay_accept_drafts(args, P16, 0))
+
+
 def test_packed_structs_have_the_librarys_sizes(B):
     """The Python functions pass the structs as packed bytes: as long as the C ones, field by field as ctypes lays them out."""
     import ctypes
