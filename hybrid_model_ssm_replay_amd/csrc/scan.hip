@@ -23,12 +23,25 @@
 // operand M of M x.  B^T and x^T operands come from row-major LDS tiles by the
 // transposing LDS read (lane l gets column l % 16 of rows 4 (l / 16) .. + 3).
 //
+// Few long sequences are cut into segments that fill the card, in three steps:
+// each segment's own state from zero (scan_k, kOwn), the states that segments
+// start from (combine_k, or the segments themselves), the outputs (kFrom).
+//
 // Precision.  bf16 records enter the products as they are, float32 records as
 // three bf16 pieces (their sum is the value; products of pieces below 2^-24 are
 // dropped).  The weighted inputs of the state update are always three pieces:
 // the state stays float32.  M and S in the output products are three pieces for
 // float32 outputs, and one bf16 for bf16 outputs: 2^-9 of each term on average
-// next to the output's own 2^-9.
+// next to the output's own 2^-9.  The diagonal tiles of M, which also carry D,
+// are two pieces there: a sequence's first outputs consist of them alone.
+//
+// What bounds it is instruction issue.  A chunk of 64 tokens costs a wave 160
+// matrix products (240 with float32 outputs) and 900 (1400) other vector
+// operations, and two waves a SIMD, all that the registers hold, issue one of
+// those about every 4.5 cycles; the matrix pipe is a third busy, the clock near 2.0
+// GHz under this load.  128 heads of 64, states of 128, bf16: one prompt of 8192
+// tokens 190 us (own states 60, combine_k 10, outputs 120; 0.3 GB would take 60 us),
+// 24 prompts of 16384 tokens with float32 outputs 400 us (1.1 GB, 211 us).
 #include "ops.h"
 
 namespace rssm {
