@@ -187,7 +187,6 @@ __device__ __forceinline__ void interleave() {
 struct ScanPlan {
   int seg;        // tokens of a segment (a multiple of 64), or 0: sequences are not split
   int items;      // segments of all sequences
-  int ct;         // 16-column tiles of a wave
   int hw, wph;    // heads of a workgroup, waves of a head in it
   int parts;      // workgroups a head's columns are spread over (then hw is 1)
   int nb;         // workgroups of a group
@@ -219,7 +218,7 @@ struct Shape_ {
   static constexpr int G0 = SC0, SC1 = G0 + (OUT ? TILES * kWave * 16 : 0);
   static constexpr int lds(int heads) { return SC1 + heads * SC; }
   // Waves a SIMD: as many as the tiles of one and the registers of the other allow.
-  static constexpr int WAVES = CT == 2 ? 2 : OUT ? 3 : 4;
+  static constexpr int WAVES = CT == 2 ? 2 : 4;
 };
 
 template <typename R, typename Y, int NK, int CT, int MODE>
@@ -759,7 +758,6 @@ __global__ __launch_bounds__(kThreads) void combine_k(ScanArgs a, ScanPlan plan,
 // The workgroups of an item with ct tiles a wave.
 void set_tiles(const ScanArgs &a, ScanPlan &p, int ct) {
   const int Hg = a.H / a.G, waves = (a.P / 16 + ct - 1) / ct;  // of a head
-  p.ct = ct;
   p.parts = (waves + kWaves - 1) / kWaves;
   p.wph = (waves + p.parts - 1) / p.parts;
   p.hw = kWaves / p.wph < Hg ? kWaves / p.wph : Hg;
@@ -795,16 +793,13 @@ ScanPlan make_plan(const ScanArgs &a) {
 
 size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.items * a.H * 4 + 255) / 256 * 256; }
 
-template <typename R, typename Y, int NK, int MODE>
-int launch_part(const ScanArgs &a, ScanPlan p, int ct, hipStream_t st) {
-  set_tiles(a, p, ct);
+template <typename R, typename Y, int NK, int CT, int MODE>
+int launch_part(const ScanArgs &a, ScanPlan p, hipStream_t st) {
+  set_tiles(a, p, CT);
   const int64_t blocks = ((int64_t)p.units + kXcds - 1) / kXcds * kXcds * p.nb;
   if (blocks > 0x7fffffffLL) return (int)hipErrorInvalidValue;
-  const dim3 grid((uint32_t)blocks), block(kThreads);
-  if (ct == 1)
-    hipLaunchKernelGGL((scan_k<R, Y, NK, 1, MODE>), grid, block, (Shape_<R, Y, NK, 1, MODE>::lds(p.hw)), st, a, p);
-  else
-    hipLaunchKernelGGL((scan_k<R, Y, NK, 2, MODE>), grid, block, (Shape_<R, Y, NK, 2, MODE>::lds(p.hw)), st, a, p);
+  hipLaunchKernelGGL((scan_k<R, Y, NK, CT, MODE>), dim3((uint32_t)blocks), dim3(kThreads), (Shape_<R, Y, NK, CT, MODE>::lds(p.hw)),
+                     st, a, p);
   return (int)hipGetLastError();
 }
 
@@ -812,15 +807,14 @@ template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
   if ((int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  if (!p.seg) return launch_part<R, Y, NK, 2, kAll>(a, p, st);
   // Own states of float32 records: half the columns leave LDS for four workgroups a CU
   // (2048 tokens of 64 heads: 100 us a pass against 109).
-  const int ct = 2, ct_own = sizeof(R) == 4 ? 1 : 2;
-  if (!p.seg) return launch_part<R, Y, NK, kAll>(a, p, ct, st);
-  const int e = launch_part<R, Y, NK, kOwn>(a, p, ct_own, st);
+  const int e = launch_part<R, Y, NK, sizeof(R) == 4 ? 1 : 2, kOwn>(a, p, st);
   if (e) return e;
   if (!p.adds)
     hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
-  return launch_part<R, Y, NK, kFrom>(a, p, ct, st);
+  return launch_part<R, Y, NK, 2, kFrom>(a, p, st);
 }
 
 template <typename R, typename Y>
