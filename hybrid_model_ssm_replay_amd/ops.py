@@ -81,9 +81,11 @@ def _status(status, at) -> int:
 
 def _short_conv(x, weight, ring, pos, widths, bias, activation, status, dims):
     at = _vectors(x, "x", dims)
-    C = x.shape[-1]
-    w3 = (*widths, 0, 0)[:3]
-    if not 1 <= len(widths) <= 3 or sum(w3) != C or min(w3) < 0:
+    shape = x.shape
+    C = shape[-1]
+    parts = len(widths)
+    w0, w1, w2 = (*widths, 0, 0)[:3] if 0 < parts < 3 else widths if parts == 3 else (-1, 0, 0)
+    if w0 < 0 or w1 < 0 or w2 < 0 or w0 + w1 + w2 != C:
         raise ValueError(f"widths {tuple(widths)} must be one to three extents that add up to {C} channels")
     if activation not in ("silu", None):
         raise ValueError(f"unknown activation {activation!r}")
@@ -93,14 +95,22 @@ def _short_conv(x, weight, ring, pos, widths, bias, activation, status, dims):
         raise ValueError("ring must be [slots, batch, channels], on the device")
     taps = weight.shape[1]
     slots, batch, _ = ring.shape
-    conv = _CONV(C, taps, slots, batch, _DT[x.dtype], 1 if activation else 0, *w3, 0,
+    dtype = x.dtype
+    conv = _CONV(C, taps, slots, batch, _DT[dtype], 1 if activation else 0, w0, w1, w2, 0,
                  _check(weight, "weight", _F32, (C, taps), at),
                  0 if bias is None else _check(bias, "bias", _F32, (C,), at),
-                 _check(ring, "ring", x.dtype, (slots, batch, C), at),
-                 0 if pos is None else _check(pos, "pos", _I32, (batch,), at), _status(status, at))
-    lead = x.shape[:-1]
-    outs = [torch.empty((*lead, w), dtype=x.dtype, device=x.device) for w in widths]
-    return at, conv, batch, outs, ([o.data_ptr() for o in outs] + [0, 0])[:3]
+                 _check(ring, "ring", dtype, (slots, batch, C), at),
+                 0 if pos is None else _check(pos, "pos", _I32, (batch,), at),
+                 0 if status is None else _status(status, at))
+    empty = x.new_empty
+    if dims == 3:
+        n, T, _ = shape
+        outs = [empty(n, T, w) for w in widths]
+    else:
+        n = shape[0]
+        outs = [empty(n, w) for w in widths]
+    to = [o.data_ptr() for o in outs]
+    return at, conv, batch, outs, to if parts == 3 else (to + [0, 0])[:3]
 
 
 def short_conv_step(x, weight, ring, pos, widths, *, bias=None, activation="silu", status=None):
@@ -168,8 +178,8 @@ def scan_prompt(x, Bm, Cm, dt, A, D, seq_start, state, *, initial=None, rows=Non
     prompt, n = _prompt(tokens, seq_start, rows, resume, status, at)
     cfg = _CONFIG(B.KIND_MAMBA2, batch, H, G, P, N, 1, 0, 0, 0, 0, B.FLAG_BF16_RECORDS if dtype is _BF16 else 0, 0)
     nbytes = B.replay_scan_workspace_bytes(cfg, tokens, n)
-    y = torch.empty((tokens, H, P), dtype=out_dtype, device=x.device)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    y = x.new_empty(tokens, H, P, dtype=out_dtype)
+    ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     B.replay_scan_prompt(cfg, prompt, rec, _check(A, "A", _F32, (H,), at), _check(D, "D", _F32, (H,), at), start, to,
                          y.data_ptr(), _DT[out_dtype], ws.data_ptr() if nbytes else 0, _raw_stream(at))
     return y
@@ -194,7 +204,7 @@ def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=Non
     wn = weight.shape[0] if isinstance(weight, torch.Tensor) and weight.dim() == 1 else -1
     if group < 1 or C % group or (wn != C and wn != group):
         raise ValueError(f"group {group} must divide {C} channels, and weight be [{C}] or [{group}]")
-    out = torch.empty((tokens, C), dtype=out_dtype, device=y.device)
+    out = z.new_empty(tokens, C) if out_dtype is z.dtype else z.new_empty(tokens, C, dtype=out_dtype)
     B.replay_gated_norm(_NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0,
                               eps, 0, y.stride(0), z.stride(0), C, y.data_ptr(), z.data_ptr(),
                               _check(weight, "weight", _F32, (wn,), at), out.data_ptr()), _raw_stream(at))
@@ -222,13 +232,11 @@ def accept_drafts(tokens, target, uniforms, *, draft=None, lengths=None):
             _refuse(draft, "draft", tuple(_DT), (batch, T, V))
         ds, q, qt = draft.stride(), draft.data_ptr(), _DT[draft.dtype]
     ts = target.stride()
-    device = target.device
-    accepted = torch.empty(batch, dtype=_I32, device=device)
-    following = torch.empty(batch, dtype=_I32, device=device)
-    ws = torch.empty(B.replay_accept_workspace_bytes(batch, V), dtype=torch.uint8, device=device)
+    drafts = _check(tokens, "tokens", _I32, (batch, T), at)
+    accepted, following = tokens.new_empty(batch), tokens.new_empty(batch)
+    ws = target.new_empty(B.replay_accept_workspace_bytes(batch, V), dtype=torch.uint8)
     args = _ACCEPT(batch, T, V, _DT[target.dtype], qt, 0, ts[0], ts[1], ds[0], ds[1],
-                   _check(tokens, "tokens", _I32, (batch, T), at),
-                   0 if lengths is None else _check(lengths, "lengths", _I32, (batch,), at), target.data_ptr(), q,
+                   drafts, 0 if lengths is None else _check(lengths, "lengths", _I32, (batch,), at), target.data_ptr(), q,
                    _check(uniforms, "uniforms", _F32, (batch, T + 1), at), accepted.data_ptr(), following.data_ptr())
     B.replay_accept_drafts(args, ws.data_ptr(), _raw_stream(at))
     return accepted, following
