@@ -260,6 +260,22 @@ def test_scan_prompt(H, G, P, N, lens, resumed, name, out):
         assert bool((state[b] == 5).all())
 
 
+@pytest.mark.parametrize("H,G,P,N,lens,resumed,name,out", [
+    # A token around each length at which a prompt is cut, and pieces of exactly that length.
+    (2, 1, 64, 128, [256], "all", "bf16", "bf16"),
+    (2, 1, 64, 128, [257], [1], "bf16", "f32"),
+    (2, 1, 64, 128, [384], "all", "bf16", "bf16"),
+    (2, 1, 64, 128, [385], None, "f32", "f32"),
+    (4, 2, 48, 64, [768], [1], "bf16", "bf16"),        # six segments add up their starts
+    (4, 2, 48, 64, [769], [1], "bf16", "bf16"),        # seven: the states are combined apart
+    (4, 2, 64, 128, [1000, 3, 400, 0, 128, 129], [1, 0, 0, 1, 1, 0], "bf16", "bf16"),
+    (2, 2, 128, 16, [600, 130, 256], [0, 1, 1], "f32", "f32"),
+    (64, 8, 64, 128, [640, 130], "all", "bf16", "f32"),
+])
+def test_scan_prompt_around_its_cuts(H, G, P, N, lens, resumed, name, out):
+    test_scan_prompt(H, G, P, N, lens, resumed, name, out)
+
+
 def test_scan_prompt_long_steps_and_fast_decay():
     """Heads whose decay over one token underflows, and heads that hardly decay."""
     import torch
