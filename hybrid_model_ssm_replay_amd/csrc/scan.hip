@@ -259,7 +259,12 @@ void scan_k(ScanArgs a, ScanPlan plan) {
     if (it.index < 0 || (it.index > 0 && t_first >= len)) return;
     if (MODE == kFrom && plan.adds) before = it.index;
     t_end = min(len, t_first + plan.seg);
-    if (MODE == kOwn && t_end == len) return;  // nothing starts from the last segment's state
+    // Nothing starts from the last segment's state.  Its place keeps where the sequence
+    // starts if segments add up for themselves: kFrom may write over `initial`.
+    if (MODE == kOwn && t_end == len) {
+      if (!plan.adds || it.index == 0) return;
+      t_end = t_first;
+    }
   }
   const int row = batch_row(a.p, seq, g == 0 && blk == 0 && tid == 0 && MODE != kOwn && t_first == 0);
   if (row < 0) return;
@@ -285,11 +290,11 @@ void scan_k(ScanArgs a, ScanPlan plan) {
   floatx4 S[NT][CT];
   const size_t tile0 = (size_t)h * P * N + (size_t)(16 * pt0 + r) * N + 4 * q;
   const size_t states = (size_t)a.H * P * N;
-  bool split = false;
-  if constexpr (MODE == kFrom) split = len > plan.seg && !plan.adds;
   const bool known = a.initial && (!a.p.resume || a.p.resume[seq]);
-  const float *from = nullptr;
-  if constexpr (MODE != kOwn) from = split ? plan.state + item * states : known ? a.initial + row * states : nullptr;
+  const float *from = known && (MODE != kOwn || t_end == t_first) ? a.initial + row * states : nullptr;
+  if constexpr (MODE == kFrom) {
+    if (len > plan.seg) from = plan.state + (plan.adds ? item - before + (len - 1) / plan.seg : item) * states;
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

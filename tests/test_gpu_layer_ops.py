@@ -318,6 +318,25 @@ def test_scan_prompt_in_place_continues(name, cuts):
     _near(_values(state[0]), S, _scan_bars(Sa, n, N, name, "f32") * Sa + 1e-37)
 
 
+@pytest.mark.parametrize("G,lens", [(8, (1400, 100, 1500)), (1, (900, 1100, 30, 970)), (8, (8000,))])
+def test_scan_prompt_in_place_is_bit_equal_where_segments_outnumber_the_card(G, lens):
+    """Segments that read where their sequence starts must not meet the state that its last one leaves."""
+    import torch
+    from hybrid_model_ssm_replay_amd import ops
+    announce("scan_prompt in place, wide", G, lens)
+    torch.manual_seed(3)
+    H, P, N, n = 128, 64, 128, sum(lens)
+    rand = lambda *s: torch.randn(s, device="cuda").to(torch.bfloat16)  # noqa: E731
+    x, Bm, Cm, dt = rand(n, H, P), rand(n, G, N), rand(n, G, N), torch.rand(n, H, device="cuda") * 0.01
+    A, D = -torch.rand(H, device="cuda"), torch.randn(H, device="cuda")
+    seq = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    start = torch.randn(len(lens), H, P, N, device="cuda")
+    apart, place = torch.empty_like(start), start.clone()
+    y0 = ops.scan_prompt(x, Bm, Cm, dt, A, D, seq, apart, initial=start)
+    y1 = ops.scan_prompt(x, Bm, Cm, dt, A, D, seq, place, initial=place)
+    assert torch.equal(y0, y1) and torch.equal(apart, place)
+
+
 def test_scan_prompt_bad_values_stay_in_their_sequence():
     import torch
     from hybrid_model_ssm_replay_amd import ops
