@@ -40,7 +40,7 @@
 // operations, and two waves a SIMD, all that the registers hold, issue one of
 // those about every 4.5 cycles; the matrix pipe is a third busy, the clock near 2.0
 // GHz under this load.  128 heads of 64, states of 128, bf16: one prompt of 8192
-// tokens 190 us (own states 60, combine_k 10, outputs 120; 0.3 GB would take 60 us),
+// tokens 193 us (own states 61, combine_k 10, outputs 120; 0.3 GB would take 60 us),
 // 24 prompts of 16384 tokens with float32 outputs 400 us (1.1 GB, 211 us).
 #include "ops.h"
 
@@ -783,14 +783,13 @@ ScanPlan make_plan(const ScanArgs &a) {
   const int want = (512 + per - 1) / per, whole = max(want - a.p.n / 2, 1);
   const int seg = ((a.p.tokens + whole - 1) / whole + 63) / 64 * 64;
   // Below 128 tokens a segment costs more than it saves, and up to 256 tokens so do two
-  // launches (150 tokens of 128 heads: 21 us whole, 25 split; 300: 30 and 28).
+  // launches (150 tokens of 128 heads: 21 us whole, 25 split; 300: 31 and 30).
   p.seg = a.p.n >= want || seg >= a.p.tokens || a.p.tokens <= 256 ? 0 : seg < 128 ? 128 : seg;
   if (p.seg >= a.p.tokens) p.seg = 0;
   // A few segments add up the own states before them as they start, without combine_k's
-  // launch (300 tokens of 128 heads, three segments: 28 us against 37; 5000 of six
-  // sequences, at most six: 144 against 155); more would keep the last one waiting (8192
-  // tokens, eight: 212 against 201).
-  p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 6;
+  // launch (300 tokens of 128 heads, three segments: 30 us against 38); more would keep the
+  // last one waiting (600 tokens, five: 48 against 46; 8192, eight: 212 against 201).
+  p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 4;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
   p.units = p.items * a.G;
   return p;

@@ -266,8 +266,10 @@ def test_scan_prompt(H, G, P, N, lens, resumed, name, out):
     (2, 1, 64, 128, [257], [1], "bf16", "f32"),
     (2, 1, 64, 128, [384], "all", "bf16", "bf16"),
     (2, 1, 64, 128, [385], None, "f32", "f32"),
-    (4, 2, 48, 64, [768], [1], "bf16", "bf16"),        # six segments add up their starts
-    (4, 2, 48, 64, [769], [1], "bf16", "bf16"),        # seven: the states are combined apart
+    (4, 2, 48, 64, [512], [1], "bf16", "bf16"),        # four segments add up their starts
+    (4, 2, 48, 64, [513], [1], "bf16", "bf16"),        # five: the states are combined apart
+    (4, 2, 48, 64, [768], [1], "bf16", "bf16"),
+    (4, 2, 48, 64, [769], [1], "bf16", "bf16"),
     (4, 2, 64, 128, [1000, 3, 400, 0, 128, 129], [1, 0, 0, 1, 1, 0], "bf16", "bf16"),
     (2, 2, 128, 16, [600, 130, 256], [0, 1, 1], "f32", "f32"),
     (64, 8, 64, 128, [640, 130], "all", "bf16", "f32"),
@@ -318,7 +320,8 @@ def test_scan_prompt_in_place_continues(name, cuts):
     _near(_values(state[0]), S, _scan_bars(Sa, n, N, name, "f32") * Sa + 1e-37)
 
 
-@pytest.mark.parametrize("G,lens", [(8, (1400, 100, 1500)), (1, (900, 1100, 30, 970)), (8, (8000,))])
+@pytest.mark.parametrize("G,lens", [(8, (1400, 100, 1500)), (1, (900, 1100, 30, 970)), (8, (8000,)), (8, (700, 90)),
+                                    (8, (6000, 100, 2500, 3000))])
 def test_scan_prompt_in_place_is_bit_equal_where_segments_outnumber_the_card(G, lens):
     """Segments that read where their sequence starts must not meet the state that its last one leaves."""
     import torch
