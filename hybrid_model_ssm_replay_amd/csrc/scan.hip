@@ -217,8 +217,9 @@ struct Shape_ {
   static constexpr int SC = 6 * Q * 4;  // per head: six values a token
   static constexpr int G0 = SC0, SC1 = G0 + (OUT ? TILES * kWave * 16 : 0);
   static constexpr int lds(int heads) { return SC1 + heads * SC; }
-  // Waves a SIMD: as many as the tiles of one and the registers of the other allow.
-  static constexpr int WAVES = CT == 2 ? 2 : 4;
+  // Waves a SIMD: as many as registers (outputs, 32 columns) and tiles allow; kernels of 16
+  // columns with outputs run where there are few workgroups.
+  static constexpr int WAVES = CT == 2 || OUT ? 2 : 4;
 };
 
 template <typename R, typename Y, int NK, int CT, int MODE>
@@ -782,13 +783,16 @@ ScanPlan make_plan(const ScanArgs &a) {
   // tokens of five sequences: 99 us against 104, 4096 of nine: 93 against 99).
   const int want = (512 + per - 1) / per, whole = max(want - a.p.n / 2, 1);
   const int seg = ((a.p.tokens + whole - 1) / whole + 63) / 64 * 64;
-  // Below 128 tokens a segment costs more than it saves, and up to 256 tokens so do two
-  // launches (150 tokens of 128 heads: 21 us whole, 25 split; 300: 31 and 30).
-  p.seg = a.p.n >= want || seg >= a.p.tokens || a.p.tokens <= 256 ? 0 : seg < 128 ? 128 : seg;
+  // Below 128 tokens a segment costs more than it saves, and up to 320 tokens so do two
+  // launches (300 tokens of 128 heads: 25 us whole, 28 split; 400: 39 and 32).
+  // Up to four segments add up the own states before them as they start, without
+  // combine_k's launch, and up to 768 tokens four are enough (600 tokens of 128 heads: 37
+  // us, five and combine_k 46); more would keep the last one waiting (8192 tokens, eight:
+  // 212 us against 201), and fewer of more tokens take longer (800 tokens of 32 heads,
+  // four: 33 us against 30).
+  const int least = a.p.tokens > 512 && a.p.tokens <= 768 ? 192 : 128;
+  p.seg = a.p.n >= want || seg >= a.p.tokens || a.p.tokens <= 320 ? 0 : max(seg, least);
   if (p.seg >= a.p.tokens) p.seg = 0;
-  // A few segments add up the own states before them as they start, without combine_k's
-  // launch (300 tokens of 128 heads, three segments: 30 us against 38); more would keep the
-  // last one waiting (600 tokens, five: 48 against 46; 8192, eight: 212 against 201).
   p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 4;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
   p.units = p.items * a.G;
@@ -811,14 +815,17 @@ template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
   if ((int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
-  if (!p.seg) return launch_part<R, Y, NK, 2, kAll>(a, p, st);
+  // At most one workgroup a CU: waves of half the columns, on twice as many, end sooner
+  // (200 tokens of 32 heads: 20 us against 25; 600: 28 against 34).
+  const bool few = (int64_t)p.units * p.nb <= 256;
+  if (!p.seg) return few ? launch_part<R, Y, NK, 1, kAll>(a, p, st) : launch_part<R, Y, NK, 2, kAll>(a, p, st);
   // Own states of float32 records: half the columns leave LDS for four workgroups a CU
   // (2048 tokens of 64 heads: 100 us a pass against 109).
-  const int e = launch_part<R, Y, NK, sizeof(R) == 4 ? 1 : 2, kOwn>(a, p, st);
+  const int e = sizeof(R) == 4 || few ? launch_part<R, Y, NK, 1, kOwn>(a, p, st) : launch_part<R, Y, NK, 2, kOwn>(a, p, st);
   if (e) return e;
   if (!p.adds)
     hipLaunchKernelGGL(combine_k, dim3((uint32_t)(a.p.n * per_seq)), dim3(kThreads), 0, st, a, p, make_fastdiv((uint32_t)per_seq));
-  return launch_part<R, Y, NK, 2, kFrom>(a, p, st);
+  return few ? launch_part<R, Y, NK, 1, kFrom>(a, p, st) : launch_part<R, Y, NK, 2, kFrom>(a, p, st);
 }
 
 template <typename R, typename Y>

@@ -264,6 +264,8 @@ def test_scan_prompt(H, G, P, N, lens, resumed, name, out):
     # A token around each length at which a prompt is cut, and pieces of exactly that length.
     (2, 1, 64, 128, [256], "all", "bf16", "bf16"),
     (2, 1, 64, 128, [257], [1], "bf16", "f32"),
+    (2, 1, 64, 128, [320], [1], "bf16", "f32"),
+    (2, 1, 64, 128, [321], [1], "bf16", "bf16"),
     (2, 1, 64, 128, [384], "all", "bf16", "bf16"),
     (2, 1, 64, 128, [385], None, "f32", "f32"),
     (4, 2, 48, 64, [512], [1], "bf16", "bf16"),        # four segments add up their starts
