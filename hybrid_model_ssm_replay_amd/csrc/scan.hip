@@ -32,8 +32,11 @@
 // dropped).  The weighted inputs of the state update are always three pieces:
 // the state stays float32.  M and S in the output products are three pieces for
 // float32 outputs, and one bf16 for bf16 outputs: 2^-9 of each term on average
-// next to the output's own 2^-9.  The diagonal tiles of M, which also carry D,
-// are two pieces there: a sequence's first outputs consist of them alone.
+// next to the output's own 2^-9.  Two cases have two pieces there: the diagonal
+// tiles of M, which also carry D (a sequence's first outputs consist of them
+// alone), and S where few workgroups leave the card idle (the first outputs of a
+// resumed prompt are S C above all; five tokens: error 0.0021 with one piece, and
+// with two 0.0017, the rounding of the outputs).
 //
 // What bounds it is instruction issue.  A chunk of 64 tokens costs a wave 160
 // matrix products (240 with float32 outputs) and 900 (1400) other vector
@@ -209,7 +212,8 @@ struct Shape_ {
   static constexpr int COLS = 16 * CT * kWaves;            // x columns of a workgroup
   static constexpr bool OUT = MODE != kOwn;
   static constexpr int IP = sizeof(R) == 4 ? 3 : 1;        // pieces of an input
-  static constexpr int MP = sizeof(Y) == 4 ? 3 : 1;        // pieces of M and S
+  static constexpr int MP = sizeof(Y) == 4 ? 3 : 1;        // pieces of M
+  static constexpr int SP = MP == 1 && CT == 1 ? 2 : MP;   // and of S
   static constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;  // blocks and tokens of a chunk
   static constexpr int TILES = QB * (QB + 1) / 2;
   static constexpr int RS = kRow, XS = 2 * COLS;           // bytes of a row of B and C, and of x
@@ -228,7 +232,7 @@ __attribute__((amdgpu_waves_per_eu(Shape_<R, Y, NK, CT, MODE>::WAVES, Shape_<R, 
 void scan_k(ScanArgs a, ScanPlan plan) {
   typedef Shape_<R, Y, NK, CT, MODE> Z;
   constexpr int kCols = Z::COLS;
-  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
+  constexpr int IP = Z::IP, MP = Z::MP, SP = Z::SP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
   constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
   constexpr int NV = 4 * NK, XV = kCols / 8;             // granules of a row
   constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one granule a thread
@@ -520,17 +524,17 @@ void scan_k(ScanArgs a, ScanPlan plan) {
 #pragma unroll
             for (int g = 0; g < GT; ++g) acc[g] = mfma32(gb[g][k], gc[g][k], acc[g]);
         }
-      Frag sp[NK][CT][MP];
+      Frag sp[NK][CT][SP];
       auto cut_state = [&](int k) {
 #pragma unroll
         for (int pt = 0; pt < CT; ++pt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const floatx4 &s = S[2 * k + i / 2][pt];
-            uint32_t w[MP];
-            pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
+            uint32_t w[SP];
+            pieces<SP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
 #pragma unroll
-            for (int u = 0; u < MP; ++u) sp[k][pt][u].w[i] = w[u];
+            for (int u = 0; u < SP; ++u) sp[k][pt][u].w[i] = w[u];
           }
       };
       Frag cf[2][QB];
@@ -554,14 +558,14 @@ void scan_k(ScanArgs a, ScanPlan plan) {
         if (v == IP - 1 && k + 1 < NK) cut_state(k + 1);
         if (at < KB * CT) weigh(at / CT, at % CT);
 #pragma unroll
-        for (int u = MP - 1; u >= 0; --u)
+        for (int u = SP - 1; u >= 0; --u)
           if (u + v < 3) {
 #pragma unroll
             for (int tb = 0; tb < QB; ++tb)
 #pragma unroll
               for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(sp[k][pt][u], cf[at % 2][tb], Yt[tb][pt]);
           }
-        interleave<QB * CT * (MP == 1 ? 1 : IP == 1 ? 3 : 2), MP == 1 ? 8 : 4>();
+        interleave<QB * CT * (MP == 1 ? SP : IP == 1 ? 3 : 2), MP == 1 ? 8 / SP : 4>();
       }
 #pragma unroll
       for (int i = NK * IP; i < KB * CT; ++i) weigh(i / CT, i % CT);
