@@ -31,20 +31,18 @@
 // three bf16 pieces (their sum is the value; products of pieces below 2^-24 are
 // dropped).  The weighted inputs of the state update are always three pieces:
 // the state stays float32.  M and S in the output products are three pieces for
-// float32 outputs, and one bf16 for bf16 outputs: 2^-9 of each term on average
-// next to the output's own 2^-9.  Two cases have two pieces there: the diagonal
-// tiles of M, which also carry D (a sequence's first outputs consist of them
-// alone), and S where few workgroups leave the card idle (the first outputs of a
-// resumed prompt are S C above all; five tokens: error 0.0021 with one piece, and
-// with two 0.0017, the rounding of the outputs).
+// float32 outputs and two for bf16 outputs, whatever the launch: within 2^-16 of
+// each term, next to the output's own 2^-8.  One piece there is 3 to 10 % faster and
+// leaves the outputs of a resumed batch at an error of 0.0021 where their rounding
+// is 0.0017; three pieces are up to 10 % slower than two and leave the same 0.0017.
 //
-// What bounds it is instruction issue.  A chunk of 64 tokens costs a wave 160
-// matrix products (240 with float32 outputs) and 900 (1400) other vector
+// What bounds it is instruction issue.  A chunk of 64 tokens costs a wave 196
+// matrix products (240 with float32 outputs) and 1140 (1400) other vector
 // operations, and two waves a SIMD, all that the registers hold, issue one of
-// those about every 4.5 cycles; the matrix pipe is a third busy, the clock near 2.0
-// GHz under this load.  128 heads of 64, states of 128, bf16: one prompt of 8192
-// tokens 193 us (own states 61, combine_k 10, outputs 120; 0.3 GB would take 60 us),
-// 24 prompts of 16384 tokens with float32 outputs 400 us (1.1 GB, 211 us).
+// those about every six cycles; the matrix pipe is busy 38 % of the time, the clock
+// near 2.0 GHz under this load.  128 heads of 64, states of 128, bf16: one prompt of
+// 8192 tokens 204 us (own states 61, combine_k 10, outputs 133; 0.3 GB would take 60
+// us), 24 prompts of 16384 tokens with float32 outputs 398 us (1.1 GB, 211 us).
 #include "ops.h"
 
 namespace rssm {
@@ -115,12 +113,14 @@ __device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t b, int at,
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, at, plus, 0));
 }
 
-// Two values as MP words of bf16 pairs: one piece rounds to nearest, three pieces
-// cut (8 bits each: together the 24 bits of the value).
+// Two values as MP words of bf16 pairs: two pieces round to nearest (together within
+// 2^-16 of the value), three pieces cut (8 bits each: the 24 bits of the value).
 template <int MP>
 __device__ __forceinline__ void pieces(float a, float b, uint32_t (&w)[MP]) {
-  if constexpr (MP == 1) {
+  static_assert(MP == 2 || MP == 3);
+  if constexpr (MP == 2) {
     w[0] = pack_bf16(a, b);
+    w[1] = pack_bf16(a - lower(w[0]), b - upper(w[0]));
   } else {
 #pragma unroll
     for (int u = 0; u < MP; ++u) {
@@ -212,8 +212,7 @@ struct Shape_ {
   static constexpr int COLS = 16 * CT * kWaves;            // x columns of a workgroup
   static constexpr bool OUT = MODE != kOwn;
   static constexpr int IP = sizeof(R) == 4 ? 3 : 1;        // pieces of an input
-  static constexpr int MP = sizeof(Y) == 4 ? 3 : 1;        // pieces of M
-  static constexpr int SP = MP == 1 && CT == 1 ? 2 : MP;   // and of S
+  static constexpr int MP = sizeof(Y) == 4 ? 3 : 2;        // pieces of M and S in the output products
   static constexpr int QB = IP == 3 ? 2 : 4, Q = 16 * QB;  // blocks and tokens of a chunk
   static constexpr int TILES = QB * (QB + 1) / 2;
   static constexpr int RS = kRow, XS = 2 * COLS;           // bytes of a row of B and C, and of x
@@ -232,7 +231,7 @@ __attribute__((amdgpu_waves_per_eu(Shape_<R, Y, NK, CT, MODE>::WAVES, Shape_<R, 
 void scan_k(ScanArgs a, ScanPlan plan) {
   typedef Shape_<R, Y, NK, CT, MODE> Z;
   constexpr int kCols = Z::COLS;
-  constexpr int IP = Z::IP, MP = Z::MP, SP = Z::SP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
+  constexpr int IP = Z::IP, MP = Z::MP, QB = Z::QB, Q = Z::Q, TILES = Z::TILES, RS = Z::RS, XS = Z::XS;
   constexpr int KB = QB / 2, NT = 2 * NK;                // 32-token steps, 16-column tiles of the state
   constexpr int NV = 4 * NK, XV = kCols / 8;             // granules of a row
   constexpr int RB = kThreads / NV, RX = kThreads / XV;  // rows of one granule a thread
@@ -524,17 +523,17 @@ void scan_k(ScanArgs a, ScanPlan plan) {
 #pragma unroll
             for (int g = 0; g < GT; ++g) acc[g] = mfma32(gb[g][k], gc[g][k], acc[g]);
         }
-      Frag sp[NK][CT][SP];
+      Frag sp[NK][CT][MP];
       auto cut_state = [&](int k) {
 #pragma unroll
         for (int pt = 0; pt < CT; ++pt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const floatx4 &s = S[2 * k + i / 2][pt];
-            uint32_t w[SP];
-            pieces<SP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
+            uint32_t w[MP];
+            pieces<MP>(s[i % 2 * 2], s[i % 2 * 2 + 1], w);
 #pragma unroll
-            for (int u = 0; u < SP; ++u) sp[k][pt][u].w[i] = w[u];
+            for (int u = 0; u < MP; ++u) sp[k][pt][u].w[i] = w[u];
           }
       };
       Frag cf[2][QB];
@@ -558,14 +557,14 @@ void scan_k(ScanArgs a, ScanPlan plan) {
         if (v == IP - 1 && k + 1 < NK) cut_state(k + 1);
         if (at < KB * CT) weigh(at / CT, at % CT);
 #pragma unroll
-        for (int u = SP - 1; u >= 0; --u)
+        for (int u = MP - 1; u >= 0; --u)
           if (u + v < 3) {
 #pragma unroll
             for (int tb = 0; tb < QB; ++tb)
 #pragma unroll
               for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(sp[k][pt][u], cf[at % 2][tb], Yt[tb][pt]);
           }
-        interleave<QB * CT * (MP == 1 ? SP : IP == 1 ? 3 : 2), MP == 1 ? 8 / SP : 4>();
+        interleave<QB * CT * (IP == 1 ? MP : 2), 4>();
       }
 #pragma unroll
       for (int i = NK * IP; i < KB * CT; ++i) weigh(i / CT, i % CT);
@@ -639,8 +638,7 @@ void scan_k(ScanArgs a, ScanPlan plan) {
         // M^T from G^T, and x M^T.
 #pragma unroll
         for (int k = 0; k <= tb / 2; ++k) {
-          Frag mf[MP], left;  // left: what rounding leaves of the diagonal tile
-          left.v = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+          Frag mf[MP];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int jb = 2 * k + half;
@@ -674,7 +672,6 @@ void scan_k(ScanArgs a, ScanPlan plan) {
               pieces<MP>(m[2 * i], m[2 * i + 1], w);
 #pragma unroll
               for (int u = 0; u < MP; ++u) mf[u].w[2 * half + i] = w[u];
-              if (MP == 1 && jb == tb) left.w[2 * half + i] = pack_bf16(m[2 * i] - lower(w[0]), m[2 * i + 1] - upper(w[0]));
             }
           }
 #pragma unroll
@@ -685,10 +682,6 @@ void scan_k(ScanArgs a, ScanPlan plan) {
 #pragma unroll
                 for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(xf[k][pt][v], mf[u], Yt[tb][pt]);
               }
-          if (MP == 1 && tb / 2 == k) {
-#pragma unroll
-            for (int pt = 0; pt < CT; ++pt) Yt[tb][pt] = mfma32(xf[k][pt][0], left, Yt[tb][pt]);
-          }
         }
       }
       // y: this lane holds four neighbouring channels of token 16 tb + r.

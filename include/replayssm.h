@@ -427,7 +427,8 @@ int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt 
  *              sequence: its start).  It may be `initial`, and it may be the
  *              F32 checkpoint of a layer whose windows are empty in those rows.
  *   y          [tokens][heads][P] in y_dtype (REPLAY_DT_F32; REPLAY_DT_BF16 with
- *              bf16 records only).
+ *              bf16 records only): before their rounding bf16 outputs are good
+ *              to 2^-16 of each term that they add, float32 outputs to float32.
  *   workspace  replay_scan_workspace_bytes bytes (256-byte aligned), or NULL
  *              when that is 0.
  * A NaN or infinity in one token reaches that head's later tokens, and may
