@@ -1,8 +1,9 @@
 """The operators around the recurrence, on torch tensors.
 
 Each function checks its tensors, allocates its outputs and workspace with torch
-and forwards to the library on the current stream; the arithmetic is in the HIP
-kernels.  See include/replayssm.h for the definitions.
+and forwards to the library on the current stream of its tensors' device, which
+need not be the current one; the arithmetic is in the HIP kernels.  See
+include/replayssm.h for the definitions.
 
 * ``short_conv_prompt`` / ``short_conv_step``: the short causal convolution in
   front of the recurrence, for packed prompts and for one token or T drafts.
@@ -33,6 +34,7 @@ _ACCEPT = struct.Struct("@6i4q7P").pack
 _CONFIG = struct.Struct("@10iQ2I").pack
 _RECORD = struct.Struct("@5P").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
+_device = torch._C._cuda_getDevice  # the index of the current device
 
 
 def _refuse(t, name, dtypes, shape, dense=True):
@@ -42,6 +44,16 @@ def _refuse(t, name, dtypes, shape, dense=True):
     if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
     raise ValueError(f"{name} must be contiguous" if dense else f"{name} must be dense along its last axis")
+
+
+def _launch(call, at, *args):
+    """call(*args, stream) with device `at`, the tensors', current: kernels go to the
+    current device, and the default stream's handle is the same on every one."""
+    if _device() == at:
+        call(*args, _raw_stream(at))
+    else:
+        with torch.cuda.device(at):
+            call(*args, _raw_stream(at))
 
 
 def _check(t, name, dtype, shape, at):
@@ -126,7 +138,7 @@ def short_conv_step(x, weight, ring, pos, widths, *, bias=None, activation="silu
     at, conv, batch, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 3)
     if pos is None or x.shape[0] != batch:
         raise ValueError(f"x has {x.shape[0]} rows, ring {batch}, and pos is needed")
-    B.replay_short_conv_step(conv, x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], to, _raw_stream(at))
+    _launch(B.replay_short_conv_step, at, conv, x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], to)
     return outs
 
 
@@ -142,7 +154,7 @@ def short_conv_prompt(x, weight, ring, seq_start, widths, *, bias=None, activati
     [tokens, width] tensor for each width."""
     at, conv, _, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 2)
     prompt, _ = _prompt(x.shape[0], seq_start, rows, resume, status, at)
-    B.replay_short_conv_prompt(conv, prompt, x.data_ptr(), x.stride(0), to, _raw_stream(at))
+    _launch(B.replay_short_conv_prompt, at, conv, prompt, x.data_ptr(), x.stride(0), to)
     return outs
 
 
@@ -180,8 +192,8 @@ def scan_prompt(x, Bm, Cm, dt, A, D, seq_start, state, *, initial=None, rows=Non
     nbytes = B.replay_scan_workspace_bytes(cfg, tokens, n)
     y = x.new_empty(tokens, H, P, dtype=out_dtype)
     ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
-    B.replay_scan_prompt(cfg, prompt, rec, _check(A, "A", _F32, (H,), at), _check(D, "D", _F32, (H,), at), start, to,
-                         y.data_ptr(), _DT[out_dtype], ws.data_ptr() if nbytes else 0, _raw_stream(at))
+    _launch(B.replay_scan_prompt, at, cfg, prompt, rec, _check(A, "A", _F32, (H,), at), _check(D, "D", _F32, (H,), at), start,
+            to, y.data_ptr(), _DT[out_dtype], ws.data_ptr() if nbytes else 0)
     return y
 
 
@@ -205,9 +217,9 @@ def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=Non
     if group < 1 or C % group or (wn != C and wn != group):
         raise ValueError(f"group {group} must divide {C} channels, and weight be [{C}] or [{group}]")
     out = z.new_empty(tokens, C) if out_dtype is z.dtype else z.new_empty(tokens, C, dtype=out_dtype)
-    B.replay_gated_norm(_NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0,
-                              eps, 0, y.stride(0), z.stride(0), C, y.data_ptr(), z.data_ptr(),
-                              _check(weight, "weight", _F32, (wn,), at), out.data_ptr()), _raw_stream(at))
+    _launch(B.replay_gated_norm, at,
+            _NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0, eps, 0, y.stride(0),
+                  z.stride(0), C, y.data_ptr(), z.data_ptr(), _check(weight, "weight", _F32, (wn,), at), out.data_ptr()))
     return out
 
 
@@ -238,5 +250,5 @@ def accept_drafts(tokens, target, uniforms, *, draft=None, lengths=None):
     args = _ACCEPT(batch, T, V, _DT[target.dtype], qt, 0, ts[0], ts[1], ds[0], ds[1],
                    drafts, 0 if lengths is None else _check(lengths, "lengths", _I32, (batch,), at), target.data_ptr(), q,
                    _check(uniforms, "uniforms", _F32, (batch, T + 1), at), accepted.data_ptr(), following.data_ptr())
-    B.replay_accept_drafts(args, ws.data_ptr(), _raw_stream(at))
+    _launch(B.replay_accept_drafts, at, args, ws.data_ptr())
     return accepted, following

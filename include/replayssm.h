@@ -23,6 +23,8 @@
  *     every buffer and keeps it alive until the work queued on the stream ends.
  *   - `stream` is a hipStream_t (NULL = the default stream).  Every call only
  *     enqueues work on that stream and returns; none synchronises the host.
+ *     It launches on the current device, which the stream and every array
+ *     belong to.
  *   - Return value: REPLAY_OK, or a negative code.  REPLAY_EINVAL (bad shape,
  *     NULL pointer, misaligned pointer, unsupported pair of formats) is returned
  *     before anything is enqueued; REPLAY_EHIP reports a failed kernel launch.
