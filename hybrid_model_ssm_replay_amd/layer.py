@@ -203,15 +203,19 @@ class ReplayLayer:
         f32 = self.cfg.ckpt_fmt == B.FMT_F32
         if not f32 and (resume is not None or rows is not None or n != s.batch):
             raise ValueError("with a checkpoint below float32, prompts are for the whole batch, in order, and from zero")
-        at = torch.arange(s.batch, device=self.ckpt.device)
-        mask = at < n if rows is None else (at[:, None] == rows[None, :]).any(1)
-        self.flush(None if rows is None and n == s.batch else mask.to(torch.uint8))
+        s.record(rec, (rec["x"].shape[0],))
         in_place = f32 and self.read_copy is None
-        state = self.checkpoint if in_place else self.checkpoint.clone() if f32 else torch.empty(
+        state = self.checkpoint if in_place else torch.empty(
             (s.batch, s.heads, s.head_dim, s.state_dim), dtype=torch.float32, device=self.ckpt.device)
-        y = ops.scan_prompt(rec["x"], rec["B"], rec["C"], rec["dt"], self.A, self.D, seq_start, state,
-                            initial=None if resume is None else state, rows=rows, resume=resume, out_dtype=out_dtype,
-                            status=self.status_word)
+        at, args, y, _ = ops.scan_call(rec["x"], rec["B"], rec["C"], rec["dt"], self.A, self.D, seq_start, state,
+                                       None if resume is None else state, rows, resume, out_dtype, self.status_word)
+        # Everything has been looked at: a call that raises leaves the layer as it was.
+        each = torch.arange(s.batch, device=self.ckpt.device)
+        mask = each < n if rows is None else (each[:, None] == rows[None, :]).any(1)
+        self.flush(None if rows is None and n == s.batch else mask.to(torch.uint8))
+        if f32 and not in_place:
+            state.copy_(self.checkpoint)
+        ops.launch(B.replay_scan_prompt, at, *args)
         if not in_place:
             self.set_state(state)
         return y

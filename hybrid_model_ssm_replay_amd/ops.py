@@ -46,7 +46,7 @@ def _refuse(t, name, dtypes, shape, dense=True):
     raise ValueError(f"{name} must be contiguous" if dense else f"{name} must be dense along its last axis")
 
 
-def _launch(call, at, *args):
+def launch(call, at, *args):
     """call(*args, stream) with device `at`, the tensors', current: kernels go to the
     current device, and the default stream's handle is the same on every one."""
     if _device() == at:
@@ -138,7 +138,7 @@ def short_conv_step(x, weight, ring, pos, widths, *, bias=None, activation="silu
     at, conv, batch, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 3)
     if pos is None or x.shape[0] != batch:
         raise ValueError(f"x has {x.shape[0]} rows, ring {batch}, and pos is needed")
-    _launch(B.replay_short_conv_step, at, conv, x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], to)
+    launch(B.replay_short_conv_step, at, conv, x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], to)
     return outs
 
 
@@ -154,7 +154,7 @@ def short_conv_prompt(x, weight, ring, seq_start, widths, *, bias=None, activati
     [tokens, width] tensor for each width."""
     at, conv, _, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 2)
     prompt, _ = _prompt(x.shape[0], seq_start, rows, resume, status, at)
-    _launch(B.replay_short_conv_prompt, at, conv, prompt, x.data_ptr(), x.stride(0), to)
+    launch(B.replay_short_conv_prompt, at, conv, prompt, x.data_ptr(), x.stride(0), to)
     return outs
 
 
@@ -169,6 +169,13 @@ def scan_prompt(x, Bm, Cm, dt, A, D, seq_start, state, *, initial=None, rows=Non
     initial (same shape, may be ``state`` itself): where sequences start, all of
     them or those with resume nonzero; None: from zero.  out_dtype: float32
     (default) or, with bfloat16 inputs, bfloat16."""
+    at, args, y, _ = scan_call(x, Bm, Cm, dt, A, D, seq_start, state, initial, rows, resume, out_dtype, status)
+    launch(B.replay_scan_prompt, at, *args)
+    return y
+
+
+def scan_call(x, Bm, Cm, dt, A, D, seq_start, state, initial, rows, resume, out_dtype, status):
+    """scan_prompt up to its launch, which then refuses nothing: (device index, arguments, y, workspace)."""
     at = _vectors(x, "x", 3)
     tokens, H, P = x.shape
     dtype = x.dtype
@@ -181,20 +188,27 @@ def scan_prompt(x, Bm, Cm, dt, A, D, seq_start, state, *, initial=None, rows=Non
     out_dtype = _F32 if out_dtype is None else out_dtype
     if out_dtype not in _DT:
         raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
+    if out_dtype is _BF16 and dtype is _F32:
+        raise ValueError("bfloat16 outputs are for bfloat16 inputs")
     if initial is None and resume is not None:
         raise ValueError("resume needs initial")
-    rec = _RECORD(_check(x, "x", dtype, (tokens, H, P), at), _check(Bm, "Bm", dtype, (tokens, G, N), at),
-                  _check(Cm, "Cm", dtype, (tokens, G, N), at), _check(dt, "dt", _F32, (tokens, H), at), 0)
+    xs, Bs, Cs = (_check(x, "x", dtype, (tokens, H, P), at), _check(Bm, "Bm", dtype, (tokens, G, N), at),
+                  _check(Cm, "Cm", dtype, (tokens, G, N), at))
+    rec = _RECORD(xs, Bs, Cs, _check(dt, "dt", _F32, (tokens, H), at), 0)
     to = _check(state, "state", _F32, (batch, H, P, N), at)
     start = 0 if initial is None else to if initial is state else _check(initial, "initial", _F32, (batch, H, P, N), at)
+    if tokens > 1 << 30:
+        raise ValueError(f"{tokens} tokens: at most 2^30")
+    if (xs | Bs | Cs | to | start) & 15:
+        raise ValueError("x, Bm, Cm, state and initial must start at multiples of 16 bytes")
     prompt, n = _prompt(tokens, seq_start, rows, resume, status, at)
     cfg = _CONFIG(B.KIND_MAMBA2, batch, H, G, P, N, 1, 0, 0, 0, 0, B.FLAG_BF16_RECORDS if dtype is _BF16 else 0, 0)
     nbytes = B.replay_scan_workspace_bytes(cfg, tokens, n)
     y = x.new_empty(tokens, H, P, dtype=out_dtype)
     ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
-    _launch(B.replay_scan_prompt, at, cfg, prompt, rec, _check(A, "A", _F32, (H,), at), _check(D, "D", _F32, (H,), at), start,
-            to, y.data_ptr(), _DT[out_dtype], ws.data_ptr() if nbytes else 0)
-    return y
+    args = (cfg, prompt, rec, _check(A, "A", _F32, (H,), at), _check(D, "D", _F32, (H,), at), start, to, y.data_ptr(),
+            _DT[out_dtype], ws.data_ptr() if nbytes else 0)
+    return at, args, y, ws
 
 
 def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=None):
@@ -217,9 +231,9 @@ def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=Non
     if group < 1 or C % group or (wn != C and wn != group):
         raise ValueError(f"group {group} must divide {C} channels, and weight be [{C}] or [{group}]")
     out = z.new_empty(tokens, C) if out_dtype is z.dtype else z.new_empty(tokens, C, dtype=out_dtype)
-    _launch(B.replay_gated_norm, at,
-            _NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0, eps, 0, y.stride(0),
-                  z.stride(0), C, y.data_ptr(), z.data_ptr(), _check(weight, "weight", _F32, (wn,), at), out.data_ptr()))
+    launch(B.replay_gated_norm, at,
+           _NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0, eps, 0, y.stride(0),
+                 z.stride(0), C, y.data_ptr(), z.data_ptr(), _check(weight, "weight", _F32, (wn,), at), out.data_ptr()))
     return out
 
 
@@ -250,5 +264,5 @@ def accept_drafts(tokens, target, uniforms, *, draft=None, lengths=None):
     args = _ACCEPT(batch, T, V, _DT[target.dtype], qt, 0, ts[0], ts[1], ds[0], ds[1],
                    drafts, 0 if lengths is None else _check(lengths, "lengths", _I32, (batch,), at), target.data_ptr(), q,
                    _check(uniforms, "uniforms", _F32, (batch, T + 1), at), accepted.data_ptr(), following.data_ptr())
-    _launch(B.replay_accept_drafts, at, args, ws.data_ptr())
+    launch(B.replay_accept_drafts, at, args, ws.data_ptr())
     return accepted, following
