@@ -105,6 +105,7 @@ _SIG = {
     "replay_init": (ctypes.c_int, [ctypes.POINTER(replay_ctx), ctypes.POINTER(replay_config),
                                    ctypes.POINTER(replay_buffers), _P]),
     "replay_set_state": (ctypes.c_int, [ctypes.POINTER(replay_ctx), _P, _P]),
+    "replay_renew_read_copy": (ctypes.c_int, [ctypes.POINTER(replay_ctx), _P, _P]),
     "replay_step": (ctypes.c_int, [ctypes.POINTER(replay_ctx), ctypes.POINTER(replay_record), _P, _P]),
     "replay_flush": (ctypes.c_int, [ctypes.POINTER(replay_ctx), _P, _P]),
     "replay_verify": (ctypes.c_int, [ctypes.POINTER(replay_ctx), ctypes.c_int32, ctypes.POINTER(replay_record),
@@ -212,6 +213,10 @@ def replay_init(ctx: replay_ctx, cfg: replay_config, buf: replay_buffers, stream
 
 def replay_set_state(ctx, state: int, stream: int) -> None:
     _check("replay_set_state", load_library().replay_set_state(ctypes.byref(ctx), state, stream or None))
+
+
+def replay_renew_read_copy(ctx, mask: int | None, stream: int) -> None:
+    _check("replay_renew_read_copy", load_library().replay_renew_read_copy(ctypes.byref(ctx), mask or None, stream or None))
 
 
 def replay_step(ctx, rec: replay_record, y: int, stream: int) -> None:

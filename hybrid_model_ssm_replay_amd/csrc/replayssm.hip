@@ -110,6 +110,17 @@ FormatBufs formats(const replay_ctx &ctx) {
 
 int hip_status(int e) { return e == 0 ? REPLAY_OK : REPLAY_EHIP; }
 
+// The read copy of a float32 checkpoint, for the sequences of the mask (NULL: all).
+int encode_read_copy(const replay_ctx &ctx, const uint8_t *mask, void *stream) {
+  EncodeArgs a{};
+  a.s = shape_of(ctx.cfg);
+  a.src = (const float *)ctx.buf.ckpt;
+  a.ckpt_pos = halves(ctx).ckpt_in;  // all zero after the init kernel
+  a.write_ckpt = 0;
+  a.mask = mask;
+  return launch_encode_state(a, formats(ctx), (hipStream_t)stream);
+}
+
 // The fields a call reads from its record argument are present and aligned;
 // with the records in the ring only Mamba-2 C and GDN q, v are read.
 bool rec_ok(const replay_record *r, int kind, bool in_ring = false) {
@@ -193,16 +204,17 @@ int replay_init(replay_ctx *ctx, const replay_config *cfg, const replay_buffers 
   if (e) return REPLAY_EHIP;
   if (cfg->ckpt_fmt == REPLAY_FMT_F32 && cfg->read_fmt != REPLAY_FMT_F32) {
     // The read copy starts as the encoding of the initial float32 checkpoint.
-    EncodeArgs a{};
-    a.s = shape_of(*cfg);
-    a.src = (const float *)buf->ckpt;
-    a.ckpt_pos = buf->pointers;  // half 0: all zero after the init kernel
-    a.write_ckpt = 0;
-    e = launch_encode_state(a, formats(*ctx), (hipStream_t)stream);
+    e = encode_read_copy(*ctx, nullptr, stream);
     if (e) return REPLAY_EHIP;
   }
   ctx->magic = kCtxMagic;
   return REPLAY_OK;
+}
+
+int replay_renew_read_copy(replay_ctx *ctx, const uint8_t *seq_mask, void *stream) {
+  if (check_ctx(ctx) != REPLAY_OK) return REPLAY_EINVAL;
+  if (ctx->cfg.ckpt_fmt != REPLAY_FMT_F32 || ctx->cfg.read_fmt == REPLAY_FMT_F32) return REPLAY_ENOTSUP;
+  return hip_status(encode_read_copy(*ctx, seq_mask, stream));
 }
 
 int replay_set_state(replay_ctx *ctx, const float *state, void *stream) {

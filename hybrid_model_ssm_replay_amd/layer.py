@@ -204,20 +204,20 @@ class ReplayLayer:
         if not f32 and (resume is not None or rows is not None or n != s.batch):
             raise ValueError("with a checkpoint below float32, prompts are for the whole batch, in order, and from zero")
         s.record(rec, (rec["x"].shape[0],))
-        in_place = f32 and self.read_copy is None
-        state = self.checkpoint if in_place else torch.empty(
+        state = self.checkpoint if f32 else torch.empty(
             (s.batch, s.heads, s.head_dim, s.state_dim), dtype=torch.float32, device=self.ckpt.device)
         at, args, y, _ = ops.scan_call(rec["x"], rec["B"], rec["C"], rec["dt"], self.A, self.D, seq_start, state,
                                        None if resume is None else state, rows, resume, out_dtype, self.status_word)
         # Everything has been looked at: a call that raises leaves the layer as it was.
         each = torch.arange(s.batch, device=self.ckpt.device)
         mask = each < n if rows is None else (each[:, None] == rows[None, :]).any(1)
-        self.flush(None if rows is None and n == s.batch else mask.to(torch.uint8))
-        if f32 and not in_place:
-            state.copy_(self.checkpoint)
+        mask = None if rows is None and n == s.batch else mask.to(torch.uint8)
+        self.flush(mask)
         ops.launch(B.replay_scan_prompt, at, *args)
-        if not in_place:
+        if not f32:
             self.set_state(state)
+        elif self.read_copy is not None:
+            B.replay_renew_read_copy(self.ctx, mask.data_ptr() if mask is not None else None, _stream())
         return y
 
     def step(self, rec: dict, y: torch.Tensor | None = None) -> torch.Tensor:

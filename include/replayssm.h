@@ -271,6 +271,12 @@ int replay_init(replay_ctx *ctx, const replay_config *cfg, const replay_buffers 
  * windows, e.g. right after replay_init or a full replay_flush). */
 int replay_set_state(replay_ctx *ctx, const float *state, void *stream);
 
+/* With an F32 checkpoint and a separate read copy: write the read copy of the
+ * sequences with seq_mask[b] != 0 (device uint8 [batch]; NULL = all) from their
+ * checkpoint, after something other than these calls has written it
+ * (replay_scan_prompt in place).  REPLAY_ENOTSUP for other formats. */
+int replay_renew_read_copy(replay_ctx *ctx, const uint8_t *seq_mask, void *stream);
+
 /* One decode token for every sequence [P1, Interpretation 2; P3, Interpretation 2]:
  * if a sequence's window is full (L records) it is first folded into the
  * checkpoint; then the record is appended and y is computed from one read of
@@ -427,7 +433,8 @@ int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt 
  *   state      float32 [batch][heads][P][N]: rows of the call's sequences are
  *              written with the state after their last token (an empty
  *              sequence: its start).  It may be `initial`, and it may be the
- *              F32 checkpoint of a layer whose windows are empty in those rows.
+ *              F32 checkpoint of a layer whose windows are empty in those rows
+ *              (then renew its read copy, if it has one).
  *   y          [tokens][heads][P] in y_dtype (REPLAY_DT_F32; REPLAY_DT_BF16 with
  *              bf16 records only): before their rounding bf16 outputs are good
  *              to 2^-16 of each term that they add, float32 outputs to float32.
