@@ -12,6 +12,7 @@ bool dtype_ok(int d) { return d == REPLAY_DT_F32 || d == REPLAY_DT_BF16; }
 size_t elem_size(int d) { return d == REPLAY_DT_BF16 ? 2 : 4; }
 bool elem_aligned(const void *p, int d) { return ((uintptr_t)p & (elem_size(d) - 1)) == 0; }
 constexpr int kMost = 1 << 30;  // tokens, sequences, vocabulary: indexes a little past them still fit 32 bits
+constexpr int kMostRow = 1 << 23;  // values of a token's x, and of its B or C
 int hip_status(int e) { return e == 0 ? REPLAY_OK : REPLAY_EHIP; }
 
 bool prompt_ok(const replay_prompt *p, int batch) {
@@ -56,6 +57,8 @@ bool scan_cfg_ok(const replay_config *c) {
   if (c->batch < 1 || c->heads < 1 || c->groups < 1 || c->heads % c->groups) return false;
   if (c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16) return false;
   if (c->state_dim != 16 && c->state_dim != 32 && c->state_dim != 64 && c->state_dim != 128) return false;
+  // The kernel addresses a chunk's 64 rows of up to 4 bytes a value by 32 bits.
+  if ((int64_t)c->heads * c->head_dim >= kMostRow || (int64_t)c->groups * c->state_dim >= kMostRow) return false;
   return (int64_t)c->batch * c->heads <= 0x7fffffffLL;
 }
 

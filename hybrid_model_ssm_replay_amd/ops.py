@@ -197,8 +197,8 @@ def scan_call(x, Bm, Cm, dt, A, D, seq_start, state, initial, rows, resume, out_
     rec = _RECORD(xs, Bs, Cs, _check(dt, "dt", _F32, (tokens, H), at), 0)
     to = _check(state, "state", _F32, (batch, H, P, N), at)
     start = 0 if initial is None else to if initial is state else _check(initial, "initial", _F32, (batch, H, P, N), at)
-    if tokens > 1 << 30:
-        raise ValueError(f"{tokens} tokens: at most 2^30")
+    if tokens > 1 << 30 or H * P >= 1 << 23 or G * N >= 1 << 23:
+        raise ValueError(f"{tokens} tokens of {H} x {P} and {G} x {N} values: at most 2^30, below 2^23 and below 2^23")
     if (xs | Bs | Cs | to | start) & 15:
         raise ValueError("x, Bm, Cm, state and initial must start at multiples of 16 bytes")
     prompt, n = _prompt(tokens, seq_start, rows, resume, status, at)

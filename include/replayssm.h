@@ -426,8 +426,9 @@ int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt 
 /* The Mamba-2 recurrence over packed prompts, S <- exp(dt A) S + dt x B^T,
  * y = S C + D x for every token of every sequence.  cfg gives kind (Mamba-2),
  * batch, heads, groups, head_dim, state_dim and REPLAY_FLAG_BF16_RECORDS;
- * window, max_draft and formats are ignored.  rec: x [tokens][heads][P],
- * B, C [tokens][groups][N], dt [tokens][heads] (positive), as for a step.
+ * window, max_draft and formats are ignored; heads * head_dim and groups *
+ * state_dim are below 2^23.  rec: x [tokens][heads][P], B, C
+ * [tokens][groups][N], dt [tokens][heads] (positive), as for a step.
  *   initial    float32 [batch][heads][P][N]: where a resumed sequence starts
  *              (resume NULL: every sequence); NULL: every sequence starts from 0.
  *   state      float32 [batch][heads][P][N]: rows of the call's sequences are
