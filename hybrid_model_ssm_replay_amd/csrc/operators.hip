@@ -11,7 +11,7 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool dtype_ok(int d) { return d == REPLAY_DT_F32 || d == REPLAY_DT_BF16; }
 size_t elem_size(int d) { return d == REPLAY_DT_BF16 ? 2 : 4; }
 bool elem_aligned(const void *p, int d) { return ((uintptr_t)p & (elem_size(d) - 1)) == 0; }
-constexpr int kMost = 1 << 30;  // tokens, sequences, vocabulary: indexes a little past them still fit 32 bits
+constexpr int kMost = 1 << 30;  // tokens, sequences, channels, vocabulary: indexes a little past them still fit 32 bits
 constexpr int kMostRow = 1 << 23;  // values of a token's x, and of its B or C
 int hip_status(int e) { return e == 0 ? REPLAY_OK : REPLAY_EHIP; }
 
@@ -28,7 +28,7 @@ bool conv_ok(const replay_short_conv *c) {
   if (!c || c->channels < 1 || c->taps < 2 || c->taps > 4 || c->batch < 1 || !dtype_ok(c->dtype) || c->reserved)
     return false;
   if (c->silu != 0 && c->silu != 1) return false;
-  if (c->slots < c->taps - 1) return false;
+  if (c->channels > kMost || c->batch > kMost || c->slots < c->taps - 1) return false;
   int64_t sum = 0;
   for (int i = 0; i < 3; ++i) {
     if (c->width[i] < 0) return false;

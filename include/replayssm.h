@@ -381,6 +381,7 @@ typedef struct replay_prompt {
  * the input at position p of a sequence lives in slot p mod slots.  Positions
  * are the layer's own (replay_current_pointers), so rejecting drafts moves a
  * pointer and restores nothing, as for the recurrent state.
+ *   channels, batch  1..2^30.
  *   taps       2..4.
  *   slots      >= taps - 1 + T for every step of T tokens.
  *   silu       1: act(v) = v / (1 + exp(-v)); 0: act(v) = v.

@@ -25,3 +25,11 @@ def test_scan_rows_past_32_bits_are_refused(B, heads, groups, P, N):
     assert B.replay_scan_workspace_bytes(cfg, 1000, 1) == 0
     p = B.replay_prompt(8, 1, P16, 0, 0, 0)
     _refused(B, lambda: B.replay_scan_prompt(cfg, p, B.make_record(P16, P16, P16, P16), P16, P16, 0, P16, P16, B.DT_F32, P16, 0))
+
+
+def test_convolutions_of_more_channels_or_rows_than_2_to_30_are_refused(B):
+    for channels, batch in (((1 << 31) - 1, 1), ((1 << 30) + 1, 1), (8, (1 << 31) - 1), (8, (1 << 30) + 1)):
+        c = B.replay_short_conv(channels, 4, 4, batch, B.DT_BF16, 1, (channels, 0, 0), 0, P16, 0, P16, P16, 0)
+        _refused(B, lambda: B.replay_short_conv_step(c, P16, channels, channels, 1, [P16, 0, 0], 0))
+        p = B.replay_prompt(8, 1, P16, 0, 0, 0)
+        _refused(B, lambda: B.replay_short_conv_prompt(c, p, P16, channels, [P16, 0, 0], 0))
