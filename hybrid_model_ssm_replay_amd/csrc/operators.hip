@@ -120,7 +120,8 @@ int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, co
 }
 
 int replay_gated_norm(const replay_gated_norm_args *a, void *stream) {
-  if (!a || a->tokens < 0 || a->channels < 1 || a->group < 1 || a->channels % a->group || a->reserved)
+  if (!a || a->tokens < 0 || a->tokens > kMost || a->channels < 1 || a->channels > kMost || a->group < 1 ||
+      a->channels % a->group || a->reserved)
     return REPLAY_EINVAL;
   if (a->weight_len != a->channels && a->weight_len != a->group) return REPLAY_EINVAL;
   if (!dtype_ok(a->y_dtype) || !dtype_ok(a->z_dtype) || !dtype_ok(a->out_dtype)) return REPLAY_EINVAL;

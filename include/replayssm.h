@@ -457,7 +457,8 @@ int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, co
  * Rows of y, z, out start at multiples of their strides (elements; >= 0 for y
  * and z, whose rows may repeat, >= channels for out); each array has its type.
  * weight: float32 [weight_len], weight_len = channels or group (one vector
- * shared by the groups).  Statistics are float32. */
+ * shared by the groups).  tokens and channels are at most 2^30.  Statistics are
+ * float32. */
 typedef struct replay_gated_norm_args {
   int32_t tokens;
   int32_t channels;

@@ -33,3 +33,13 @@ def test_convolutions_of_more_channels_or_rows_than_2_to_30_are_refused(B):
         _refused(B, lambda: B.replay_short_conv_step(c, P16, channels, channels, 1, [P16, 0, 0], 0))
         p = B.replay_prompt(8, 1, P16, 0, 0, 0)
         _refused(B, lambda: B.replay_short_conv_prompt(c, p, P16, channels, [P16, 0, 0], 0))
+
+
+def _norm(B, tokens, channels, group):
+    return B.replay_gated_norm_args(tokens, channels, group, group, 0, 0, 0, 0, 1e-5, 0, 0, 0, channels, P16, P16, P16, P16)
+
+
+def test_norms_of_more_tokens_or_channels_than_2_to_30_are_refused(B):
+    for tokens, channels, group in (((1 << 31) - 1, 1, 1), ((1 << 30) + 1, 8, 8), (1, (1 << 31) - 1, (1 << 31) - 1),
+                                    (1, (1 << 30) + 128, 128)):
+        _refused(B, lambda: B.replay_gated_norm(_norm(B, tokens, channels, group), 0))
