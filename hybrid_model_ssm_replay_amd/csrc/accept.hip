@@ -285,7 +285,7 @@ size_t accept_workspace(int batch, int vocab) {
 
 int launch_accept(const replay_accept_args &a, void *workspace, hipStream_t st) {
   Slices s = slices_of(a.batch, a.vocab);
-  if ((int64_t)a.batch * s.n > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  if ((int64_t)a.batch * s.n > kMostBlocks) return kTooLarge;
   s.sums = (double2 *)workspace;
   if (a.target_dtype == REPLAY_DT_BF16)
     launch_q<bf16_t>(a, s, st);

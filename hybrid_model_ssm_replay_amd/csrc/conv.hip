@@ -342,11 +342,13 @@ int launch(ShortConvArgs a, bool prompt, hipStream_t st) {
   const int per = (a.C + kThreads * V - 1) / (kThreads * V);
   if (prompt) a.T = kTile;
   const int64_t rows = prompt ? items_of(a.p.tokens, a.p.n, a.T) : a.batch;
-  if (rows * per > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  // Two rows a thread still leave two workgroups a CU (256 rows: 11.0 us, one by one 12.4).
+  const bool two = !prompt && rows * per >= 1024;
+  if ((two ? (rows + 1) / 2 : rows) * per > kMostBlocks) return kTooLarge;
   if (prompt) {
     hipLaunchKernelGGL((short_conv_prompt_k<T, V, K>), dim3((uint32_t)(rows * per)), dim3(kThreads), 0, st, a,
                        make_fastdiv((uint32_t)per));
-  } else if (rows * per >= 1024) {  // two rows a thread still leave two workgroups a CU (256 rows: 11.0 us, one by one 12.4)
+  } else if (two) {
     launch_step<T, V, K, 2>(a, per, st);
   } else {
     launch_step<T, V, K, 1>(a, per, st);

@@ -125,9 +125,10 @@ int launch_fast(const replay_gated_norm_args &a, hipStream_t st) {
   // groups of 1024, bf16: 4096 tokens 34 us, one by one 35, by fours 36; 1024 tokens one
   // by one 12.2, by twos 12.5).
   const int tok = (int64_t)a.tokens * sets >= 2 * 32 * 256 ? 2 : 1;
-  const int64_t items = (int64_t)((a.tokens + tok - 1) / tok) * sets;
-  hipLaunchKernelGGL((gated_norm_k<TY, TZ, TO, LANES, IT>), dim3((uint32_t)((items + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                     st, a, sets, make_fastdiv((uint32_t)sets), tok);
+  const int64_t blocks = ((int64_t)((a.tokens + tok - 1) / tok) * sets + kWaves - 1) / kWaves;
+  if (blocks > kMostBlocks) return kTooLarge;
+  hipLaunchKernelGGL((gated_norm_k<TY, TZ, TO, LANES, IT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a, sets,
+                     make_fastdiv((uint32_t)sets), tok);
   return (int)hipGetLastError();
 }
 
@@ -139,6 +140,7 @@ int launch(const replay_gated_norm_args &a, hipStream_t st) {
   if (a.group <= 1024) return launch_fast<TY, TZ, TO, 64, 2>(a, st);
   if (a.group <= 2048) return launch_fast<TY, TZ, TO, 64, 4>(a, st);
   const int groups = a.channels / a.group;
+  if ((int64_t)a.tokens * groups > kMostBlocks) return kTooLarge;
   hipLaunchKernelGGL((gated_norm_long_k<TY, TZ, TO>), dim3((uint32_t)(a.tokens * groups)), dim3(kThreads), 0, st, a,
                      make_fastdiv((uint32_t)groups));
   return (int)hipGetLastError();

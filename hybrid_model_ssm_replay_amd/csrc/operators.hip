@@ -13,7 +13,7 @@ size_t elem_size(int d) { return d == REPLAY_DT_BF16 ? 2 : 4; }
 bool elem_aligned(const void *p, int d) { return ((uintptr_t)p & (elem_size(d) - 1)) == 0; }
 constexpr int kMost = 1 << 30;  // tokens, sequences, channels, vocabulary: indexes a little past them still fit 32 bits
 constexpr int kMostRow = 1 << 23;  // values of a token's x, and of its B or C
-int hip_status(int e) { return e == 0 ? REPLAY_OK : REPLAY_EHIP; }
+int hip_status(int e) { return e == 0 ? REPLAY_OK : e == kTooLarge ? REPLAY_EINVAL : REPLAY_EHIP; }
 
 bool prompt_ok(const replay_prompt *p, int batch) {
   return p && p->tokens >= 0 && p->tokens <= kMost && p->sequences >= 1 && p->sequences <= batch &&
@@ -127,7 +127,6 @@ int replay_gated_norm(const replay_gated_norm_args *a, void *stream) {
   if (!dtype_ok(a->y_dtype) || !dtype_ok(a->z_dtype) || !dtype_ok(a->out_dtype)) return REPLAY_EINVAL;
   if ((a->norm_first != 0 && a->norm_first != 1) || !(a->eps >= 0.f)) return REPLAY_EINVAL;
   if (a->tokens == 0) return REPLAY_OK;
-  if ((int64_t)a->tokens * (a->channels / a->group) > 0x7fffffffLL) return REPLAY_EINVAL;
   if (!a->y || !a->z || !a->weight || !a->out) return REPLAY_EINVAL;
   if (!elem_aligned(a->y, a->y_dtype) || !elem_aligned(a->z, a->z_dtype) || !elem_aligned(a->out, a->out_dtype) ||
       !elem_aligned(a->weight, REPLAY_DT_F32))

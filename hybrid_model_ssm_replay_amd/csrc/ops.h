@@ -148,6 +148,10 @@ __device__ __forceinline__ int batch_row(const Packed &p, int i, bool report) {
 }
 
 // ---- launches -------------------------------------------------------------------
+// A launch holds fewer than 2^32 work-items.  A launch function returns kTooLarge before
+// anything is enqueued where its workgroups of 256 are more.
+constexpr int64_t kMostBlocks = (1 << 24) - 1;
+constexpr int kTooLarge = -1;
 struct ShortConvArgs {
   int C, K, slots, batch, dtype, silu;
   int w[3];

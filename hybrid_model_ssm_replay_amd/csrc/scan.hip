@@ -194,7 +194,7 @@ struct ScanPlan {
   int parts;      // workgroups a head's columns are spread over (then hw is 1)
   int nb;         // workgroups of a group
   int adds;       // segments add up the own states before them themselves; 0: combine_k does
-  int units;      // items x groups: the workgroups of a unit share B and C
+  int64_t units;  // items x groups: the workgroups of a unit share B and C
   FastDiv fnb, fG, fparts;
   float *state;   // [items][H][P N]: a segment's own state, then its start
   float *decay;   // [items][H]
@@ -792,7 +792,7 @@ ScanPlan make_plan(const ScanArgs &a) {
   if (p.seg >= a.p.tokens) p.seg = 0;
   p.adds = p.seg && (a.p.tokens + p.seg - 1) / p.seg <= 4;
   p.items = p.seg ? items_of(a.p.tokens, a.p.n, p.seg) : a.p.n;
-  p.units = p.items * a.G;
+  p.units = (int64_t)p.items * a.G;
   return p;
 }
 
@@ -801,8 +801,8 @@ size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.ite
 template <typename R, typename Y, int NK, int CT, int MODE>
 int launch_part(const ScanArgs &a, ScanPlan p, hipStream_t st) {
   set_tiles(a, p, CT);
-  const int64_t blocks = ((int64_t)p.units + kXcds - 1) / kXcds * kXcds * p.nb;
-  if (blocks > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  const int64_t blocks = (p.units + kXcds - 1) / kXcds * kXcds * p.nb;
+  if (blocks > kMostBlocks) return kTooLarge;
   hipLaunchKernelGGL((scan_k<R, Y, NK, CT, MODE>), dim3((uint32_t)blocks), dim3(kThreads), (Shape_<R, Y, NK, CT, MODE>::lds(p.hw)),
                      st, a, p);
   return (int)hipGetLastError();
@@ -811,10 +811,10 @@ int launch_part(const ScanArgs &a, ScanPlan p, hipStream_t st) {
 template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
-  if ((int64_t)a.p.n * per_seq > 0x7fffffffLL) return (int)hipErrorInvalidValue;
+  if (p.seg && !p.adds && (int64_t)a.p.n * per_seq > kMostBlocks) return kTooLarge;
   // At most one workgroup a CU: waves of half the columns, on twice as many, end sooner
   // (200 tokens of 32 heads: 20 us against 25; 600: 28 against 34).
-  const bool few = (int64_t)p.units * p.nb <= 256;
+  const bool few = p.units * p.nb <= 256;
   if (!p.seg) return few ? launch_part<R, Y, NK, 1, kAll>(a, p, st) : launch_part<R, Y, NK, 2, kAll>(a, p, st);
   // Own states of float32 records: half the columns leave LDS for four workgroups a CU
   // (2048 tokens of 64 heads: 100 us a pass against 109).
