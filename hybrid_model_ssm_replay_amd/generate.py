@@ -125,14 +125,22 @@ class Model:
 
 
 def generate(model, prompts, count, drafted=4, rng=None):
-    """At least ``count`` new tokens behind each prompt (lists of token numbers, one for
-    every sequence of the model).  Returns the new tokens, a list for each prompt, and
+    """At least ``count`` new tokens behind each prompt (lists of at least one token
+    number, one for every sequence of the model).  Returns the new tokens, a list for each prompt, and
     how many calls of the model made them.
 
     Each call runs the last token and ``drafted`` drafts; the drafts are drawn from the
     model's bigram table, and the kept tokens follow the model's own distribution."""
-    device = model.embed.device
-    batch = len(prompts)
+    device, vocab = model.embed.device, model.embed.shape[0]
+    batch, state = len(prompts), model.mixers[0].state
+    if batch != state.shapes.batch:
+        raise ValueError(f"{batch} prompts for {state.shapes.batch} sequences")
+    if not all(len(p) for p in prompts):
+        raise ValueError("a prompt is empty")
+    if not all(0 <= t < vocab for p in prompts for t in p):
+        raise ValueError(f"token numbers are 0 to {vocab - 1}")
+    if not 0 <= drafted < state.cfg.max_draft:
+        raise ValueError(f"drafted is 0 to {state.cfg.max_draft - 1}: a call runs the last token too")
     start = torch.tensor([0] + [len(p) for p in prompts], device=device).cumsum(0).to(torch.int32)
     probs = model.prefill(torch.tensor([t for p in prompts for t in p], device=device), start)
     last = torch.multinomial(probs[start[1:].long() - 1], 1, generator=rng).to(torch.int32)  # [batch, 1]
