@@ -91,6 +91,11 @@ class replay_accept_args(ctypes.Structure):
                 ("next", ctypes.c_void_p)]
 
 
+class replay_scan_layout(ctypes.Structure):
+    _fields_ = [("segment", ctypes.c_int32), ("adds", ctypes.c_int32), ("columns", ctypes.c_int32),
+                ("workgroups", ctypes.c_int32)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -125,6 +130,7 @@ _SIG = {
     "replay_short_conv_step": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P]),
     "replay_short_conv_prompt": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P]),
     "replay_scan_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
+    "replay_scan_plan": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(replay_scan_layout)]),
     "replay_scan_prompt": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
     "replay_gated_norm": (ctypes.c_int, [_P, _P]),
     "replay_accept_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -154,7 +160,7 @@ def load_library(path: str | None = None):
         fn.restype = res
         fn.argtypes = args
     for i, st in enumerate((replay_config, replay_buffers, replay_record, replay_ctx, replay_ring_view, replay_prompt,
-                            replay_short_conv, replay_gated_norm_args, replay_accept_args)):
+                            replay_short_conv, replay_gated_norm_args, replay_accept_args, replay_scan_layout)):
         if lib.replay_abi_sizeof(i) != ctypes.sizeof(st):
             raise ImportError(f"ABI mismatch for {st.__name__}: C {lib.replay_abi_sizeof(i)} "
                               f"vs ctypes {ctypes.sizeof(st)}")
@@ -293,6 +299,12 @@ def replay_short_conv_prompt(conv, prompt, x: int, row_stride: int, outs, stream
 
 def replay_scan_workspace_bytes(cfg, tokens: int, sequences: int) -> int:
     return (_lib or load_library()).replay_scan_workspace_bytes(_by_address(cfg), tokens, sequences)
+
+
+def replay_scan_plan(cfg, tokens: int, sequences: int) -> replay_scan_layout:
+    layout = replay_scan_layout()
+    _check("replay_scan_plan", load_library().replay_scan_plan(_by_address(cfg), tokens, sequences, ctypes.byref(layout)))
+    return layout
 
 
 def replay_scan_prompt(cfg, prompt, rec, A: int, D: int, initial: int, state: int, y: int, y_dtype: int, workspace: int,

@@ -62,6 +62,10 @@ bool scan_cfg_ok(const replay_config *c) {
   return (int64_t)c->batch * c->heads <= 0x7fffffffLL;
 }
 
+bool scan_size_ok(const replay_config *c, int tokens, int sequences) {
+  return scan_cfg_ok(c) && tokens >= 0 && tokens <= kMost && sequences >= 1 && sequences <= c->batch && sequences <= kMost;
+}
+
 ScanArgs scan_args(const replay_config &c, int tokens, int sequences) {
   ScanArgs a{};
   a.H = c.heads, a.G = c.groups, a.P = c.head_dim, a.N = c.state_dim;
@@ -96,8 +100,15 @@ int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt 
 }
 
 size_t replay_scan_workspace_bytes(const replay_config *cfg, int32_t tokens, int32_t sequences) {
-  if (!scan_cfg_ok(cfg) || tokens < 0 || tokens > kMost || sequences < 1 || sequences > cfg->batch || sequences > kMost) return 0;
-  return scan_workspace(scan_args(*cfg, tokens, sequences));
+  return scan_size_ok(cfg, tokens, sequences) ? scan_workspace(scan_args(*cfg, tokens, sequences)) : 0;
+}
+
+int replay_scan_plan(const replay_config *cfg, int32_t tokens, int32_t sequences, replay_scan_layout *layout) {
+  if (!scan_size_ok(cfg, tokens, sequences) || !layout) return REPLAY_EINVAL;
+  int32_t plan[4];
+  scan_plan(scan_args(*cfg, tokens, sequences), plan);
+  *layout = replay_scan_layout{plan[0], plan[1], plan[2], plan[3]};
+  return REPLAY_OK;
 }
 
 int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, const replay_record *rec,

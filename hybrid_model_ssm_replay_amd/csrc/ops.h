@@ -179,6 +179,7 @@ struct ScanArgs {
 };
 size_t scan_workspace(const ScanArgs &a);
 int launch_scan(const ScanArgs &a, hipStream_t st);
+void scan_plan(const ScanArgs &a, int32_t (&plan)[4]);  // see replay_scan_plan
 
 int launch_gated_norm(const replay_gated_norm_args &a, hipStream_t st);
 

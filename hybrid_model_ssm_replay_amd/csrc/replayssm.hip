@@ -181,6 +181,7 @@ size_t replay_abi_sizeof(int which) {
     case 6: return sizeof(replay_short_conv);
     case 7: return sizeof(replay_gated_norm_args);
     case 8: return sizeof(replay_accept_args);
+    case 9: return sizeof(replay_scan_layout);
     default: return 0;
   }
 }

@@ -796,6 +796,11 @@ ScanPlan make_plan(const ScanArgs &a) {
   return p;
 }
 
+// Column tiles of a wave with outputs.  At most one workgroup a CU: waves of half the
+// columns, on twice as many, end sooner (200 tokens of 32 heads: 20 us against 25; 600:
+// 28 against 34).
+int tiles(const ScanPlan &p) { return p.units * p.nb <= 256 ? 1 : 2; }
+
 size_t decay_bytes(const ScanArgs &a, const ScanPlan &p) { return ((size_t)p.items * a.H * 4 + 255) / 256 * 256; }
 
 template <typename R, typename Y, int NK, int CT, int MODE>
@@ -812,9 +817,7 @@ template <typename R, typename Y, int NK>
 int launch(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
   const int per_seq = (a.H * a.P * a.N / 4 + kThreads - 1) / kThreads;
   if (p.seg && !p.adds && (int64_t)a.p.n * per_seq > kMostBlocks) return kTooLarge;
-  // At most one workgroup a CU: waves of half the columns, on twice as many, end sooner
-  // (200 tokens of 32 heads: 20 us against 25; 600: 28 against 34).
-  const bool few = p.units * p.nb <= 256;
+  const bool few = tiles(p) == 1;
   if (!p.seg) return few ? launch_part<R, Y, NK, 1, kAll>(a, p, st) : launch_part<R, Y, NK, 2, kAll>(a, p, st);
   // Own states of float32 records: half the columns leave LDS for four workgroups a CU
   // (2048 tokens of 64 heads: 100 us a pass against 109).
@@ -837,6 +840,13 @@ int launch_n(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
 size_t scan_workspace(const ScanArgs &a) {
   const ScanPlan p = make_plan(a);
   return p.seg ? decay_bytes(a, p) + (size_t)p.items * a.H * a.P * a.N * 4 : 0;
+}
+
+void scan_plan(const ScanArgs &a, int32_t (&plan)[4]) {
+  ScanPlan p = make_plan(a);
+  plan[0] = p.seg, plan[1] = p.adds, plan[2] = 16 * tiles(p);
+  set_tiles(a, p, tiles(p));
+  plan[3] = (int32_t)(p.units * p.nb < INT32_MAX ? p.units * p.nb : INT32_MAX);
 }
 
 int launch_scan(const ScanArgs &a, hipStream_t st) {

@@ -246,7 +246,8 @@ size_t replay_pointer_words(const replay_config *cfg);
 const char *replay_strerror(int code);
 /* sizeof of the ABI structs, for bindings: 0 replay_config, 1 replay_buffers,
  * 2 replay_record, 3 replay_ctx, 4 replay_ring_view, 5 replay_prompt,
- * 6 replay_short_conv, 7 replay_gated_norm_args, 8 replay_accept_args. */
+ * 6 replay_short_conv, 7 replay_gated_norm_args, 8 replay_accept_args,
+ * 9 replay_scan_layout. */
 size_t replay_abi_sizeof(int which);
 
 /* ---- the decode calls -------------------------------------------------- */
@@ -446,6 +447,19 @@ int replay_short_conv_prompt(const replay_short_conv *conv, const replay_prompt 
  * reach earlier ones of the same 64-token stretch of the same sequence; it
  * never reaches another sequence. */
 size_t replay_scan_workspace_bytes(const replay_config *cfg, int32_t tokens, int32_t sequences);
+/* How a call of these sizes is laid out on the card: what tests and profiles name
+ * a launch by.  Results do not depend on it beyond float32 rounding.
+ *   segment     tokens of the segments that sequences are cut into, or 0.
+ *   adds        1: segments add up where they start themselves; 0: a launch does.
+ *   columns     columns of x that a wave holds, 16 or 32, where outputs are made.
+ *   workgroups  of that launch. */
+typedef struct replay_scan_layout {
+  int32_t segment;
+  int32_t adds;
+  int32_t columns;
+  int32_t workgroups;
+} replay_scan_layout;
+int replay_scan_plan(const replay_config *cfg, int32_t tokens, int32_t sequences, replay_scan_layout *layout);
 int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, const replay_record *rec,
                        const float *A, const float *D, const float *initial, float *state, void *y, int32_t y_dtype,
                        void *workspace, void *stream);
