@@ -12,7 +12,7 @@
 // adds the slices up in their order, takes the one that holds the sampling
 // number, and looks for the token in it: the rows of 64 within a slice, then the
 // lane.  Every sum has a fixed order: no atomics.
-// 128 sequences of 50021, bf16: sums_k reads 26 MB in 9.5 us, pick_k takes 6.9 (a chain of
+// 128 sequences of 50021, bf16: sums_k reads 26 MB in 9.1 us, pick_k takes 7.4 (a chain of
 // loads and scans, each waiting for the one before); one of 131072: 3.5 and 4.0 us.
 //
 // Sums are float64: p - q of float32 or bf16 values is exact or nearly so there,
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void pick_k(replay_accept_args a, Slices 
 }
 
 // Slices of 2048 values, longer where there would be more than 2048 workgroups: those
-// fill the card at once (128 sequences of 50021, bf16: sums_k 9.5 us, with 2048 values
+// fill the card at once (128 sequences of 50021, bf16: sums_k 9.1 us, with 2048 values
 // 12.7).
 Slices slices_of(int batch, int vocab) {
   Slices s{};

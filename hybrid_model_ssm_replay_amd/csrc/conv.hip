@@ -8,8 +8,11 @@
 // issues the loads of several tokens (a prompt) or batch rows (a step) at a time:
 // that is what keeps enough bytes under way, and in a step it also shares the
 // weights, which are as large as a row's inputs and outputs together.
-// With 10240 channels, 4 taps, bf16: a prompt of 8192 tokens moves 336 MB in 72 us (4.7
-// TB/s; a large copy reaches 5.1), a step of 256 rows 31 MB in 11 us.
+// With 10240 channels, 4 taps, bf16: a prompt of 8192 tokens moves 336 MB in 74 us (4.5
+// TB/s; a large copy reaches 5.1), a step of 256 rows 31 MB in 11 us.  Rows of odd
+// length cost more, all accesses being unaligned and the threads at a field's border
+// going element by element: 4096 tokens of 10235 channels 168 MB in 108 us, a step of
+// 256 rows 20 us.
 #include "ops.h"
 
 namespace rssm {
@@ -333,8 +336,9 @@ void launch_step(const ShortConvArgs &a, int per, hipStream_t st) {
 }
 
 // Tokens of a prompt tile: short enough for many workgroups, so that those of uneven
-// sequences end together; a tile reads K - 1 of its predecessor's rows once more, mostly
-// from L2 (16384 tokens of 10240 channels, bf16: 142 us with 12 to 24, 156 with 64).
+// sequences end together; a tile reads K - 1 of its predecessor's rows once more, from
+// HBM: neighbouring tiles of a channel block are on other XCDs (8192 tokens of 10240
+// channels, bf16: 197 MB read for 168; 16384 tokens: 142 us with 12 to 24, 156 with 64).
 constexpr int kTile = 24;
 
 template <typename T, int V, int K>

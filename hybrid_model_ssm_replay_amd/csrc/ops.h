@@ -100,8 +100,8 @@ __device__ __forceinline__ void store_part(T *p, int n, const float (&v)[V]) {
   }
 }
 
-// v / (1 + exp(-v)) by the hardware exponential and reciprocal (about 1e-7
-// relative each).  exp(-v) overflows to infinity for v < -88, where the result is -0.
+// v / (1 + exp(-v)) by the hardware exponential and reciprocal: a few 2^-24 relative,
+// and about |v| 2^-24 from rounding the exponential's argument.  exp(-v) overflows to infinity for v < -88, where the result is -0.
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
 // ---- packed sequences -----------------------------------------------------------

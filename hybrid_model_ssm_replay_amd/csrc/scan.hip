@@ -15,7 +15,8 @@
 //
 // A workgroup takes up to 128 columns of x (heads of one group, which share
 // B, C and G) of one sequence, and walks its chunks; a wave owns 32 columns of
-// one head with their whole state in registers (S^T as accumulators of
+// one head (16, and a workgroup 64, in calls of few workgroups and for the own
+// states of float32 records) with their whole state in registers (S^T as accumulators of
 // v_mfma_f32_16x16x32_bf16: lane l holds rows n = 4 (l / 16) + i of column p =
 // l % 16).  That layout is at once the operand layout of S C^T with the sum
 // over n taken in the order n = 32 k + 16 (i / 4) + 4 (l / 16) + i % 4, so the
@@ -41,8 +42,9 @@
 // operations, and two waves a SIMD, all that the registers hold, issue one of
 // those about every six cycles; the matrix pipe is busy 38 % of the time, the clock
 // near 2.0 GHz under this load.  128 heads of 64, states of 128, bf16: one prompt of
-// 8192 tokens 204 us (own states 61, combine_k 10, outputs 133; 0.3 GB would take 60
-// us), 24 prompts of 16384 tokens with float32 outputs 398 us (1.1 GB, 211 us).
+// 8192 tokens 204 to 210 us (own states 61, combine_k 10, outputs 133; 0.3 GB would
+// take 60), 24 prompts of 16384 tokens with float32 outputs 398 to 403
+// us (1.1 GB, 211 us).
 #include "ops.h"
 
 namespace rssm {
@@ -775,7 +777,12 @@ ScanPlan make_plan(const ScanArgs &a) {
   set_tiles(a, p, 2);
   const int per = a.G * p.nb;
   // Split sequences along the length when there are too few to fill the card, which
-  // holds 512 workgroups.  Each sequence ends with a part of a segment, half of one on
+  // holds 512 workgroups.  Lengths are on the device, so the rules go by the number of
+  // sequences and all their tokens: a long prompt among enough short ones to fill the
+  // card by their number stays whole (128 heads: 8000 tokens alone 236 us, with six
+  // prompts of ten 269, with seven 672).  The thresholds in tokens were measured with 32
+  // and 128 heads of 64 columns and stand for where a segment's start and the launches
+  // cost what its length saves; they do not depend on the heads.  Each sequence ends with a part of a segment, half of one on
   // average; with those counted, few segments wait for a second round (2048 float32
   // tokens of five sequences: 99 us against 104, 4096 of nine: 93 against 99).
   const int want = (512 + per - 1) / per, whole = max(want - a.p.n / 2, 1);

@@ -151,7 +151,7 @@ def short_conv_prompt(x, weight, ring, seq_start, widths, *, bias=None, activati
     ...), all different; resume uint8 or bool [sequences]: continue from the ring's
     history (None: no sequence does); pos as for a step (None: 0).  The ring's rows
     are left so that a step at pos continues the sequence.  Returns one contiguous
-    [tokens, width] tensor for each width."""
+    [tokens, width] tensor for each width; rows outside every sequence are not written."""
     at, conv, _, outs, to = _short_conv(x, weight, ring, pos, widths, bias, activation, status, 2)
     prompt, _ = _prompt(x.shape[0], seq_start, rows, resume, status, at)
     launch(B.replay_short_conv_prompt, at, conv, prompt, x.data_ptr(), x.stride(0), to)
@@ -160,7 +160,8 @@ def short_conv_prompt(x, weight, ring, seq_start, widths, *, bias=None, activati
 
 def scan_prompt(x, Bm, Cm, dt, A, D, seq_start, state, *, initial=None, rows=None, resume=None, out_dtype=None,
                 status=None):
-    """The Mamba-2 recurrence over packed prompts: y for every token, and the state after the last.
+    """The Mamba-2 recurrence over packed prompts: y for every token of a sequence (other rows
+    are not written), and the state after the last.
 
     x [tokens, heads, head_dim], Bm and Cm [tokens, groups, state_dim], all float32
     or all bfloat16; dt float32 [tokens, heads] (positive); A, D float32 [heads];

@@ -360,7 +360,8 @@ int replay_record_slots(const replay_ctx *ctx, int32_t *slots, void *stream);
  *   seq_start  device int32 [sequences + 1], non-decreasing, within 0..tokens:
  *              sequence i is rows seq_start[i] .. seq_start[i + 1] - 1 (it may
  *              be empty).  Values are clamped into that range, never followed
- *              outside it.
+ *              outside it.  Outputs of rows outside every sequence, and of
+ *              skipped sequences, are not written.
  *   rows       device int32 [sequences]: the batch row (state, ring, pos) of
  *              each sequence, all different; NULL: row i.  A sequence whose row
  *              is outside 0..batch-1 is skipped and REPLAY_STATUS_BAD_PROMPT set.
