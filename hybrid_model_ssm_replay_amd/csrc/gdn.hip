@@ -1076,7 +1076,6 @@ __global__ __launch_bounds__(256) void gdn_encode_state(EncodeArgs a, StateBufs 
   const Shape &sh = a.s;
   const int tile = xcd_remap(blockIdx.x, gridDim.x);
   const int b = fdiv(tile, sh.fH), h = tile - b * sh.H;
-  if (a.mask && !a.mask[b]) return;
   const int DV = sh.P, rb0 = wave * RBW;
   const size_t head = ((size_t)b * sh.H + h) * DV * DK;
   float4 s[RBW][NCH];

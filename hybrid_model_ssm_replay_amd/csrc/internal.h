@@ -242,7 +242,6 @@ struct EncodeArgs {
   const float *src;         // [B][H][P][N] float32 state (GDN: P = d_v, N = d_k)
   const int32_t *ckpt_pos;  // current ckpt_pos[B] (stochastic-rounding counter)
   int write_ckpt;           // 0: write only the read copy
-  const uint8_t *mask;      // [B] or NULL: the sequences to encode
 };
 
 // Bytes of one stored copy of n elements with ncols state columns in all

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.h"
+#include "internal.h"
 
 namespace rssm {
 
@@ -180,6 +181,8 @@ struct ScanArgs {
 size_t scan_workspace(const ScanArgs &a);
 int launch_scan(const ScanArgs &a, hipStream_t st);
 void scan_plan(const ScanArgs &a, int32_t (&plan)[4]);  // see replay_scan_plan
+
+int launch_renew_read_copy(const Shape &s, const FormatBufs &f, const uint8_t *mask, hipStream_t st);
 
 int launch_gated_norm(const replay_gated_norm_args &a, hipStream_t st);
 

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "internal.h"
+#include "ops.h"
 
 using namespace rssm;
 
@@ -110,17 +111,6 @@ FormatBufs formats(const replay_ctx &ctx) {
 
 int hip_status(int e) { return e == 0 ? REPLAY_OK : REPLAY_EHIP; }
 
-// The read copy of a float32 checkpoint, for the sequences of the mask (NULL: all).
-int encode_read_copy(const replay_ctx &ctx, const uint8_t *mask, void *stream) {
-  EncodeArgs a{};
-  a.s = shape_of(ctx.cfg);
-  a.src = (const float *)ctx.buf.ckpt;
-  a.ckpt_pos = halves(ctx).ckpt_in;  // all zero after the init kernel
-  a.write_ckpt = 0;
-  a.mask = mask;
-  return launch_encode_state(a, formats(ctx), (hipStream_t)stream);
-}
-
 // The fields a call reads from its record argument are present and aligned;
 // with the records in the ring only Mamba-2 C and GDN q, v are read.
 bool rec_ok(const replay_record *r, int kind, bool in_ring = false) {
@@ -205,7 +195,12 @@ int replay_init(replay_ctx *ctx, const replay_config *cfg, const replay_buffers 
   if (e) return REPLAY_EHIP;
   if (cfg->ckpt_fmt == REPLAY_FMT_F32 && cfg->read_fmt != REPLAY_FMT_F32) {
     // The read copy starts as the encoding of the initial float32 checkpoint.
-    e = encode_read_copy(*ctx, nullptr, stream);
+    EncodeArgs a{};
+    a.s = shape_of(*cfg);
+    a.src = (const float *)buf->ckpt;
+    a.ckpt_pos = buf->pointers;  // half 0: all zero after the init kernel
+    a.write_ckpt = 0;
+    e = launch_encode_state(a, formats(*ctx), (hipStream_t)stream);
     if (e) return REPLAY_EHIP;
   }
   ctx->magic = kCtxMagic;
@@ -215,7 +210,7 @@ int replay_init(replay_ctx *ctx, const replay_config *cfg, const replay_buffers 
 int replay_renew_read_copy(replay_ctx *ctx, const uint8_t *seq_mask, void *stream) {
   if (check_ctx(ctx) != REPLAY_OK) return REPLAY_EINVAL;
   if (ctx->cfg.ckpt_fmt != REPLAY_FMT_F32 || ctx->cfg.read_fmt == REPLAY_FMT_F32) return REPLAY_ENOTSUP;
-  return hip_status(encode_read_copy(*ctx, seq_mask, stream));
+  return hip_status(launch_renew_read_copy(shape_of(ctx->cfg), formats(*ctx), seq_mask, (hipStream_t)stream));
 }
 
 int replay_set_state(replay_ctx *ctx, const float *state, void *stream) {

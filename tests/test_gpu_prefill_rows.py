@@ -102,3 +102,39 @@ def test_renewing_a_read_copy_refuses_other_formats():
         with pytest.raises(B.ReplayError) as e:
             B.replay_renew_read_copy(lay.ctx, None, 0)
         assert e.value.code == B.ENOTSUP
+
+
+@pytest.mark.parametrize("kind,rf", [("gdn", "FMT_F4E2M1_CS"), ("gdn", "FMT_F4E2M1_B16"), ("mamba2", "FMT_F4E2M1_B16")])
+@pytest.mark.parametrize("P", [64, 128])
+@pytest.mark.parametrize("rows", [[1, 4], None])
+def test_renewing_a_read_copy_is_set_state_of_the_masked_rows(kind, rf, P, rows):
+    import torch
+    from hybrid_model_ssm_replay_amd import binding as B
+    from hybrid_model_ssm_replay_amd.layer import ReplayLayer
+    announce("renew read copy", kind, rf, P, rows)
+    g = torch.Generator(device="cuda").manual_seed(P)
+    params = dict(A=-torch.ones(H, device="cuda"), D=torch.ones(H, device="cuda"), groups=G) if kind == "mamba2" else {}
+    make = lambda: ReplayLayer(kind, BATCH, H, P, N, 4, read_fmt=getattr(B, rf), **params)  # noqa: E731
+    lay, ref = make(), make()
+    state = torch.randn(BATCH, H, P, N, generator=g, device="cuda")
+    n = BATCH * H * P * N
+    scales = (n // 2 + 255) // 256 * 256
+    cols = (scales + n // 16 + 255) // 256 * 256
+
+    def parts(copy):
+        got = [copy[:n // 2].view(BATCH, -1), copy[scales:scales + n // 16].view(BATCH, -1)]
+        return got + ([copy[cols:cols + BATCH * H * N].view(BATCH, -1)] if rf == "FMT_F4E2M1_CS" else [])
+
+    ref.set_state(state)
+    lay.checkpoint.copy_(state)
+    lay.read_copy.fill_(0x5A)
+    mask = None
+    if rows is not None:
+        mask = torch.zeros(BATCH, dtype=torch.uint8, device="cuda")
+        mask[rows] = 1
+    B.replay_renew_read_copy(lay.ctx, None if mask is None else mask.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    mine = list(range(BATCH)) if rows is None else rows
+    others = [b for b in range(BATCH) if b not in mine]
+    for part, want in zip(parts(lay.read_copy), parts(ref.read_copy)):
+        assert torch.equal(part[mine], want[mine]) and bool((part[others] == 0x5A).all())
+    assert torch.equal(lay.checkpoint, state)
