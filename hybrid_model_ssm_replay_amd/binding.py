@@ -132,6 +132,8 @@ _SIG = {
     "replay_scan_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32]),
     "replay_scan_plan": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(replay_scan_layout)]),
     "replay_scan_prompt": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
+    "replay_delta_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "replay_delta_prompt": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
     "replay_gated_norm": (ctypes.c_int, [_P, _P]),
     "replay_accept_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "replay_accept_drafts": (ctypes.c_int, [_P, _P, _P]),
@@ -313,6 +315,17 @@ def replay_scan_prompt(cfg, prompt, rec, A: int, D: int, initial: int, state: in
                                                      initial, state, y, y_dtype, workspace, stream)
     if rc:
         _check("replay_scan_prompt", rc)
+
+
+def replay_delta_workspace_bytes(cfg, tokens: int, sequences: int, y_dtype: int) -> int:
+    return (_lib or load_library()).replay_delta_workspace_bytes(_by_address(cfg), tokens, sequences, y_dtype)
+
+
+def replay_delta_prompt(cfg, prompt, rec, initial: int, state: int, y: int, y_dtype: int, workspace: int, stream: int) -> None:
+    rc = (_lib or load_library()).replay_delta_prompt(_by_address(cfg), _by_address(prompt), _by_address(rec), initial, state,
+                                                      y, y_dtype, workspace, stream)
+    if rc:
+        _check("replay_delta_prompt", rc)
 
 
 def replay_gated_norm(args, stream: int) -> None:

@@ -19,6 +19,7 @@
 // and the order of a sum over a large vocabulary then moves a sampling border by
 // about 1e-13 of the total instead of 1e-4.
 #include "ops.h"
+#include "pieces.h"
 
 namespace rssm {
 namespace {
@@ -78,28 +79,6 @@ __device__ __forceinline__ Row row_of(const replay_accept_args &a, int b, int ac
 __device__ __forceinline__ double plain(float p) { return p > 0.f ? (double)p : 0.0; }
 __device__ __forceinline__ double residual(float p, float q) { return p > fmaxf(q, 0.f) ? (double)p - (double)fmaxf(q, 0.f) : 0.0; }
 
-// Moves of the low and high half of a double between lanes; lanes without a source get 0.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double moved(double v) {
-  const int2 w = __builtin_bit_cast(int2, v);
-  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, w.x, CTRL, ROWS, 0xF, false),
-                                              __builtin_amdgcn_update_dpp(0, w.y, CTRL, ROWS, 0xF, false)));
-}
-__device__ __forceinline__ double lane_value(double v, int lane) {  // lane: the same for the whole wave
-  const int2 w = __builtin_bit_cast(int2, v);
-  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(w.x, lane), __builtin_amdgcn_readlane(w.y, lane)));
-}
-// Inclusive prefix sum of a wave: within rows of 16 by shifts, then the last lane of a
-// row to the next row, and lane 31 to the upper half.
-__device__ __forceinline__ double scan64(double v) {
-  v += moved<0x111, 0xF>(v);
-  v += moved<0x112, 0xF>(v);
-  v += moved<0x114, 0xF>(v);
-  v += moved<0x118, 0xF>(v);
-  v += moved<0x142, 0xA>(v);
-  v += moved<0x143, 0xC>(v);
-  return v;
-}
 __device__ __forceinline__ double sum64(double v) { return lane_value(scan64(v), kWave - 1); }
 
 // The first lane whose running sum from `run` exceeds want, else the last with any

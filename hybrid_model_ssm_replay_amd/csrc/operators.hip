@@ -74,6 +74,25 @@ ScanArgs scan_args(const replay_config &c, int tokens, int sequences) {
   return a;
 }
 
+bool delta_cfg_ok(const replay_config *c) {
+  if (!c || c->kind != REPLAY_KIND_GDN) return false;
+  if (c->batch < 1 || c->heads < 1 || c->groups != c->heads) return false;
+  if (c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16) return false;
+  if (c->state_dim != 16 && c->state_dim != 32 && c->state_dim != 64 && c->state_dim != 128) return false;
+  // The kernels address a chunk's 64 rows of up to 4 bytes a value by 32 bits.
+  if ((int64_t)c->heads * c->head_dim >= kMostRow || (int64_t)c->heads * c->state_dim >= kMostRow) return false;
+  return (int64_t)c->batch * c->heads <= 0x7fffffffLL;
+}
+
+DeltaArgs delta_args(const replay_config &c, int tokens, int sequences, int y_dtype) {
+  DeltaArgs a{};
+  a.H = c.heads, a.P = c.head_dim, a.N = c.state_dim;
+  a.bf16 = (c.flags & REPLAY_FLAG_BF16_RECORDS) ? 1 : 0;
+  a.y_bf16 = y_dtype == REPLAY_DT_BF16;
+  a.p.tokens = tokens, a.p.n = sequences, a.p.batch = c.batch;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,6 +147,30 @@ int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, co
   if (rec) a.x = rec->f0, a.Bm = rec->f1, a.Cm = rec->f2, a.dt = rec->f3;
   a.A = A, a.D = D, a.initial = initial, a.state = state, a.y = y, a.workspace = workspace;
   return hip_status(launch_scan(a, (hipStream_t)stream));
+}
+
+size_t replay_delta_workspace_bytes(const replay_config *cfg, int32_t tokens, int32_t sequences, int32_t y_dtype) {
+  if (!delta_cfg_ok(cfg) || tokens < 0 || tokens > kMost || sequences < 1 || sequences > cfg->batch || sequences > kMost ||
+      !dtype_ok(y_dtype) || (y_dtype == REPLAY_DT_BF16 && !(cfg->flags & REPLAY_FLAG_BF16_RECORDS)))
+    return 0;
+  return delta_workspace(delta_args(*cfg, tokens, sequences, y_dtype));
+}
+
+int replay_delta_prompt(const replay_config *cfg, const replay_prompt *prompt, const replay_record *rec,
+                        const float *initial, float *state, void *y, int32_t y_dtype, void *workspace, void *stream) {
+  if (!delta_cfg_ok(cfg) || !prompt_ok(prompt, cfg->batch)) return REPLAY_EINVAL;
+  if (!state || !aligned16(state) || !aligned16(initial) || !dtype_ok(y_dtype)) return REPLAY_EINVAL;
+  DeltaArgs a = delta_args(*cfg, prompt->tokens, prompt->sequences, y_dtype);
+  if (a.y_bf16 && !a.bf16) return REPLAY_ENOTSUP;
+  if (prompt->tokens > 0) {
+    if (!rec || !rec->f0 || !rec->f1 || !rec->f2 || !rec->f3 || !rec->f4 || !y) return REPLAY_EINVAL;
+    if (!aligned16(rec->f0) || !aligned16(rec->f1) || !aligned16(rec->f2) || !aligned16(y)) return REPLAY_EINVAL;
+  }
+  if (delta_workspace(a) && (!workspace || ((uintptr_t)workspace & 255u))) return REPLAY_EINVAL;
+  a.p = packed_of(*prompt, cfg->batch);
+  if (rec) a.q = rec->f0, a.k = rec->f1, a.v = rec->f2, a.alpha = rec->f3, a.beta = rec->f4;
+  a.initial = initial, a.state = state, a.y = y, a.workspace = workspace;
+  return hip_status(launch_delta(a, (hipStream_t)stream));
 }
 
 int replay_gated_norm(const replay_gated_norm_args *a, void *stream) {

@@ -1,6 +1,6 @@
 // Shared parts of the operators around the recurrence (short convolution,
-// prompt scan, gated norm, draft acceptance): packed sequences, element types,
-// launch declarations.
+// prompts of both families, norms, draft acceptance, log probabilities): packed
+// sequences, element types, launch declarations.
 #pragma once
 
 #include "common.h"
@@ -181,6 +181,18 @@ struct ScanArgs {
 size_t scan_workspace(const ScanArgs &a);
 int launch_scan(const ScanArgs &a, hipStream_t st);
 void scan_plan(const ScanArgs &a, int32_t (&plan)[4]);  // see replay_scan_plan
+
+struct DeltaArgs {
+  int H, P, N, bf16, y_bf16;  // P rows (v), N columns (k, q) of a head's state
+  Packed p;
+  const void *q, *k, *v;
+  const float *alpha, *beta, *initial;
+  float *state;
+  void *y;
+  void *workspace;
+};
+size_t delta_workspace(const DeltaArgs &a);
+int launch_delta(const DeltaArgs &a, hipStream_t st);
 
 int launch_renew_read_copy(const Shape &s, const FormatBufs &f, const uint8_t *mask, hipStream_t st);
 

@@ -46,15 +46,11 @@
 // take 60), 24 prompts of 16384 tokens with float32 outputs 398 to 403
 // us (1.1 GB, 211 us).
 #include "ops.h"
+#include "pieces.h"
 
 namespace rssm {
 namespace {
 
-typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kThreads = 256;
@@ -80,21 +76,7 @@ __device__ __forceinline__ int in_row_x(int row, int c) {
 // .. + 3 and 32 k + 16 + 4 q .. + 3, and is read whole by 16 rows at a time.
 __device__ __forceinline__ int in_row_c(int row, int k, int q) { return ((4 * k + q) ^ (row & 15)) << 4; }
 
-union Frag {  // eight bf16 of one lane: an operand of the 16x16x32 product
-  s16x8 v;
-  s16x4 h[2];
-  uint32_t w[4];
-};
-
-__device__ __forceinline__ floatx4 mfma32(const Frag &a, const Frag &b, floatx4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
-}
-
 __device__ __forceinline__ s16x4 read_tr(const char *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
-
-__device__ __forceinline__ float upper(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ float lower(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
 
 // A value all lanes share, in a scalar register.
 __device__ __forceinline__ float uniform(float v) {
@@ -105,31 +87,6 @@ __device__ __forceinline__ float uniform(float v) {
 __device__ __forceinline__ int again(int v) {
   asm volatile("" : "+v"(v));
   return v;
-}
-
-// A buffer of n bytes: loads past its end give zeros, stores past it do nothing.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, size_t n) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)n, 0x00020000);
-}
-__device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t b, int at, int plus) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, at, plus, 0));
-}
-
-// Two values as MP words of bf16 pairs: two pieces round to nearest (together within
-// 2^-16 of the value), three pieces cut (8 bits each: the 24 bits of the value).
-template <int MP>
-__device__ __forceinline__ void pieces(float a, float b, uint32_t (&w)[MP]) {
-  static_assert(MP == 2 || MP == 3);
-  if constexpr (MP == 2) {
-    w[0] = pack_bf16(a, b);
-    w[1] = pack_bf16(a - lower(w[0]), b - upper(w[0]));
-  } else {
-#pragma unroll
-    for (int u = 0; u < MP; ++u) {
-      w[u] = __builtin_amdgcn_perm(bits(b), bits(a), 0x07060302u);  // the upper halves, b's on top
-      if (u + 1 < MP) a -= upper(bits(a)), b -= upper(bits(b));
-    }
-  }
 }
 
 // Eight neighbouring elements of a record on their way to a granule of LDS: as

@@ -177,20 +177,22 @@ class ReplayLayer:
 
     def prefill(self, rec: dict, seq_start: torch.Tensor, rows: torch.Tensor | None = None,
                 resume: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
-        """Run packed prompts (Mamba-2): y for every token, [tokens, heads, head_dim];
-        the layer's next step of a prompted sequence continues behind its last token.
+        """Run packed prompts: y for every token, [tokens, heads, head_dim]; the layer's
+        next step of a prompted sequence continues behind its last token.
 
-        rec: x [tokens, heads, head_dim], B and C [tokens, groups, state_dim], dt
-        [tokens, heads]; seq_start, rows, resume, out_dtype as for ``ops.scan_prompt``,
-        whose resumed sequences continue from their state here, the records of their
-        window included.  The windows of prompted sequences are emptied; the others
-        are left alone, except for drafts still pending, which are discarded as by a
-        step.  Positions do not move.  The state is computed in float32 and stored in
-        the layer's formats; where the checkpoint itself is in a lower one, prompts
-        are for the whole batch (rows None) and resume is not possible."""
+        rec: Mamba-2 x [tokens, heads, head_dim], B and C [tokens, groups, state_dim], dt
+        [tokens, heads]; Gated DeltaNet q, k [tokens, heads, state_dim], v [tokens, heads,
+        head_dim], alpha, beta [tokens, heads]; seq_start, rows, resume, out_dtype as for
+        ``ops.scan_prompt`` and ``ops.delta_prompt``, whose resumed sequences continue from
+        their state here, the records of their window included.  The windows of prompted
+        sequences are emptied; the others are left alone, except for drafts still pending,
+        which are discarded as by a step.  Positions do not move.  The state is computed in
+        float32 and stored in the layer's formats; where the checkpoint itself is in a lower
+        one, prompts are for the whole batch (rows None) and resume is not possible."""
         s = self.shapes
-        if s.kind != B.KIND_MAMBA2:
-            raise ValueError("prompts are for Mamba-2 layers")
+        names = _FIELDS[s.kind]
+        if s.kind == B.KIND_GDN and any(f not in rec for f in names):
+            raise ValueError("a Gated DeltaNet layer's prompts are q, k, v, alpha and beta (x, B, C and dt are a Mamba-2 layer's)")
         if not isinstance(seq_start, torch.Tensor) or seq_start.dim() != 1 or seq_start.shape[0] < 2:
             raise ValueError("seq_start must be int32 [sequences + 1], on the device")
         n = seq_start.shape[0] - 1
@@ -198,22 +200,25 @@ class ReplayLayer:
             raise ValueError(f"{n} prompts for {s.batch} sequences")
         if rows is not None and not (rows.is_cuda and rows.dtype == torch.int32 and tuple(rows.shape) == (n,)):
             raise ValueError("rows must be an int32 device tensor [sequences]")
-        if rec["x"].dtype is not s.vec_dtype:
-            raise ValueError(f"x must be {s.vec_dtype}, the type of the layer's records")
+        if rec[names[0]].dtype is not s.vec_dtype:
+            raise ValueError(f"{names[0]} must be {s.vec_dtype}, the type of the layer's records")
         f32 = self.cfg.ckpt_fmt == B.FMT_F32
         if not f32 and (resume is not None or rows is not None or n != s.batch):
             raise ValueError("with a checkpoint below float32, prompts are for the whole batch, in order, and from zero")
-        s.record(rec, (rec["x"].shape[0],))
+        s.record(rec, (rec[names[0]].shape[0],))
         state = self.checkpoint if f32 else torch.empty(
             (s.batch, s.heads, s.head_dim, s.state_dim), dtype=torch.float32, device=self.ckpt.device)
-        at, args, y, _ = ops.scan_call(rec["x"], rec["B"], rec["C"], rec["dt"], self.A, self.D, seq_start, state,
-                                       None if resume is None else state, rows, resume, out_dtype, self.status_word)
+        more = (seq_start, state, None if resume is None else state, rows, resume, out_dtype, self.status_word)
+        if s.kind == B.KIND_MAMBA2:
+            run, (at, args, y, _) = B.replay_scan_prompt, ops.scan_call(rec["x"], rec["B"], rec["C"], rec["dt"], self.A, self.D, *more)
+        else:
+            run, (at, args, y, _) = B.replay_delta_prompt, ops.delta_call(*(rec[f] for f in names), *more)
         # Everything has been looked at: a call that raises leaves the layer as it was.
         each = torch.arange(s.batch, device=self.ckpt.device)
         mask = each < n if rows is None else (each[:, None] == rows[None, :]).any(1)
         mask = None if rows is None and n == s.batch else mask.to(torch.uint8)
         self.flush(mask)
-        ops.launch(B.replay_scan_prompt, at, *args)
+        ops.launch(run, at, *args)
         if not f32:
             self.set_state(state)
         elif self.read_copy is not None:

@@ -212,6 +212,54 @@ def scan_call(x, Bm, Cm, dt, A, D, seq_start, state, initial, rows, resume, out_
     return at, args, y, ws
 
 
+def delta_prompt(q, k, v, alpha, beta, seq_start, state, *, initial=None, rows=None, resume=None, out_dtype=None,
+                 status=None):
+    """The Gated DeltaNet recurrence over packed prompts: o for every token of a sequence (other
+    rows are not written), and the state after the last.
+
+    q, k [tokens, heads, state_dim] and v [tokens, heads, head_dim], all float32 or all
+    bfloat16; alpha in [0, 1] and beta float32 [tokens, heads]; state float32 [batch,
+    heads, head_dim, state_dim]; everything else as for ``scan_prompt``."""
+    at, args, y, _ = delta_call(q, k, v, alpha, beta, seq_start, state, initial, rows, resume, out_dtype, status)
+    launch(B.replay_delta_prompt, at, *args)
+    return y
+
+
+def delta_call(q, k, v, alpha, beta, seq_start, state, initial, rows, resume, out_dtype, status):
+    """delta_prompt up to its launch, which then refuses nothing: (device index, arguments, y, workspace)."""
+    at = _vectors(q, "q", 3)
+    tokens, H, N = q.shape
+    dtype = q.dtype
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("v must be [tokens, heads, head_dim], on the device")
+    P = v.shape[2]
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be float32 [batch, heads, head_dim, state_dim], on the device")
+    batch = state.shape[0]
+    out_dtype = _F32 if out_dtype is None else out_dtype
+    if out_dtype not in _DT:
+        raise ValueError(f"out_dtype {out_dtype} is not float32 or bfloat16")
+    if out_dtype is _BF16 and dtype is _F32:
+        raise ValueError("bfloat16 outputs are for bfloat16 inputs")
+    if initial is None and resume is not None:
+        raise ValueError("resume needs initial")
+    qs, ks, vs = (_check(q, "q", dtype, (tokens, H, N), at), _check(k, "k", dtype, (tokens, H, N), at),
+                  _check(v, "v", dtype, (tokens, H, P), at))
+    rec = _RECORD(qs, ks, vs, _check(alpha, "alpha", _F32, (tokens, H), at), _check(beta, "beta", _F32, (tokens, H), at))
+    to = _check(state, "state", _F32, (batch, H, P, N), at)
+    start = 0 if initial is None else to if initial is state else _check(initial, "initial", _F32, (batch, H, P, N), at)
+    if tokens > 1 << 30 or H * P >= 1 << 23 or H * N >= 1 << 23:
+        raise ValueError(f"{tokens} tokens of {H} x {P} and {H} x {N} values: at most 2^30, below 2^23 and below 2^23")
+    if (qs | ks | vs | to | start) & 15:
+        raise ValueError("q, k, v, state and initial must start at multiples of 16 bytes")
+    prompt, n = _prompt(tokens, seq_start, rows, resume, status, at)
+    cfg = _CONFIG(B.KIND_GDN, batch, H, H, P, N, 1, 0, 0, 0, 0, B.FLAG_BF16_RECORDS if dtype is _BF16 else 0, 0)
+    nbytes = B.replay_delta_workspace_bytes(cfg, tokens, n, _DT[out_dtype])
+    y = v.new_empty(tokens, H, P, dtype=out_dtype)
+    ws = q.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    return at, (cfg, prompt, rec, start, to, y.data_ptr(), _DT[out_dtype], ws.data_ptr() if nbytes else 0), y, ws
+
+
 def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=None):
     """RMS norm over groups of ``group`` channels with the gate silu(z), per token.
 

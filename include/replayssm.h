@@ -465,6 +465,21 @@ int replay_scan_prompt(const replay_config *cfg, const replay_prompt *prompt, co
                        const float *A, const float *D, const float *initial, float *state, void *y, int32_t y_dtype,
                        void *workspace, void *stream);
 
+/* The Gated DeltaNet recurrence over packed prompts, S <- alpha S (I - beta k k^T)
+ * + beta v k^T, o = S q for every token of every sequence.  cfg gives kind (GDN),
+ * batch, heads (= groups), head_dim (d_v), state_dim (d_k) and
+ * REPLAY_FLAG_BF16_RECORDS; window, max_draft and formats are ignored; heads *
+ * head_dim and heads * state_dim are below 2^23.  rec: q, k [tokens][heads][d_k],
+ * v [tokens][heads][d_v], alpha in [0, 1] (0 forgets everything before), beta
+ * [tokens][heads], as for a step.  initial, state and y as for
+ * replay_scan_prompt ([batch][heads][d_v][d_k]; y [tokens][heads][d_v]), with the
+ * same precision of y and the same reach of a NaN or infinity.
+ *   workspace  replay_delta_workspace_bytes bytes (256-byte aligned), or NULL
+ *              when that is 0. */
+size_t replay_delta_workspace_bytes(const replay_config *cfg, int32_t tokens, int32_t sequences, int32_t y_dtype);
+int replay_delta_prompt(const replay_config *cfg, const replay_prompt *prompt, const replay_record *rec,
+                        const float *initial, float *state, void *y, int32_t y_dtype, void *workspace, void *stream);
+
 /* The gated norm behind the recurrence, over groups of `group` consecutive
  * channels (channels % group == 0), per token:
  *   gate first (norm_first 0):  h = y silu(z),  out = w h / sqrt(mean(h^2) + eps)

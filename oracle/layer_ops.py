@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import mamba2
+from . import gdn, mamba2
 
 
 def silu(v):
@@ -50,6 +50,23 @@ def scan(x, B, C, dt, A, D, S0=None):
         S, y[t] = mamba2.step(S, x[t], B[t], C[t], dt[t], A, D)
         Sa, size[t] = mamba2.step(Sa, np.abs(x[t]), np.abs(B[t]), np.abs(C[t]), dt[t], A, np.abs(D))
     return y, S, size, Sa
+
+
+def delta(q, k, v, alpha, beta, S0=None):
+    """The Gated DeltaNet recurrence over one sequence: q, k [n, H, N], v [n, H, P], alpha, beta [n, H].
+
+    Returns (o [n, H, P], S [H, P, N] after the last token, size [H, P]: the largest Euclidean
+    norm that a row of the state has on the way, plus the largest |v| of the row).  For keys and
+    queries of length 1, factors alpha (I - beta k k^T) of norm at most 1, what a product with
+    the state sums is no longer than that, and an error in a row does not grow."""
+    n, H, N = k.shape
+    P = v.shape[-1]
+    S = np.zeros((H, P, N)) if S0 is None else np.asarray(S0, np.float64)
+    o, size = np.zeros((n, H, P)), np.linalg.norm(S, axis=-1)
+    for t in range(n):
+        S, o[t] = gdn.step(S, q[t], k[t], v[t], alpha[t], beta[t])
+        size = np.maximum(size, np.linalg.norm(S, axis=-1))
+    return o, S, size + (np.abs(v).max(0) if n else 0.0)
 
 
 def gated_norm(y, z, weight, group, eps, norm_first):
