@@ -42,10 +42,7 @@ struct Cell {
   static constexpr int MP = sizeof(Y) == 4 ? 3 : 2;  // pieces of P, U and S in the output products
   static constexpr int A0 = 0;                       // [3][kSteps]
   static constexpr int P0 = A0 + 3 * kSteps * kFrag;     // [MP][kSteps]
-  static constexpr int KT0 = P0 + MP * kSteps * kFrag;   // [IP][2 NK tiles of k's columns][2 steps]
-  static constexpr int K0 = KT0 + IP * 4 * NK * kFrag;   // [IP][4 token tiles][NK], float32 records only
-  static constexpr int Q0 = K0 + (IP == 3 ? IP * 4 * NK * kFrag : 0);
-  static constexpr int G0 = Q0 + (IP == 3 ? IP * 4 * NK * kFrag : 0);  // e^{g_t} [64], e^{g_C - g_t} [64]
+  static constexpr int G0 = P0 + MP * kSteps * kFrag;    // e^{g_t} [64], e^{g_C - g_t} [64]
   static constexpr int BYTES = G0 + 2 * Q * 4;
 };
 
@@ -57,19 +54,20 @@ struct DeltaPlan {
   char *cells;     // [hi - lo][H] of Cell
 };
 
-// Rows of a record, eight neighbouring columns a lane, as an operand in IP pieces.
+// Eight neighbouring columns of a record's row: as loaded, and as an operand in IP pieces.
 template <typename R>
-struct Rows;
-template <>
-struct Rows<bf16_t> {
-  static __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, Frag (&f)[1]) {
-    f[0].v = __builtin_bit_cast(s16x8, buffer_load16(b, at, 0));
-  }
+struct Rows {
+  uint4 v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, int plus) { v = buffer_load16(b, at, plus); }
+  __device__ __forceinline__ void cut(Frag (&f)[1]) const { f[0].v = __builtin_bit_cast(s16x8, v); }
 };
 template <>
 struct Rows<float> {
-  static __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, Frag (&f)[3]) {
-    const uint4 v = buffer_load16(b, at, 0), w = buffer_load16(b, at, 16);
+  uint4 v, w;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, int plus) {
+    v = buffer_load16(b, at, plus), w = buffer_load16(b, at, plus + 16);
+  }
+  __device__ __forceinline__ void cut(Frag (&f)[3]) const {
     const uint32_t e[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -90,12 +88,16 @@ __device__ __forceinline__ Frag get(const char *from, int lane) {
 
 constexpr int kT = Q + 4;  // floats of a row of T and A in LDS
 
+// v where `keep`, else 0: a mask, since a condition would become a branch around v.
+__device__ __forceinline__ float only(float v, bool keep) { return __uint_as_float(bits(v) & (keep ? ~0u : 0u)); }
+
 template <typename R, typename Y, int NK>
-__global__ __launch_bounds__(kThreads) void cells_k(DeltaArgs a, DeltaPlan plan) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(R) == 4 ? 2 : 4)))
+void cells_k(DeltaArgs a, DeltaPlan plan) {
   typedef Cell<R, Y, NK> C;
   constexpr int IP = C::IP, MP = C::MP;
   __shared__ __attribute__((aligned(16))) float sT[Q * kT], sA[Q * kT], sD[kWaves][16][20], sB[Q];
-  __shared__ double sG[Q];
+  __shared__ __attribute__((aligned(16))) double sG[Q];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane % 16, q = lane / 16;
   const int place = fdiv(blockIdx.x, plan.fH), h = blockIdx.x - place * a.H;
@@ -109,172 +111,149 @@ __global__ __launch_bounds__(kThreads) void cells_k(DeltaArgs a, DeltaPlan plan)
   // Decays: lane = token; past the end a = 1 and b = 0.  A decay of zero forgets everything.
   const int tl = min(lane, rem - 1);
   const float al = a.alpha[(row0 + tl) * a.H + h], be = a.beta[(row0 + tl) * a.H + h];
-  double g = lane < rem ? log2((double)al) : 0.0;
-  g = scan64(g < -4096.0 ? -4096.0 : g);
-  const double gC = lane_value(g, kWave - 1);
-  if (wave == 0) {
-    sG[lane] = g;
-    sB[lane] = lane < rem ? be : 0.f;
-    float *const e = reinterpret_cast<float *>(cell + C::G0);
-    e[lane] = __builtin_amdgcn_exp2f((float)g);
-    e[Q + lane] = __builtin_amdgcn_exp2f((float)(gC - g));
-  }
-  __syncthreads();
-
-  // P^T of this wave's rows of 16 tokens, G^T = (K K^T)^T of the rows 3 - wave.
-  const int wg = 3 - wave;
   const int64_t rK = (int64_t)a.H * N;
   const size_t nK = (size_t)((rem - 1) * rK + N) * sizeof(R);
   const auto bK = buffer_of((const R *)a.k + row0 * rK + (int64_t)h * N, nK);
   const auto bQ = buffer_of((const R *)a.q + row0 * rK + (int64_t)h * N, nK);
+  const int oK = (int)((r * rK + 8 * q) * sizeof(R)), tile = (int)(16 * rK * sizeof(R));
+  auto at = [&](int s) { return NK > 1 || 8 * q < N ? oK + 32 * s * (int)sizeof(R) : kNowhere; };
+
+  // P^T of this wave's rows of 16 tokens, G^T = (K K^T)^T of the rows 3 - wave; all four
+  // tiles of a row, of which those right of the diagonal are masked away.
+  const int wg = 3 - wave;
   floatx4 aP[4], aG[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) aP[j] = aG[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
+#pragma unroll IP == 1 ? NK : 1
   for (int s = 0; s < NK; ++s) {
-    const int c = 32 * s + 8 * q;
-    auto at = [&](int tile) { return c < N ? (int)(((16 * tile + r) * rK + c) * sizeof(R)) : kNowhere; };
+    Rows<R> rk[4], rq, rg;
     Frag k[4][IP], qf[IP], kg[IP];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) Rows<R>::load(bK, at(j), k[j]);
-    Rows<R>::load(bQ, at(wave), qf);
-    Rows<R>::load(bK, at(wg), kg);
+    for (int j = 0; j < 4; ++j) rk[j].load(bK, at(s), j * tile);
+    rq.load(bQ, at(s), wave * tile);
+    rg.load(bK, at(s), wg * tile);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rk[j].cut(k[j]);
+    rq.cut(qf), rg.cut(kg);
 #pragma unroll
     for (int u = IP - 1; u >= 0; --u)
 #pragma unroll
       for (int v = IP - 1 - u; v >= 0; --v)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j <= wave) aP[j] = mfma32(k[j][u], qf[v], aP[j]);
-          if (j <= wg) aG[j] = mfma32(k[j][u], kg[v], aG[j]);
+          aP[j] = mfma32(k[j][u], qf[v], aP[j]);
+          aG[j] = mfma32(k[j][u], kg[v], aG[j]);
         }
-    // K^T of column tile 2 s + half: the products of K's rows with the unit vectors give
-    // its values (one factor is 1, the others 0) with a column a lane.
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if ((2 * s + half) % kWaves != wave) continue;
-      Frag one;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c0 = 8 * q + 2 * i - 16 * half;
-        one.w[i] = (c0 == r ? 0x3F80u : 0u) | (c0 + 1 == r ? 0x3F800000u : 0u);
-      }
-#pragma unroll
-      for (int u = 0; u < IP; ++u)
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts) {
-          Frag f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const floatx4 x = mfma32(k[2 * ts + e][u], one, floatx4{0.f, 0.f, 0.f, 0.f});
-            f.w[2 * e] = __builtin_amdgcn_perm(bits(x[1]), bits(x[0]), 0x07060302u);
-            f.w[2 * e + 1] = __builtin_amdgcn_perm(bits(x[3]), bits(x[2]), 0x07060302u);
-          }
-          put(cell + C::KT0 + ((u * 2 * NK + 2 * s + half) * 2 + ts) * kFrag, lane, f);
-        }
-    }
-    if constexpr (IP == 3) {
-#pragma unroll
-      for (int u = 0; u < IP; ++u) {
-        put(cell + C::Q0 + ((u * 4 + wave) * NK + s) * kFrag, lane, qf[u]);
-        put(cell + C::K0 + ((u * 4 + wg) * NK + s) * kFrag, lane, kg[u]);
-      }
-    }
   }
+  if (wave == 0) {
+    double g = lane < rem ? (double)log2f(al) : 0.0;
+    g = scan64(g < -4096.0 ? -4096.0 : g);
+    sG[lane] = g;
+    sB[lane] = lane < rem ? be : 0.f;
+    float *const e = reinterpret_cast<float *>(cell + C::G0);
+    e[lane] = __builtin_amdgcn_exp2f((float)g);
+    e[Q + lane] = __builtin_amdgcn_exp2f((float)(lane_value(g, kWave - 1) - g));
+  }
+  __syncthreads();
   {
     const double gt = sG[16 * wave + r], gg = sG[16 * wg + r];
     const float bt = sB[16 * wg + r];
-    Frag f[2][MP];
+    char *const to = cell + C::P0 + step_of(wave, 0) * kFrag;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float p[4], t[4];
+    for (int s = 0; s < 2; ++s) {
+      Frag f[MP];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 16 * j + 4 * q + i;
-        const double gj = sG[tok];
-        p[i] = tok <= 16 * wave + r ? aP[j][i] * __builtin_amdgcn_exp2f((float)(gt - gj)) : 0.f;
-        t[i] = tok < 16 * wg + r ? bt * (aG[j][i] * __builtin_amdgcn_exp2f((float)(gg - gj))) : 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const int j = 2 * s + e;
+        float p[4], t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 16 * j + 4 * q + i;
+          const double gj = sG[tok];
+          p[i] = only(aP[j][i] * __builtin_amdgcn_exp2f((float)(gt - gj)), tok <= 16 * wave + r);
+          t[i] = only(bt * (aG[j][i] * __builtin_amdgcn_exp2f((float)(gg - gj))), tok < 16 * wg + r);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[MP];
+          pieces<MP>(p[2 * i], p[2 * i + 1], w);
+#pragma unroll
+          for (int u = 0; u < MP; ++u) f[u].w[2 * e + i] = w[u];
+        }
+        st4(sT + (16 * wg + r) * kT + 16 * j + 4 * q, make_float4(t[0], t[1], t[2], t[3]));
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[MP];
-        pieces<MP>(p[2 * i], p[2 * i + 1], w);
-#pragma unroll
-        for (int u = 0; u < MP; ++u) f[j / 2][u].w[j % 2 * 2 + i] = w[u];
-      }
-      st4(sT + (16 * wg + r) * kT + 16 * j + 4 * q, make_float4(t[0], t[1], t[2], t[3]));
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
       if (s <= wave / 2) {
 #pragma unroll
-        for (int u = 0; u < MP; ++u) put(cell + C::P0 + (u * kSteps + step_of(wave, s)) * kFrag, lane, f[s][u]);
+        for (int u = 0; u < MP; ++u) put(to + (u * kSteps + s) * kFrag, lane, f[u]);
       }
+    }
   }
   __syncthreads();
 
-  // Column r of the inverse of the diagonal block `wave`, by substitution.
-  float x[16];
+  // Column r of the inverse of the diagonal block `wave`, by substitution, in every 16 lanes.
+  {
+    float x[16];
+    const float *const T = sT + 16 * wave * kT + 16 * wave;
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    x[t] = t == r ? 1.f : 0.f;
-    const float *const row = sT + (16 * wave + t) * kT + 16 * wave;
+    for (int t = 0; t < 16; ++t) {
+      x[t] = t == r ? 1.f : 0.f;
+      if (t % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // not all rows' loads at once
 #pragma unroll
-    for (int s4 = 0; s4 < t; s4 += 4) {
-      const float4 tv = ld4(row + s4);
+      for (int s4 = 0; s4 < t; s4 += 4) {
+        const float4 tv = ld4(T + t * kT + s4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (s4 + i < t) x[t] = fmaf(-f4get(tv, i), x[s4 + i], x[t]);
+        for (int i = 0; i < 4; ++i)
+          if (s4 + i < t) x[t] = fmaf(-f4get(tv, i), x[s4 + i], x[t]);
+      }
+    }
+    if (q == 0) {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) sD[wave][t][r] = x[t];
     }
   }
-  floatx4 X[4];  // block column `wave` of the inverse: rows 16 i + 4 q + e, column r
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    X[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i == wave) X[i][e] = q == 0 ? x[e] : q == 1 ? x[4 + e] : q == 2 ? x[8 + e] : x[12 + e];
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sD[wave][4 * q + e][r] = q == 0 ? x[e] : q == 1 ? x[4 + e] : q == 2 ? x[8 + e] : x[12 + e];
   __syncthreads();
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    if (i <= wave) continue;
-    floatx4 acc = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int m = 0; m < i; ++m) {
-      if (m < wave) continue;
-      const float4 tv = ld4(sT + (16 * i + r) * kT + 16 * m + 4 * q);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc = mfma_16x16x4(f4get(tv, e), X[m][e], acc);
-    }
-    const float4 dv = ld4(&sD[i][r][4 * q]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) X[i] = mfma_16x16x4(-f4get(dv, e), acc[e], X[i]);
-  }
+  // Block column `wave` of the inverse, tile d below the diagonal: rows 16 (wave + d) + 4 q + e, column r.
+  floatx4 X[4];
   const float bj = sB[16 * wave + r];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int e = 0; e < 4; ++e) X[0][e] = sD[wave][4 * q + e][r];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sA[(16 * i + 4 * q + e) * kT + 16 * wave + r] = X[i][e] * bj;
+  for (int d = 0; d < 4; ++d) {
+    if (wave + d >= 4) break;
+    if (d > 0) {
+      floatx4 acc = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < d; ++m) {
+        const float4 tv = ld4(sT + (16 * (wave + d) + r) * kT + 16 * (wave + m) + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = mfma_16x16x4(f4get(tv, e), X[m][e], acc);
+      }
+      const float4 dv = ld4(&sD[wave + d][r][4 * q]);
+      X[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) X[d] = mfma_16x16x4(-f4get(dv, e), acc[e], X[d]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sA[(16 * (wave + d) + 4 * q + e) * kT + 16 * wave + r] = X[d][e] * bj;
+  }
   __syncthreads();
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (s <= wave / 2) {
-      Frag f[3];
+  for (int s = 0; s < 2; ++s) {
+    if (s > wave / 2) break;
+    Frag f[3];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 v = ld4(sA + (16 * wave + r) * kT + 32 * s + 16 * e + 4 * q);
-        uint32_t w0[3], w1[3];
-        pieces<3>(v.x, v.y, w0);
-        pieces<3>(v.z, v.w, w1);
+    for (int e = 0; e < 2; ++e) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (2 * s + e <= wave) v = ld4(sA + (16 * wave + r) * kT + 32 * s + 16 * e + 4 * q);
+      uint32_t w0[3], w1[3];
+      pieces<3>(v.x, v.y, w0);
+      pieces<3>(v.z, v.w, w1);
 #pragma unroll
-        for (int u = 0; u < 3; ++u) f[u].w[2 * e] = w0[u], f[u].w[2 * e + 1] = w1[u];
-      }
-#pragma unroll
-      for (int u = 0; u < 3; ++u) put(cell + C::A0 + (u * kSteps + step_of(wave, s)) * kFrag, lane, f[u]);
+      for (int u = 0; u < 3; ++u) f[u].w[2 * e] = w0[u], f[u].w[2 * e + 1] = w1[u];
     }
+#pragma unroll
+    for (int u = 0; u < 3; ++u) put(cell + C::A0 + (u * kSteps + step_of(wave, 0) + s) * kFrag, lane, f[u]);
+  }
 }
 
 // Four float32 values in a row of 16-bit places, NP pieces `gap` bytes apart.
@@ -287,14 +266,26 @@ __device__ __forceinline__ void hand(char *to, int gap, const floatx4 &v) {
   for (int u = 0; u < NP; ++u) *reinterpret_cast<uint2 *>(to + u * gap) = make_uint2(a[u], b[u]);
 }
 
+// Byte of a granule of eight columns in its row of K in LDS, permuted so that neither the
+// writes (16 rows at a granule) nor the transposing reads (eight rows at two granules) meet
+// in a bank (rows of 128 and 64 bytes: the reads).
+template <int NK>
+__device__ __forceinline__ int granule(int row, int g) {
+  return (g ^ (NK == 4 ? 2 * (row & 7) | (row >> 3 & 1) : NK == 2 ? row & 6 : row >> 1 & 2)) * 16;
+}
+
+// Waves 0 to 3 carry the state, waves 4 to 7 make the outputs; wave w of either has the
+// chunk's tokens 16 w .. + 15.
 template <typename R, typename Y, int NK, int CT>
-__global__ __launch_bounds__(kThreads) void chain_k(DeltaArgs a, DeltaPlan plan) {
+__global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan plan) {
   typedef Cell<R, Y, NK> C;
   constexpr int IP = C::IP, MP = C::MP, COLS = 16 * CT;
-  constexpr int MT = NK == 4 ? 2 : 1;            // tiles of the state's columns that a wave has
+  constexpr int MT = NK == 4 ? 2 : 1;                // tiles of the state's columns that a wave has
   constexpr int SR = 64 * NK + 16, TR = 2 * Q + 16;  // bytes of a row of S, and of 64 tokens, in LDS
+  constexpr int KR = 64 * NK;                        // bytes of a row of K in LDS
   __shared__ __attribute__((aligned(16))) char sS[3][COLS * SR], sR[3][COLS * TR], sW[3][COLS * TR], sU[MP][COLS * TR];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  __shared__ __attribute__((aligned(16))) char sK[IP][Q * KR];
+  const int tid = threadIdx.x, lane = tid % kWave, eighth = __builtin_amdgcn_readfirstlane(tid / kWave), wave = eighth % 4;
   const int r = lane % 16, q = lane / 16;
   // Unit u, a sequence's head, on XCD u % 8: its slices share what cells_k left in an L2.
   const int k8 = blockIdx.x / kXcds, u8 = fdiv(k8, plan.fny);
@@ -310,200 +301,284 @@ __global__ __launch_bounds__(kThreads) void chain_k(DeltaArgs a, DeltaPlan plan)
   const int row = batch_row(a.p, seq, h == 0 && slice == 0 && tid == 0 && c0 == 0);
   if (row < 0) return;
 
-  // The state, transposed: tile m of this wave, columns 16 (wave + 4 m) + 4 q + i of k, row r of the slice's tile.
-  floatx4 S[MT][CT];
-  auto there = [&](int m) { return wave + 4 * m < 2 * NK; };
-  const size_t tile0 = ((size_t)row * a.H + h) * P * N + (size_t)(slice * COLS + r) * N + 16 * wave + 4 * q;
-  const bool known = a.initial && (!a.p.resume || a.p.resume[seq]);
-  const float *const from = c0 ? a.state : known ? a.initial : nullptr;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      S[m][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
-      if (from && 16 * (wave + 4 * m) < N) {
-        const float4 v = ld4(from + tile0 + (size_t)16 * ct * N + 64 * m);
-        S[m][ct] = floatx4{v.x, v.y, v.z, v.w};
-      }
-    }
-  auto hand_state = [&]() {
+  // Everything that a chunk reads from memory is loaded a chunk ahead, right behind the use
+  // of the chunk before; behind the last one the loads repeat it, or read nothing.
+  const int64_t rK = (int64_t)a.H * N, rV = (int64_t)a.H * P, cells = (int64_t)a.H * C::BYTES;
+  const char *cell = plan.cells + ((int64_t)(base + c0 - plan.lo) * a.H + h) * C::BYTES;
+  const int64_t row0 = (int64_t)begin + c0 * Q;
+  int rem = len - c0 * Q;  // of the chunk to be loaded next
+  const int most = wave / 2;  // the last step of the wave's rows of the lower triangle
+  const int oF0 = step_of(wave, 0) * kFrag + lane * 16, oF1 = step_of(wave, min(1, most)) * kFrag + lane * 16;
+  const int oK = (int)(((16 * wave + r) * rK + 8 * q) * sizeof(R));
+  auto at_k = [&](int s) { return NK > 1 || 8 * q < N ? oK + 32 * s * (int)sizeof(R) : kNowhere; };
+  auto rows_k = [&](const char *p) {
+    const int m = min(rem, Q);
+    return buffer_of(p, m > 0 ? (size_t)((m - 1) * rK + N) * sizeof(R) : 0);
+  };
+  auto rows_v = [&](const void *p, int esize) {
+    const int m = min(rem, Q);
+    return buffer_of(p, m > 0 ? (size_t)((m - 1) * rV + COLS) * esize : 0);
+  };
+  auto operand = [&](__amdgpu_buffer_rsrc_t b, int at, int plus) {
+    Frag f;
+    f.v = __builtin_bit_cast(s16x8, buffer_load16(b, at, plus));
+    return f;
+  };
+  const int oF = r * TR + 16 * q;  // of 64 tokens' row r, slots 8 q .. + 7
+
+  if (eighth < 4) {
+    // The state, transposed: tile m of this wave, columns 16 (wave + 4 m) + 4 q + i of k, row r of the slice's tile.
+    floatx4 S[MT][CT];
+    auto there = [&](int m) { return NK > 1 || wave + 4 * m < 2 * NK; };
+    const size_t tile0 = ((size_t)row * a.H + h) * P * N + (size_t)(slice * COLS + r) * N + 16 * wave + 4 * q;
+    const bool known = a.initial && (!a.p.resume || a.p.resume[seq]);
+    const float *const from = c0 ? a.state : known ? a.initial : nullptr;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        if (there(m)) hand<3>(sS[0] + (16 * ct + r) * SR + (16 * (wave + 4 * m) + 4 * q) * 2, COLS * SR, S[m][ct]);
-  };
-  hand_state();
-
-  const int64_t rK = (int64_t)a.H * N, rV = (int64_t)a.H * P;
-  const char *cell = plan.cells + ((int64_t)(base + c0 - plan.lo) * a.H + h) * C::BYTES;
-  const int64_t cells = (int64_t)a.H * C::BYTES;
-  // Place of the wave's tokens 4 q + i in a row of 64: step wave / 2, half wave % 2.
-  const int oT = r * TR + (32 * (wave / 2) + 8 * q + 4 * (wave % 2)) * 2;
-
-  for (int c = c0; c < c1; ++c, cell += cells) {
-    const int rem = min(Q, len - c * Q);
-    const int64_t row0 = (int64_t)begin + c * Q;
-    Frag kf[NK][IP], qf[NK][IP];
-    if constexpr (IP == 1) {
-      const size_t nK = (size_t)((rem - 1) * rK + N) * sizeof(R);
-      const auto bK = buffer_of((const R *)a.k + row0 * rK + (int64_t)h * N, nK);
-      const auto bQ = buffer_of((const R *)a.q + row0 * rK + (int64_t)h * N, nK);
-#pragma unroll
-      for (int s = 0; s < NK; ++s) {
-        const int col = 32 * s + 8 * q, at = col < N ? (int)(((16 * wave + r) * rK + col) * sizeof(R)) : kNowhere;
-        Rows<R>::load(bK, at, kf[s]);
-        Rows<R>::load(bQ, at, qf[s]);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < NK; ++s)
-#pragma unroll
-        for (int u = 0; u < IP; ++u) {
-          kf[s][u] = get(cell + C::K0 + ((u * 4 + wave) * NK + s) * kFrag, lane);
-          qf[s][u] = get(cell + C::Q0 + ((u * 4 + wave) * NK + s) * kFrag, lane);
+      for (int ct = 0; ct < CT; ++ct) {
+        S[m][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (from && 16 * (wave + 4 * m) < N) {
+          const float4 v = ld4(from + tile0 + (size_t)16 * ct * N + 64 * m);
+          S[m][ct] = floatx4{v.x, v.y, v.z, v.w};
         }
-    }
+      }
+    auto hand_state = [&]() {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          if (there(m)) hand<3>(sS[0] + (16 * ct + r) * SR + (16 * (wave + 4 * m) + 4 * q) * 2, COLS * SR, S[m][ct]);
+    };
+    const char *pK = (const char *)((const R *)a.k + row0 * rK + (int64_t)h * N);
+    const char *pV = (const char *)((const R *)a.v + row0 * rV + (int64_t)h * P + slice * COLS);
+    int oV[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) oV[i] = (int)(((16 * wave + 4 * q + i) * rV + r) * sizeof(R));
+    Rows<R> kr[NK];
+    Frag af[2][3];
     float v[CT][4];
-    {
-      const auto bV = buffer_of((const R *)a.v + row0 * rV + (int64_t)h * P + slice * COLS,
-                                (size_t)((rem - 1) * rV + COLS) * sizeof(R));
+    float4 eg4, left4;
+    float whole;
+    auto load_k = [&]() {
+      const auto b = rows_k(pK);
+#pragma unroll
+      for (int s = 0; s < NK; ++s) kr[s].load(b, at_k(s), 0);
+    };
+    auto load_v = [&]() {
+      const auto b = rows_v(pV, sizeof(R));
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = (int)(((16 * wave + 4 * q + i) * rV + 16 * ct + r) * sizeof(R));
           if constexpr (IP == 1)
-            v[ct][i] = lower((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bV, at, 0, 0));
+            v[ct][i] = lower((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, oV[i] + 32 * ct, 0, 0));
           else
-            v[ct][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bV, at, 0, 0));
+            v[ct][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, oV[i] + 64 * ct, 0, 0));
         }
-    }
-    const float *const e = reinterpret_cast<const float *>(cell + C::G0);
-    const float4 eg4 = ld4(e + 16 * wave + 4 * q), left4 = ld4(e + Q + 16 * wave + 4 * q);
-    const float eg = e[16 * wave + r], whole = e[Q - 1];
-
-    lds_barrier();  // S is there
-    floatx4 X[CT], O[CT];
+    };
+    auto load_g = [&]() {
+      const auto b = buffer_of(cell, C::BYTES);
+      eg4 = __builtin_bit_cast(float4, buffer_load16(b, 64 * wave + 16 * q, C::G0));
+      left4 = __builtin_bit_cast(float4, buffer_load16(b, 64 * wave + 16 * q, C::G0 + 4 * Q));
+      whole = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, 4 * (Q - 1), C::G0, 0));
+    };
+    auto load_a = [&]() {
+      const auto b = buffer_of(cell, C::BYTES);
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) X[ct] = O[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < NK; ++s)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        Frag sf[3];
-#pragma unroll
-        for (int u = 0; u < 3; ++u) sf[u].v = *reinterpret_cast<const s16x8 *>(sS[u] + (16 * ct + r) * SR + (32 * s + 8 * q) * 2);
-#pragma unroll
-        for (int u = 2; u >= 0; --u)
-#pragma unroll
-          for (int w = IP - 1; w >= 0; --w)
-            if (u + w < 3) {
-              X[ct] = mfma32(kf[s][w], sf[u], X[ct]);
-              if (u < MP) O[ct] = mfma32(sf[u], qf[s][w], O[ct]);
-            }
+      for (int u = 0; u < 3; ++u) {
+        af[0][u] = operand(b, oF0, C::A0 + u * kSteps * kFrag);
+        af[1][u] = operand(b, oF1, C::A0 + u * kSteps * kFrag);
       }
-    const float egv[4] = {eg4.x, eg4.y, eg4.z, eg4.w}, lev[4] = {left4.x, left4.y, left4.z, left4.w};
+    };
+    // Where this lane writes its rows of K in LDS, and reads K's columns from: the transposing
+    // read leaves column r of rows 4 q .. + 3 in a lane, in the order of the slots.
+    char *const toK = sK[0] + (16 * wave + r) * KR;
+    const char *const fromK = sK[0] + (4 * q + r / 4) * KR + r % 2 * 8;
+    if (c0 < c1) load_k(), load_v(), load_g(), load_a();
+    hand_state();
+    // Place of the wave's tokens 4 q + i in a row of 64: step wave / 2, half wave % 2.
+    const int oT = r * TR + (32 * (wave / 2) + 8 * q + 4 * (wave % 2)) * 2;
+    for (int c = c0; c < c1; ++c) {
+      rem -= Q;
+      pK += Q * rK * sizeof(R), pV += Q * rV * sizeof(R);
+      if (c + 1 < c1) cell += cells;
+      lds_barrier();  // S is there
+      floatx4 X[CT];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      floatx4 d;
+      for (int ct = 0; ct < CT; ++ct) X[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = fmaf(-egv[i], X[ct][i], v[ct][i]);
-      hand<3>(sR[0] + 16 * ct * TR + oT, COLS * TR, d);
-      O[ct] *= eg;
-    }
-    Frag af[2][3], pf[2][MP];
+      for (int s = 0; s < NK; ++s) {
+        Frag kf[IP];
+        kr[s].cut(kf);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (s <= wave / 2) {
+        for (int u = 0; u < IP; ++u)
+          *reinterpret_cast<s16x8 *>(toK + u * Q * KR + granule<NK>(r, 4 * s + q)) = kf[u].v;
 #pragma unroll
-        for (int u = 0; u < 3; ++u) af[s][u] = get(cell + C::A0 + (u * kSteps + step_of(wave, s)) * kFrag, lane);
+        for (int ct = 0; ct < CT; ++ct) {
+          Frag sf[3];
 #pragma unroll
-        for (int u = 0; u < MP; ++u) pf[s][u] = get(cell + C::P0 + (u * kSteps + step_of(wave, s)) * kFrag, lane);
-      }
-    Frag kt[MT][2][IP];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      if (there(m)) {
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts)
-#pragma unroll
-          for (int u = 0; u < IP; ++u) kt[m][ts][u] = get(cell + C::KT0 + ((u * 2 * NK + wave + 4 * m) * 2 + ts) * kFrag, lane);
-      }
-    lds_barrier();  // V - K S^T is there
-    const int oF = r * TR + 16 * q;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      floatx4 U = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s <= wave / 2) {
-          Frag rf[3];
-#pragma unroll
-          for (int u = 0; u < 3; ++u) rf[u].v = *reinterpret_cast<const s16x8 *>(sR[u] + 16 * ct * TR + oF + 64 * s);
+          for (int u = 0; u < 3; ++u) sf[u].v = *reinterpret_cast<const s16x8 *>(sS[u] + (16 * ct + r) * SR + (32 * s + 8 * q) * 2);
 #pragma unroll
           for (int u = 2; u >= 0; --u)
 #pragma unroll
-            for (int w = 2 - u; w >= 0; --w) U = mfma32(af[s][u], rf[w], U);
+            for (int w = IP - 1; w >= 0; --w)
+              if (u + w < 3) X[ct] = mfma32(kf[w], sf[u], X[ct]);
         }
-      hand<MP>(sU[0] + 16 * ct * TR + oT, COLS * TR, U);
+      }
+      load_k();
+      const float egv[4] = {eg4.x, eg4.y, eg4.z, eg4.w}, lev[4] = {left4.x, left4.y, left4.z, left4.w}, all = whole;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) U[i] *= lev[i];
-      hand<3>(sW[0] + 16 * ct * TR + oT, COLS * TR, U);
-    }
-    lds_barrier();  // U is there
+      for (int ct = 0; ct < CT; ++ct) {
+        floatx4 d;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
+        for (int i = 0; i < 4; ++i) d[i] = fmaf(-egv[i], X[ct][i], v[ct][i]);
+        hand<3>(sR[0] + 16 * ct * TR + oT, COLS * TR, d);
+      }
+      load_v();
+      load_g();
+      lds_barrier();  // V - K S^T is there, and K
+      Frag kt[MT][2][IP];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) S[m][ct] *= whole;
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int ts = 0; ts < 2; ++ts) {
-        Frag wf[3];
+        for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
-        for (int u = 0; u < 3; ++u) wf[u].v = *reinterpret_cast<const s16x8 *>(sW[u] + 16 * ct * TR + oF + 64 * ts);
+          for (int u = 0; u < IP; ++u)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (there(m)) {
+            for (int e = 0; e < 2; ++e)
+              kt[m][ts][u].h[e] = read_tr(fromK + (u * Q + 32 * ts + 16 * e) * KR +
+                                          granule<NK>(4 * q + r / 4, 2 * (there(m) ? wave + 4 * m : 0) + r % 4 / 2));
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        floatx4 U = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (s <= most) {
+            Frag rf[3];
+#pragma unroll
+            for (int u = 0; u < 3; ++u) rf[u].v = *reinterpret_cast<const s16x8 *>(sR[u] + 16 * ct * TR + oF + 64 * s);
+#pragma unroll
+            for (int u = 2; u >= 0; --u)
+#pragma unroll
+              for (int w = 2 - u; w >= 0; --w) U = mfma32(af[s][u], rf[w], U);
+          }
+        hand<MP>(sU[0] + 16 * ct * TR + oT, COLS * TR, U);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) U[i] *= lev[i];
+        hand<3>(sW[0] + 16 * ct * TR + oT, COLS * TR, U);
+      }
+      load_a();
+      lds_barrier();  // U is there
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) S[m][ct] *= all;
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts) {
+          Frag wf[3];
+#pragma unroll
+          for (int u = 0; u < 3; ++u) wf[u].v = *reinterpret_cast<const s16x8 *>(sW[u] + 16 * ct * TR + oF + 64 * ts);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int u = 2; u >= 0; --u)
 #pragma unroll
               for (int w = IP - 1; w >= 0; --w)
                 if (u + w < 3) S[m][ct] = mfma32(kt[m][ts][w], wf[u], S[m][ct]);
-          }
+        }
       }
+      hand_state();
     }
-    hand_state();
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s <= wave / 2) {
-          Frag uf[MP];
+      for (int ct = 0; ct < CT; ++ct)
+        if (16 * (wave + 4 * m) < N)
+          st4(a.state + tile0 + (size_t)16 * ct * N + 64 * m, make_float4(S[m][ct][0], S[m][ct][1], S[m][ct][2], S[m][ct][3]));
+  } else {
+    const char *pQ = (const char *)((const R *)a.q + row0 * rK + (int64_t)h * N);
+    char *pY = (char *)((Y *)a.y + row0 * rV + (int64_t)h * P + slice * COLS);
+    const int oY = (int)(((16 * wave + r) * rV + 4 * q) * sizeof(Y));
+    Rows<R> qr[NK];
+    Frag pf[2][MP];
+    float eg;
+    auto load_q = [&]() {
+      const auto b = rows_k(pQ);
 #pragma unroll
-          for (int u = 0; u < MP; ++u) uf[u].v = *reinterpret_cast<const s16x8 *>(sU[u] + 16 * ct * TR + oF + 64 * s);
+      for (int s = 0; s < NK; ++s) qr[s].load(b, at_k(s), 0);
+    };
+    auto load_g = [&]() {
+      eg = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer_of(cell, C::BYTES), 64 * wave + 4 * r, C::G0, 0));
+    };
+    auto load_p = [&]() {
+      const auto b = buffer_of(cell, C::BYTES);
+#pragma unroll
+      for (int u = 0; u < MP; ++u) {
+        pf[0][u] = operand(b, oF0, C::P0 + u * kSteps * kFrag);
+        pf[1][u] = operand(b, oF1, C::P0 + u * kSteps * kFrag);
+      }
+    };
+    if (c0 < c1) load_q(), load_g(), load_p();
+    for (int c = c0; c < c1; ++c) {
+      const auto bY = rows_v(pY, sizeof(Y));  // rows past the end are not written
+      rem -= Q;
+      pQ += Q * rK * sizeof(R), pY += Q * rV * sizeof(Y);
+      if (c + 1 < c1) cell += cells;
+      lds_barrier();  // S is there
+      floatx4 O[CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) O[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NK; ++s) {
+        Frag qf[IP];
+        qr[s].cut(qf);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          Frag sf[MP];
+#pragma unroll
+          for (int u = 0; u < MP; ++u) sf[u].v = *reinterpret_cast<const s16x8 *>(sS[u] + (16 * ct + r) * SR + (32 * s + 8 * q) * 2);
 #pragma unroll
           for (int u = MP - 1; u >= 0; --u)
 #pragma unroll
-            for (int w = MP - 1 - u; w >= 0; --w) O[ct] = mfma32(uf[u], pf[s][w], O[ct]);
+            for (int w = IP - 1; w >= 0; --w)
+              if (u + w < 3) O[ct] = mfma32(sf[u], qf[w], O[ct]);
         }
+      }
+      load_q();
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) O[ct] *= eg;
+      load_g();
+      lds_barrier();  // V - K S^T is there
+      lds_barrier();  // U is there
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (s <= most) {
+            Frag uf[MP];
+#pragma unroll
+            for (int u = 0; u < MP; ++u) uf[u].v = *reinterpret_cast<const s16x8 *>(sU[u] + 16 * ct * TR + oF + 64 * s);
+#pragma unroll
+            for (int u = MP - 1; u >= 0; --u)
+#pragma unroll
+              for (int w = MP - 1 - u; w >= 0; --w) O[ct] = mfma32(uf[u], pf[s][w], O[ct]);
+          }
+      }
+      load_p();
       // This lane holds four neighbouring rows of the state's output for token 16 wave + r.
-      const auto bY = buffer_of((Y *)a.y + row0 * rV + (int64_t)h * P + slice * COLS,
-                                (size_t)((rem - 1) * rV + COLS) * sizeof(Y));  // rows past the end are not written
-      const int at = (int)(((16 * wave + r) * rV + 16 * ct + 4 * q) * sizeof(Y));
-      const floatx4 o = O[ct];
-      if constexpr (sizeof(Y) == 2)
-        __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, at, 0, 0);
-      else
-        __builtin_amdgcn_raw_buffer_store_b128(
-            i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, at, 0, 0);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const floatx4 o = O[ct];
+        const int at = oY + 16 * ct * (int)sizeof(Y);
+        if constexpr (sizeof(Y) == 2)
+          __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, at, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b128(
+              i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, at, 0, 0);
+      }
     }
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-      if (16 * (wave + 4 * m) < N)
-        st4(a.state + tile0 + (size_t)16 * ct * N + 64 * m, make_float4(S[m][ct][0], S[m][ct][1], S[m][ct][2], S[m][ct][3]));
 }
 
 // Cells of one pass: at most 256 MB of them, so that long prompts need no more than that.
@@ -528,10 +603,10 @@ int launch(const DeltaArgs &a, hipStream_t st) {
     p.lo = (int)lo, p.hi = (int)std::min<int64_t>(all, lo + most);
     const int64_t places = p.hi - p.lo, units = std::min<int64_t>(a.p.n, places) * a.H;
     const int64_t blocks = (units + kXcds - 1) / kXcds * kXcds * p.ny;
-    if (places * a.H > kMostBlocks || blocks > kMostBlocks) return kTooLarge;
+    if (places * a.H > kMostBlocks || 2 * blocks > kMostBlocks) return kTooLarge;
     p.units = (int)units;
     if (a.p.tokens) hipLaunchKernelGGL((cells_k<R, Y, NK>), dim3((uint32_t)(places * a.H)), dim3(kThreads), 0, st, a, p);
-    hipLaunchKernelGGL((chain_k<R, Y, NK, CT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, a, p);
+    hipLaunchKernelGGL((chain_k<R, Y, NK, CT>), dim3((uint32_t)blocks), dim3(2 * kThreads), 0, st, a, p);
   }
   return (int)hipGetLastError();
 }

@@ -22,6 +22,11 @@ __device__ __forceinline__ floatx4 mfma32(const Frag &a, const Frag &b, floatx4 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
 }
 
+// The transposing LDS read: 16 lanes of 8 bytes each, lane l from row l / 4 and columns
+// 4 (l % 4) .. + 3, get column l of the four rows.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 read_tr(const char *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
+
 __device__ __forceinline__ float upper(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float lower(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }

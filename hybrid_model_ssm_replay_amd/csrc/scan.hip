@@ -51,7 +51,6 @@
 namespace rssm {
 namespace {
 
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
@@ -75,8 +74,6 @@ __device__ __forceinline__ int in_row_x(int row, int c) {
 // C: a granule holds a lane's operand of one 32-column step k, columns 32 k + 4 q
 // .. + 3 and 32 k + 16 + 4 q .. + 3, and is read whole by 16 rows at a time.
 __device__ __forceinline__ int in_row_c(int row, int k, int q) { return ((4 * k + q) ^ (row & 15)) << 4; }
-
-__device__ __forceinline__ s16x4 read_tr(const char *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p); }
 
 // A value all lanes share, in a scalar register.
 __device__ __forceinline__ float uniform(float v) {
