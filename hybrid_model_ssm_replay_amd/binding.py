@@ -12,7 +12,8 @@ import os
 KIND_MAMBA2, KIND_GDN = 0, 1
 FMT_F32, FMT_F16_SR, FMT_F8E4M3, FMT_F4E2M1_B16, FMT_F4E2M1_CS = 0, 1, 2, 3, 4
 STATUS_ACCEPT_CLAMPED, STATUS_BAD_POINTERS, STATUS_BAD_PROMPT = 0x1, 0x2, 0x4
-DT_F32, DT_BF16 = 0, 1
+DT_F32, DT_BF16, DT_E4M3 = 0, 1, 2
+MAX_TOP = 32
 FLAG_DECAY_SKIP = 0x1
 FLAG_BF16_RECORDS = 0x2
 FLAG_RECORDS_IN_RING = 0x4
@@ -91,6 +92,22 @@ class replay_accept_args(ctypes.Structure):
                 ("next", ctypes.c_void_p)]
 
 
+class replay_residual_norm_args(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("channels", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("sum_stride", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("sum", ctypes.c_void_p)]
+
+
+class replay_token_logprobs_args(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("top", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("stride", ctypes.c_int64), ("reserved", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("tokens", ctypes.c_void_p), ("logprobs", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("top_logprobs", ctypes.c_void_p), ("top_tokens", ctypes.c_void_p)]
+
+
 class replay_scan_layout(ctypes.Structure):
     _fields_ = [("segment", ctypes.c_int32), ("adds", ctypes.c_int32), ("columns", ctypes.c_int32),
                 ("workgroups", ctypes.c_int32)]
@@ -135,6 +152,9 @@ _SIG = {
     "replay_delta_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
     "replay_delta_prompt": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
     "replay_gated_norm": (ctypes.c_int, [_P, _P]),
+    "replay_residual_norm": (ctypes.c_int, [_P, _P]),
+    "replay_token_logprobs_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "replay_token_logprobs": (ctypes.c_int, [_P, _P, _P]),
     "replay_accept_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "replay_accept_drafts": (ctypes.c_int, [_P, _P, _P]),
     "replay_hbm_probe": (ctypes.c_int, [_P, _P, ctypes.c_size_t, ctypes.c_int, _P]),
@@ -162,7 +182,8 @@ def load_library(path: str | None = None):
         fn.restype = res
         fn.argtypes = args
     for i, st in enumerate((replay_config, replay_buffers, replay_record, replay_ctx, replay_ring_view, replay_prompt,
-                            replay_short_conv, replay_gated_norm_args, replay_accept_args, replay_scan_layout)):
+                            replay_short_conv, replay_gated_norm_args, replay_accept_args, replay_scan_layout,
+                            replay_residual_norm_args, replay_token_logprobs_args)):
         if lib.replay_abi_sizeof(i) != ctypes.sizeof(st):
             raise ImportError(f"ABI mismatch for {st.__name__}: C {lib.replay_abi_sizeof(i)} "
                               f"vs ctypes {ctypes.sizeof(st)}")
@@ -332,6 +353,22 @@ def replay_gated_norm(args, stream: int) -> None:
     rc = (_lib or load_library()).replay_gated_norm(_by_address(args), stream)
     if rc:
         _check("replay_gated_norm", rc)
+
+
+def replay_residual_norm(args, stream: int) -> None:
+    rc = (_lib or load_library()).replay_residual_norm(_by_address(args), stream)
+    if rc:
+        _check("replay_residual_norm", rc)
+
+
+def replay_token_logprobs_workspace_bytes(rows: int, vocab: int, top: int) -> int:
+    return (_lib or load_library()).replay_token_logprobs_workspace_bytes(rows, vocab, top)
+
+
+def replay_token_logprobs(args, workspace: int, stream: int) -> None:
+    rc = (_lib or load_library()).replay_token_logprobs(_by_address(args), workspace, stream)
+    if rc:
+        _check("replay_token_logprobs", rc)
 
 
 def replay_accept_workspace_bytes(batch: int, vocab: int) -> int:

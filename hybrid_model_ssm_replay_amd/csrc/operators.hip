@@ -189,6 +189,45 @@ int replay_gated_norm(const replay_gated_norm_args *a, void *stream) {
   return hip_status(launch_gated_norm(*a, (hipStream_t)stream));
 }
 
+int replay_residual_norm(const replay_residual_norm_args *a, void *stream) {
+  if (!a || a->tokens < 0 || a->tokens > kMost || a->channels < 1 || a->channels > kMost || a->reserved) return REPLAY_EINVAL;
+  const bool codes = a->out_dtype == REPLAY_DT_E4M3;
+  if (!dtype_ok(a->x_dtype) || !dtype_ok(a->residual_dtype) || !(codes || dtype_ok(a->out_dtype)) || !(a->eps >= 0.f))
+    return REPLAY_EINVAL;
+  if (codes) {
+    const int g = a->group;
+    if (g < 1 || a->channels % g || (g != a->channels && (g < 16 || g > 512 || (g & (g - 1))))) return REPLAY_EINVAL;
+  } else if (a->group) {
+    return REPLAY_EINVAL;
+  }
+  if (a->tokens == 0) return REPLAY_OK;
+  if (!a->x || !a->out || (codes && !a->scales) || (a->residual && !a->sum)) return REPLAY_EINVAL;
+  if (!elem_aligned(a->x, a->x_dtype) || !elem_aligned(a->weight, REPLAY_DT_F32) || !elem_aligned(a->scales, REPLAY_DT_F32) ||
+      (!codes && !elem_aligned(a->out, a->out_dtype)))
+    return REPLAY_EINVAL;
+  if (a->residual && (!elem_aligned(a->residual, a->residual_dtype) || !elem_aligned(a->sum, a->residual_dtype)))
+    return REPLAY_EINVAL;
+  if (a->x_stride < 0 || a->residual_stride < 0) return REPLAY_EINVAL;
+  if (a->tokens > 1 && (a->out_stride < a->channels || (a->residual && a->sum_stride < a->channels))) return REPLAY_EINVAL;
+  return hip_status(launch_residual_norm(*a, (hipStream_t)stream));
+}
+
+size_t replay_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top) {
+  return rows < 1 || rows > kMost || vocab < 1 || vocab > kMost || top < 0 || top > REPLAY_MAX_TOP ? 0
+                                                                                                 : logprobs_workspace(rows, vocab, top);
+}
+
+int replay_token_logprobs(const replay_token_logprobs_args *a, void *workspace, void *stream) {
+  if (!a || a->rows < 0 || a->rows > kMost || a->vocab < 1 || a->vocab > kMost || a->top < 0 || a->top > REPLAY_MAX_TOP || a->reserved)
+    return REPLAY_EINVAL;
+  if (!dtype_ok(a->dtype) || a->stride < 0) return REPLAY_EINVAL;
+  if (a->rows == 0) return REPLAY_OK;
+  if (!a->logits || !elem_aligned(a->logits, a->dtype) || !a->tokens || !a->logprobs || !a->entropy) return REPLAY_EINVAL;
+  if (a->top && (!a->top_logprobs || !a->top_tokens)) return REPLAY_EINVAL;
+  if (logprobs_workspace(a->rows, a->vocab, a->top) && (!workspace || ((uintptr_t)workspace & 255u))) return REPLAY_EINVAL;
+  return hip_status(launch_logprobs(*a, workspace, (hipStream_t)stream));
+}
+
 size_t replay_accept_workspace_bytes(int32_t batch, int32_t vocab) {
   return batch < 1 || vocab < 1 || vocab > kMost ? 0 : accept_workspace(batch, vocab);
 }

@@ -198,6 +198,11 @@ int launch_renew_read_copy(const Shape &s, const FormatBufs &f, const uint8_t *m
 
 int launch_gated_norm(const replay_gated_norm_args &a, hipStream_t st);
 
+int launch_residual_norm(const replay_residual_norm_args &a, hipStream_t st);
+
+size_t logprobs_workspace(int rows, int vocab, int top);
+int launch_logprobs(const replay_token_logprobs_args &a, void *workspace, hipStream_t st);
+
 size_t accept_workspace(int batch, int vocab);
 int launch_accept(const replay_accept_args &a, void *workspace, hipStream_t st);
 

@@ -172,6 +172,8 @@ size_t replay_abi_sizeof(int which) {
     case 7: return sizeof(replay_gated_norm_args);
     case 8: return sizeof(replay_accept_args);
     case 9: return sizeof(replay_scan_layout);
+    case 10: return sizeof(replay_residual_norm_args);
+    case 11: return sizeof(replay_token_logprobs_args);
     default: return 0;
   }
 }

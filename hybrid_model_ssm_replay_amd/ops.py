@@ -9,7 +9,11 @@ include/replayssm.h for the definitions.
   front of the recurrence, for packed prompts and for one token or T drafts.
 * ``scan_prompt``: the Mamba-2 recurrence over packed prompts, into a state that
   the decode step continues from.
+* ``delta_prompt``: the same for the Gated DeltaNet recurrence.
 * ``gated_norm``: the gated group norm behind the recurrence.
+* ``residual_norm``: the norm of the residual stream, with the addition before it;
+  outputs in 8 bits with scales if asked.
+* ``token_logprobs``: log probabilities of given tokens, entropy, the largest words.
 * ``accept_drafts``: how many drafts to commit, and the token after them.
 
 The kernels of a decode step take a few microseconds, so what Python adds to a
@@ -24,6 +28,7 @@ import torch
 
 from . import binding as B
 
+_E4M3 = torch.float8_e4m3fn
 _DT = {torch.float32: B.DT_F32, torch.bfloat16: B.DT_BF16}
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 # The library's structs as bytes, in the order of their fields (native alignment).
@@ -31,6 +36,8 @@ _PROMPT = struct.Struct("@2i4P").pack
 _CONV = struct.Struct("@10i5P").pack
 _NORM = struct.Struct("@8ifi3q4P").pack
 _ACCEPT = struct.Struct("@6i4q7P").pack
+_STREAM = struct.Struct("@6ifi4q6P").pack
+_LOGPROBS = struct.Struct("@4i2q6P").pack
 _CONFIG = struct.Struct("@10iQ2I").pack
 _RECORD = struct.Struct("@5P").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
@@ -284,6 +291,68 @@ def gated_norm(y, z, weight, group, *, eps=1e-5, norm_first=False, out_dtype=Non
            _NORM(tokens, C, group, wn, _DT[y.dtype], _DT[z.dtype], _DT[out_dtype], 1 if norm_first else 0, eps, 0, y.stride(0),
                  z.stride(0), C, y.data_ptr(), z.data_ptr(), _check(weight, "weight", _F32, (wn,), at), out.data_ptr()))
     return out
+
+
+def residual_norm(x, residual, weight, *, eps=1e-5, out_dtype=None, scale_group=None):
+    """The residual stream's addition and the RMS norm over its channels, per token.
+
+    x, residual [tokens, channels] float32 or bfloat16, rows may be strided; residual
+    None: nothing is added; weight float32 [channels], or None: 1.  The norm is that of
+    x + residual in float32.  Returns (out, total): total is x + residual in residual's
+    type, or x itself without one; out has out_dtype (x's type if None).  With out_dtype
+    torch.float8_e4m3fn it returns (codes, scales, total): scale_group channels (a power
+    of two from 16 to 512, or all of them: None) share a scale, float32 [tokens,
+    channels / scale_group], and code times scale is the value."""
+    at = _vectors(x, "x", 2)
+    tokens, C = x.shape
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    codes = out_dtype is _E4M3
+    if not codes and out_dtype not in _DT:
+        raise ValueError(f"out_dtype {out_dtype} is not float32, bfloat16 or float8_e4m3fn")
+    if not codes and scale_group is not None:
+        raise ValueError("scale_group is for float8_e4m3fn outputs")
+    group = 0 if not codes else C if scale_group is None else scale_group
+    if C < 1 or codes and (group < 1 or C % group or (group != C and group not in (16, 32, 64, 128, 256, 512))):
+        raise ValueError(f"scale_group {group} must be all of {C} channels, or a power of two from 16 to 512 that divides them")
+    rs, rt, stride, to, total = 0, 0, 0, 0, x
+    if residual is not None:
+        if _vectors(residual, "residual", 2) != at:
+            raise ValueError(f"tensors are on several devices: residual is on {residual.device}")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+        total = residual.new_empty(tokens, C)
+        rs, rt, stride, to = residual.data_ptr(), _DT[residual.dtype], residual.stride(0), total.data_ptr()
+    out = x.new_empty(tokens, C) if out_dtype is x.dtype else x.new_empty(tokens, C, dtype=out_dtype)
+    scales = x.new_empty(tokens, C // group, dtype=_F32) if codes else None
+    launch(B.replay_residual_norm, at,
+           _STREAM(tokens, C, group, _DT[x.dtype], rt, B.DT_E4M3 if codes else _DT[out_dtype], eps, 0, x.stride(0), stride, C, C,
+                   x.data_ptr(), rs, 0 if weight is None else _check(weight, "weight", _F32, (C,), at), out.data_ptr(),
+                   scales.data_ptr() if codes else 0, to))
+    return (out, scales, total) if codes else (out, total)
+
+
+def token_logprobs(logits, tokens, *, top=0):
+    """What logits say of given tokens: softmax probabilities of each row, in natural logarithms.
+
+    logits [rows, vocab] float32 or bfloat16, rows may be strided; tokens int32 [rows];
+    top: 0 to 32 alternatives.  Returns (logprobs, entropy, top_logprobs, top_tokens): float32
+    [rows], float32 [rows], float32 and int32 [rows, top], the largest words first and of
+    equal ones the lower.  -inf and NaN have no weight: such a word, or a token outside the
+    vocabulary, has -inf, and missing alternatives are -inf and -1."""
+    at = _vectors(logits, "logits", 2)
+    rows, V = logits.shape
+    if V < 1 or not 0 <= top <= B.MAX_TOP:
+        raise ValueError(f"token_logprobs needs a vocabulary, and top from 0 to {B.MAX_TOP}")
+    words = _check(tokens, "tokens", _I32, (rows,), at)
+    logprobs, entropy = logits.new_empty(rows, dtype=_F32), logits.new_empty(rows, dtype=_F32)
+    best, which = logits.new_empty(rows, top, dtype=_F32), tokens.new_empty(rows, top)
+    if rows:
+        nbytes = B.replay_token_logprobs_workspace_bytes(rows, V, top)
+        ws = logits.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+        launch(B.replay_token_logprobs, at,
+               _LOGPROBS(rows, V, top, _DT[logits.dtype], logits.stride(0), 0, logits.data_ptr(), words, logprobs.data_ptr(),
+                         entropy.data_ptr(), best.data_ptr(), which.data_ptr()), ws.data_ptr() if nbytes else 0)
+    return logprobs, entropy, best, which
 
 
 def accept_drafts(tokens, target, uniforms, *, draft=None, lengths=None):

@@ -247,7 +247,7 @@ const char *replay_strerror(int code);
 /* sizeof of the ABI structs, for bindings: 0 replay_config, 1 replay_buffers,
  * 2 replay_record, 3 replay_ctx, 4 replay_ring_view, 5 replay_prompt,
  * 6 replay_short_conv, 7 replay_gated_norm_args, 8 replay_accept_args,
- * 9 replay_scan_layout. */
+ * 9 replay_scan_layout, 10 replay_residual_norm_args, 11 replay_token_logprobs_args. */
 size_t replay_abi_sizeof(int which);
 
 /* ---- the decode calls -------------------------------------------------- */
@@ -341,11 +341,12 @@ int replay_ring_fields(const replay_ctx *ctx, replay_ring_view *view);
  * the same stream (or ordered after it).  REPLAY_EINVAL unless RECORDS_IN_RING. */
 int replay_record_slots(const replay_ctx *ctx, int32_t *slots, void *stream);
 
-/* ---- around the recurrence: short convolution, prompts, norm, draft acceptance ----
+/* ---- around the recurrence: short convolution, prompts, norms, draft acceptance, log probabilities ----
  *
  * The operators a layer needs next to the decode step: the short causal
  * convolution in front of it, the scan that turns a prompt into a checkpoint,
- * the gated norm behind it, and the test that says how many drafts to commit.
+ * the gated norm behind it, the norm of the stream between layers, the test that says
+ * how many drafts to commit, and the log probabilities of tokens.
  * They share the conventions at the top of this file.  Vector arrays have an
  * element type (REPLAY_DT_*); sums, statistics and states are float32 or wider.
  */
@@ -353,6 +354,7 @@ int replay_record_slots(const replay_ctx *ctx, int32_t *slots, void *stream);
 /* Element types. */
 #define REPLAY_DT_F32 0
 #define REPLAY_DT_BF16 1
+#define REPLAY_DT_E4M3 2 /* OCP e4m3fn codes with scales, outputs of replay_residual_norm only */
 
 /* Sequences of several prompts, packed one after the other.
  *   tokens     rows of the packed arrays, 0..2^30.
@@ -509,6 +511,73 @@ typedef struct replay_gated_norm_args {
   void *out;
 } replay_gated_norm_args;
 int replay_gated_norm(const replay_gated_norm_args *args, void *stream);
+
+/* The norm of the residual stream between two layers, with the addition before it:
+ *   h = x + residual (float32),  sum = h in the residual's type,
+ *   out = weight h / sqrt(mean(h^2) + eps)  over the channels of a token.
+ * residual NULL: h = x, and no sum is written.  weight: float32 [channels], or NULL: 1.
+ * Rows start at multiples of their strides (elements; >= 0 for x and residual, whose
+ * rows may repeat, >= channels for out and sum).  sum may be residual or x itself, at
+ * the same stride and type.  tokens and channels are at most 2^30.
+ *   out_dtype  REPLAY_DT_F32, _BF16, or REPLAY_DT_E4M3: codes, one byte each, that
+ *              stand for code x scale; scales float32 [tokens][channels / group],
+ *              max(largest |out| of the group / 448, 2^-126).  A code is out / scale
+ *              (by the scale's float32 reciprocal), rounded to nearest even; NaN stays NaN.
+ *   group      channels that share a scale: channels, or 16, 32, 64, 128, 256 or 512
+ *              that divide them; 0 for other outputs. */
+typedef struct replay_residual_norm_args {
+  int32_t tokens;
+  int32_t channels;
+  int32_t group;
+  int32_t x_dtype;
+  int32_t residual_dtype;
+  int32_t out_dtype;
+  float eps;
+  int32_t reserved;
+  int64_t x_stride;
+  int64_t residual_stride;
+  int64_t out_stride;
+  int64_t sum_stride;
+  const void *x;
+  const void *residual;
+  const float *weight;
+  void *out;
+  float *scales;
+  void *sum;
+} replay_residual_norm_args;
+int replay_residual_norm(const replay_residual_norm_args *args, void *stream);
+
+/* What a model's logits say of given tokens: with p = softmax(logits) of each row,
+ *   logprobs      float32 [rows]: log p[tokens[row]]; -infinity for a word without
+ *                 weight, or a token outside 0..vocab-1.
+ *   entropy       float32 [rows]: -sum p log p (natural logarithms); 0 for a row
+ *                 without any weight.
+ *   top_logprobs, top_tokens  float32, int32 [rows][top]: the largest words, falling, of
+ *                 equal ones the lower first; -infinity and -1 where a row has no more
+ *                 words with weight.
+ * -infinity and NaN have no weight; +infinity counts as the largest float32.
+ *   logits     [rows][vocab] in dtype (REPLAY_DT_F32, _BF16) at multiples of stride (>= 0).
+ *   tokens     device int32 [rows].
+ *   rows, vocab  at most 2^30; top: 0 .. REPLAY_MAX_TOP.
+ *   workspace  replay_token_logprobs_workspace_bytes bytes (256-byte aligned), or NULL
+ *              when that is 0. */
+#define REPLAY_MAX_TOP 32
+typedef struct replay_token_logprobs_args {
+  int32_t rows;
+  int32_t vocab;
+  int32_t top;
+  int32_t dtype;
+  int64_t stride;
+  int64_t reserved;
+  const void *logits;
+  const int32_t *tokens;
+  float *logprobs;
+  float *entropy;
+  float *top_logprobs;
+  int32_t *top_tokens;
+} replay_token_logprobs_args;
+size_t replay_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top);
+int replay_token_logprobs(const replay_token_logprobs_args *args, void *workspace, void *stream);
 
 /* Which drafts to keep: draft i (token x_i = tokens[b][i], i < lengths[b]) is
  * accepted while every earlier one is and u_i q_i(x_i) < p_i(x_i), with u_i =

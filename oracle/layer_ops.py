@@ -114,3 +114,39 @@ def accept(tokens, target, uniforms, draft=None, length=None):
     run = np.cumsum(w)
     over = np.nonzero((run > float(uniforms[T]) * run[-1]) & (w > 0))[0]
     return a, int(over[0]) if len(over) else int(np.nonzero(w > 0)[0][-1])
+
+
+def e4m3(v):
+    """v rounded to the nearest e4m3 value, ties to even; |v| at most 448 and a rounding's half step."""
+    v = np.asarray(v, np.float64)
+    a = np.abs(v)
+    step = np.exp2(np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3.0)
+    return np.sign(v) * np.minimum(np.round(a / step) * step, 448.0)
+
+
+def residual_norm(x, residual, weight, eps):
+    """(out, h) of h = x + residual, out = weight h / sqrt(mean(h^2) + eps); residual or weight may be None."""
+    h = np.asarray(x, np.float64) + (0.0 if residual is None else np.asarray(residual, np.float64))
+    out = h / np.sqrt((h * h).mean(-1, keepdims=True) + eps)
+    return (out if weight is None else out * np.asarray(weight, np.float64)), h
+
+
+def token_logprobs(logits, tokens, top):
+    """For each row: log p of its token, the entropy, the largest words and their log p.
+
+    -inf and NaN have no weight, +inf counts as the largest float32."""
+    x = np.asarray(logits, np.float64)
+    x = np.where(np.isnan(x), -np.inf, np.minimum(x, np.finfo(np.float32).max))
+    lp, entropy, best, words = [], [], [], []
+    for row, tok in zip(x, tokens):
+        some = row > -np.inf
+        p = np.full(row.shape, -np.inf)
+        if some.any():
+            d = row[some] - row.max()
+            p[some] = d - np.log(np.exp(d).sum())
+        lp.append(p[tok] if 0 <= tok < len(row) else -np.inf)
+        entropy.append(-(np.exp(p[some]) * p[some]).sum())
+        order = [i for i in np.lexsort((np.arange(len(row)), -row)) if some[i]][:top]
+        words.append(order + [-1] * (top - len(order)))
+        best.append([p[i] for i in order] + [-np.inf] * (top - len(order)))
+    return np.array(lp), np.array(entropy), np.array(best).reshape(len(lp), top), np.array(words, np.int64).reshape(len(lp), top)
