@@ -8,10 +8,11 @@
 // slices, a workgroup each, whose sums and words a second launch joins in their order:
 // no atomics, and the same result every time.
 //
-// The largest words: a wave keeps a sorted list, a lane an entry, and puts in what is
-// larger than the list's last; of equal words the lower comes first.  Before a long run
-// of insertions (the first words, or rows that rise) the last entry is raised to the
-// list's size-th largest of the lanes' own maxima, which as many words reach.
+// The largest words: a wave keeps a sorted list, a lane an entry, of keys whose order is
+// that of the words (falling, of equal ones the lower first).  A few words beyond the
+// list's last are put in one by one, more are sorted into it 32 at a time.  Where many
+// are beyond it (the first words, or rows that rise), only those count that reach the
+// list's size-th largest of the lanes' own maxima: as many words do.
 //
 // -infinity and NaN have no weight; +infinity counts as the largest float32.
 #include "ops.h"
@@ -28,18 +29,19 @@ constexpr float kLowest = -3.4028234663852886e38f, kNone = -__builtin_inff();
 // Exponents below this are no weight at all; a product with it stays finite.
 constexpr float kLeast = -1e4f;
 
+typedef unsigned long long Key;
+
 struct Slices {
-  int size, n;    // values of a slice (a multiple of kStep), slices of a row
+  int size, n;   // values of a slice (a multiple of kStep), slices of a row
   FastDiv fn;
-  float4 *sums;   // [rows][n]: m, s, t
-  float *values;  // [rows][n][top]
-  int *words;
+  float4 *sums;  // [rows][n]: m, s, t
+  Key *keys;     // [rows][top][n]
 };
 
-struct Sums {  // m is finite: kLowest before any weight
+struct Sums {  // m is finite: kLowest before any weight; t has exponents of 2
   float m, s, t;
   __device__ __forceinline__ void scale_to(float to) {  // to >= m
-    const float d = fmaxf(m - to, kLeast), c = __builtin_amdgcn_exp2f(d * kLog2e);
+    const float d = fmaxf((m - to) * kLog2e, kLeast), c = __builtin_amdgcn_exp2f(d);
     t = (t + s * d) * c, s *= c, m = to;
   }
   __device__ __forceinline__ void join(Sums o) {
@@ -49,53 +51,86 @@ struct Sums {  // m is finite: kLowest before any weight
   }
 };
 
-// NaN as -infinity, +infinity as the largest number.
+// +infinity as the largest number, NaN as -infinity.
 __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, kNone), -kLowest); }
 
-// Whether a word comes before another: larger, or as large and lower.
-__device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
+// A word as a number that is larger where the word comes first; 0 for none and -infinity.
+__device__ __forceinline__ Key key_of(float x, int word) {
+  const uint32_t b = bits(x + 0.f), up = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);  // -0 as 0
+  return x > kNone ? (Key)up << 32 | ~(uint32_t)word : 0;
+}
+__device__ __forceinline__ float value_of(Key k) {
+  const uint32_t up = (uint32_t)(k >> 32);
+  return k ? __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up) : kNone;
+}
+__device__ __forceinline__ int word_of(Key k) { return k ? (int)~(uint32_t)k : -1; }
 
-// A wave's list of `top` words, lane l the l-th.
-struct List {
-  float v;
-  int i;
-  float last;  // of the last entry, the same in every lane
-  int last_i;
-  __device__ __forceinline__ void clear() { v = last = kNone, i = last_i = 0x7fffffff; }
-  __device__ __forceinline__ void put(float x, int word, int top, int lane) {  // x, word: the same in every lane
-    const int at = __popcll(__ballot(before(v, i, x, word)));
-    const float v1 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x138, 0xF, 0xF, false));
-    const int i1 = __builtin_amdgcn_update_dpp(0, i, 0x138, 0xF, 0xF, false);  // from the lane before
-    v = lane > at ? v1 : lane == at ? x : v;
-    i = lane > at ? i1 : lane == at ? word : i;
-    last = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), top - 1));
-    last_i = __builtin_amdgcn_readlane(i, top - 1);
+// The value of lane l ^ J.
+template <int J>
+__device__ __forceinline__ uint32_t other(uint32_t v, int lane) {
+  if constexpr (J == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
+  if constexpr (J == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false);
+  if constexpr (J == 4)  // 7 - l within eight lanes, then 3 - l within four
+    return __builtin_amdgcn_update_dpp(0, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false), 0x1B, 0xF, 0xF, false);
+  if constexpr (J == 8) return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, false);
+  if constexpr (J == 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return lane & 16 ? a[0] : a[1];
   }
-  // One candidate of each lane where `is`, none of -infinity.
-  __device__ __forceinline__ void offer(float x, int word, bool is, int top, int lane) {
-    uint64_t left = __ballot(is && x > kNone && before(x, word, last, last_i));
-    while (left) {
-      const int l = __builtin_ctzll(left);
-      left &= left - 1;
-      const float xl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), l));
-      const int wl = __builtin_amdgcn_readlane(word, l);
-      if (before(xl, wl, last, last_i)) put(xl, wl, top, lane);
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return lane & 32 ? a[0] : a[1];
+}
+template <int J>
+__device__ __forceinline__ Key other(Key k, int lane) {
+  return (Key)other<J>((uint32_t)(k >> 32), lane) << 32 | other<J>((uint32_t)k, lane);
+}
+template <int J>
+__device__ __forceinline__ float other(float v, int lane) { return __uint_as_float(other<J>(bits(v), lane)); }
+
+// One turn of a bitonic sort, falling over the wave: runs of K lanes, partners J apart.
+template <int K, int J, typename V>
+__device__ __forceinline__ void turn(V &v, int lane) {
+  const bool larger = ((lane & J) == 0) == ((lane & K) == 0 || K == kWave);
+  const V o = other<J>(v, lane);
+  v = (v > o) == larger ? v : o;
+  if constexpr (J > 1) turn<K, J / 2>(v, lane);
+}
+template <typename V>
+__device__ __forceinline__ void sort64(V &v, int lane) {
+  turn<2, 1>(v, lane), turn<4, 2>(v, lane), turn<8, 4>(v, lane), turn<16, 8>(v, lane), turn<32, 16>(v, lane);
+  turn<64, 32>(v, lane);
+}
+// The n-th largest of the lanes' values (n from 1), the same in every lane.
+__device__ __forceinline__ float nth(float v, int n, int lane) {
+  sort64(v, lane);
+  return __uint_as_float(__builtin_amdgcn_readlane(bits(v), n - 1));
+}
+
+// A wave's list: lanes 0 to 31 hold the largest keys seen, falling.
+struct List {
+  Key k;
+  float last;  // value of the top-th, the same in every lane
+  __device__ __forceinline__ void clear() { k = 0, last = kNone; }
+  __device__ __forceinline__ void close(int top) {
+    last = value_of((Key)__builtin_amdgcn_readlane((uint32_t)(k >> 32), top - 1) << 32 |
+                    (uint32_t)__builtin_amdgcn_readlane((uint32_t)k, top - 1));
+  }
+  __device__ __forceinline__ void put(Key x, int lane) {  // x: the same in every lane
+    const int at = __popcll(__ballot(k > x));
+    const Key up = (Key)(uint32_t)__builtin_amdgcn_update_dpp(0, (uint32_t)(k >> 32), 0x138, 0xF, 0xF, false) << 32 |
+                   (uint32_t)__builtin_amdgcn_update_dpp(0, (uint32_t)k, 0x138, 0xF, 0xF, false);  // of the lane before
+    k = lane > at ? up : lane == at ? x : k;
+  }
+  // n keys in `some`, 32 at a time.
+  __device__ __forceinline__ void sort_in(const Key *some, int n, int lane) {
+    for (int c = 0; c < n; c += 32) {
+      const int i = c + lane - 32;
+      if (lane >= 32) k = i < n ? some[i] : 0;
+      sort64(k, lane);
     }
   }
 };
-
-// The n-th largest of the lanes' values (n from 1), the same in every lane.
-__device__ __forceinline__ float nth(float v, int n, int lane) {
-#pragma unroll
-  for (int k = 2; k <= kWave; k *= 2)
-#pragma unroll
-    for (int j = k / 2; j > 0; j /= 2) {
-      const float o = __shfl_xor(v, j, kWave);
-      const bool larger = (lane & j) == 0 ? (lane & k) == 0 || k == kWave : !((lane & k) == 0 || k == kWave);
-      v = larger ? fmaxf(v, o) : fminf(v, o);
-    }
-  return __shfl(v, n - 1, kWave);
-}
+constexpr int kFew = 6;  // put in one by one
 
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {  // places past n: no weight
@@ -114,7 +149,7 @@ __device__ __forceinline__ float at(const void *p, int dtype, int64_t i) {
 // A row's results from its sums and list.
 __device__ __forceinline__ void finish(const replay_token_logprobs_args &a, int row, Sums z, const List &list, int lane) {
   const bool any = z.s > 0.f;
-  const float log_s = __builtin_amdgcn_logf(z.s) * kLn2;  // s is at least 1 where there is any weight
+  const float log2_s = __builtin_amdgcn_logf(z.s), log_s = log2_s * kLn2;  // s is at least 1 where there is any weight
   if (lane == 0) {
     const int tok = a.tokens[row];
     float lp = kNone;
@@ -123,20 +158,28 @@ __device__ __forceinline__ void finish(const replay_token_logprobs_args &a, int 
       if (x > kNone) lp = (x - z.m) - log_s;
     }
     a.logprobs[row] = lp;
-    a.entropy[row] = any ? log_s - z.t / z.s : 0.f;
+    a.entropy[row] = any ? (log2_s - z.t / z.s) * kLn2 : 0.f;
   }
   if (lane < a.top) {
-    const bool there = list.v > kNone;
-    a.top_logprobs[(int64_t)row * a.top + lane] = there ? (list.v - z.m) - log_s : kNone;
-    a.top_tokens[(int64_t)row * a.top + lane] = there ? list.i : -1;
+    a.top_logprobs[(int64_t)row * a.top + lane] = list.k ? (value_of(list.k) - z.m) - log_s : kNone;
+    a.top_tokens[(int64_t)row * a.top + lane] = word_of(list.k);
   }
+}
+
+// Every lane's sums joined.
+__device__ __forceinline__ void join_lanes(Sums &z, int lane) {
+  z.join(Sums{other<1>(z.m, lane), other<1>(z.s, lane), other<1>(z.t, lane)});
+  z.join(Sums{other<2>(z.m, lane), other<2>(z.s, lane), other<2>(z.t, lane)});
+  z.join(Sums{other<4>(z.m, lane), other<4>(z.s, lane), other<4>(z.t, lane)});
+  z.join(Sums{other<8>(z.m, lane), other<8>(z.s, lane), other<8>(z.t, lane)});
+  z.join(Sums{other<16>(z.m, lane), other<16>(z.s, lane), other<16>(z.t, lane)});
+  z.join(Sums{other<32>(z.m, lane), other<32>(z.s, lane), other<32>(z.t, lane)});
 }
 
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_args a, Slices sl) {
   __shared__ float4 part[kWaves];
-  __shared__ float sv[kWaves][REPLAY_MAX_TOP];
-  __shared__ int si[kWaves][REPLAY_MAX_TOP];
+  __shared__ Key some[kWaves][TOP ? kStep / kWaves : 1];  // a wave's words of one step beyond its list's last
   const int row = fdiv(blockIdx.x, sl.fn), slice = blockIdx.x - row * sl.n;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const T *x = (const T *)a.logits + (int64_t)row * a.stride;
@@ -150,64 +193,106 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
     load8<T>(x + at0, v1 - at0, xv);
     float largest = kNone;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xv[i] = clean(xv[i]), largest = fmaxf(largest, xv[i]);
+    for (int i = 0; i < 8; ++i) largest = fmaxf(largest, xv[i]);
+    if (largest > -kLowest) {  // +infinity
+      largest = kNone;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xv[i] = clean(xv[i]), largest = fmaxf(largest, xv[i]);
+    }
     z.scale_to(fmaxf(z.m, largest));
+    // The difference first: a product of m alone would be off by |m| 2^-24.
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float d = fmaxf(xv[i] - z.m, kLeast), e = __builtin_amdgcn_exp2f(d * kLog2e);
+      const float d = fmaxf((xv[i] - z.m) * kLog2e, kLeast), e = __builtin_amdgcn_exp2f(d);
       z.s += e, z.t = fmaf(e, d, z.t);
     }
     if constexpr (TOP) {
-      const uint64_t some = __ballot(largest > list.last);
-      if (some) {
-        // At least `top` words of these are as large as the top-th of the lanes' maxima.
+      const uint64_t beyond = __ballot(largest > list.last);
+      if (beyond) {
         float least = list.last;
-        if (__popcll(some) > a.top) least = fmaxf(least, nth(largest, a.top, lane));
+        if (__popcll(beyond) > a.top) least = fmaxf(least, nth(largest, a.top, lane));
+        int n = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) list.offer(xv[i], at0 + i, xv[i] >= least, a.top, lane);
+        for (int i = 0; i < 8; ++i) {
+          const bool is = xv[i] >= least && xv[i] > kNone;
+          const uint64_t mask = __ballot(is);
+          if (is) some[wave][n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
+              key_of(xv[i], at0 + i);
+          n += __popcll(mask);
+        }
+        wave_lds_sync();
+        if (n <= kFew)
+          for (int i = 0; i < n; ++i) list.put(some[wave][i], lane);
+        else
+          list.sort_in(some[wave], n, lane);
+        list.close(a.top);
+        wave_lds_sync();
       }
     }
   }
   // The waves in their order.
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) z.join(Sums{__shfl_xor(z.m, o, kWave), __shfl_xor(z.s, o, kWave), __shfl_xor(z.t, o, kWave)});
+  join_lanes(z, lane);
   if (lane == 0) part[wave] = make_float4(z.m, z.s, z.t, 0.f);
-  if (TOP && lane < a.top) sv[wave][lane] = list.v, si[wave][lane] = list.i;
+  if (TOP && lane < 32) some[wave][lane] = list.k;
   __syncthreads();
   if (wave) return;
   for (int w = 1; w < kWaves; ++w) {
     z.join(Sums{part[w].x, part[w].y, part[w].z});
-    if constexpr (TOP) list.offer(lane < a.top ? sv[w][lane] : kNone, lane < a.top ? si[w][lane] : 0, lane < a.top, a.top, lane);
+    if constexpr (TOP) {  // two falling lists, one of them turned round
+      if (lane >= 32) list.k = some[w][63 - lane];
+      turn<64, 32>(list.k, lane);
+    }
   }
   if (sl.n == 1) {
     finish(a, row, z, list, lane);
     return;
   }
-  const int64_t to = (int64_t)row * sl.n + slice;
-  if (lane == 0) sl.sums[to] = make_float4(z.m, z.s, z.t, 0.f);
-  if (TOP && lane < a.top) sl.values[to * a.top + lane] = list.v, sl.words[to * a.top + lane] = list.i;
+  if (lane == 0) sl.sums[(int64_t)row * sl.n + slice] = make_float4(z.m, z.s, z.t, 0.f);
+  if (TOP && lane < a.top) sl.keys[((int64_t)row * a.top + lane) * sl.n + slice] = list.k;
 }
 
-// Joins the slices of a row, a wave each: a lane's run of neighbours, then the lanes.
+// Joins the slices of a row, a wave each: a lane's slices, then the lanes.
+constexpr int kAhead = 8;  // entries of the lists loaded together
 __global__ __launch_bounds__(kWave) void join_k(replay_token_logprobs_args a, Slices sl) {
+  __shared__ Key some[kAhead * kWave];
   const int row = blockIdx.x, lane = threadIdx.x;
   const float4 *const sums = sl.sums + (int64_t)row * sl.n;
-  const int per = (sl.n + kWave - 1) / kWave;
+  const Key *const keys = sl.keys + (int64_t)row * sl.n * a.top;
   Sums z{kLowest, 0.f, 0.f};
-  for (int i = lane * per; i < min(sl.n, (lane + 1) * per); ++i) z.join(Sums{sums[i].x, sums[i].y, sums[i].z});
-#pragma unroll
-  for (int o = 1; o < kWave; o *= 2) z.join(Sums{__shfl_xor(z.m, o, kWave), __shfl_xor(z.s, o, kWave), __shfl_xor(z.t, o, kWave)});
   List list;
   list.clear();
-  // The slices' first words, then their second ones, and so on: the list is soon full of large ones.
-  const float *const values = sl.values + (int64_t)row * sl.n * a.top;
-  const int *const words = sl.words + (int64_t)row * sl.n * a.top;
-  for (int k = 0; k < a.top; ++k)
-    for (int s = 0; s < sl.n; s += kWave) {
-      const bool is = s + lane < sl.n;
-      const int64_t at = (int64_t)(is ? s + lane : 0) * a.top + k;
-      list.offer(values[at], words[at], is, a.top, lane);
+  for (int s0 = 0; s0 < sl.n; s0 += kWave) {
+    const bool is = s0 + lane < sl.n;
+    const int s = is ? s0 + lane : 0;
+    const float4 v = sums[s];
+    for (int k0 = 0; k0 < a.top; k0 += kAhead) {
+      Key k[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const Key x = keys[(int64_t)min(k0 + i, a.top - 1) * sl.n + s];
+        k[i] = is && k0 + i < a.top ? x : 0;
+      }
+      float least = list.last;
+      const float first = value_of(k[0]);
+      const uint64_t beyond = __ballot(first > least);
+      if (!beyond && !__ballot(first == least && first > kNone)) break;  // the lists fall: nothing further down either
+      if (__popcll(beyond) > a.top) least = fmaxf(least, nth(first, a.top, lane));
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const bool in = k[i] && value_of(k[i]) >= least;
+        const uint64_t mask = __ballot(in);
+        if (in) some[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = k[i];
+        n += __popcll(mask);
+      }
+      wave_lds_sync();
+      list.sort_in(some, n, lane);
+      list.close(a.top);
+      wave_lds_sync();
     }
+    if (is) z.join(Sums{v.x, v.y, v.z});
+  }
+  join_lanes(z, lane);
   finish(a, row, z, list, lane);
 }
 
@@ -222,7 +307,7 @@ Slices slices_of(int rows, int vocab) {
 }
 
 size_t sums_bytes(int rows, const Slices &s) { return ((size_t)rows * s.n * sizeof(float4) + 255) / 256 * 256; }
-size_t words_bytes(int rows, const Slices &s, int top) { return ((size_t)rows * s.n * top * 4 + 255) / 256 * 256; }
+size_t keys_bytes(int rows, const Slices &s, int top) { return (size_t)rows * s.n * top * sizeof(Key); }
 
 template <typename T>
 void launch(const replay_token_logprobs_args &a, const Slices &s, hipStream_t st) {
@@ -237,15 +322,14 @@ void launch(const replay_token_logprobs_args &a, const Slices &s, hipStream_t st
 
 size_t logprobs_workspace(int rows, int vocab, int top) {
   const Slices s = slices_of(rows, vocab);
-  return s.n == 1 ? 0 : sums_bytes(rows, s) + 2 * words_bytes(rows, s, top);
+  return s.n == 1 ? 0 : sums_bytes(rows, s) + keys_bytes(rows, s, top);
 }
 
 int launch_logprobs(const replay_token_logprobs_args &a, void *workspace, hipStream_t st) {
   Slices s = slices_of(a.rows, a.vocab);
   if ((int64_t)a.rows * s.n > kMostBlocks) return kTooLarge;
   s.sums = (float4 *)workspace;
-  s.values = (float *)((char *)workspace + sums_bytes(a.rows, s));
-  s.words = (int *)((char *)s.values + words_bytes(a.rows, s, a.top));
+  s.keys = (Key *)((char *)workspace + sums_bytes(a.rows, s));
   if (a.dtype == REPLAY_DT_BF16)
     launch<bf16_t>(a, s, st);
   else
