@@ -24,6 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kStep = 8 * kThreads;  // values a workgroup reads at a time, 8 a thread
+constexpr int kTurn = 2;             // such reads under way together
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f, kNone = -__builtin_inff();
 // Exponents below this are no weight at all; a product with it stays finite.
@@ -130,34 +131,52 @@ struct List {
     }
   }
 };
-constexpr int kFew = 6;  // put in one by one
+constexpr int kFew = 12;  // put in one by one: about as long as sorting them in
 
+// Eight neighbouring values as loaded; places past the n-th: no weight.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {  // places past n: no weight
-  if (n >= 8) {
-    load_vec<T, 8>(p, v);
-  } else {
+struct Eight {
+  static constexpr int W = sizeof(T) * 2;
+  typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));  // of its element only
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const loose v = *reinterpret_cast<const loose *>((const char *)p + 4 * i);
+      w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+    }
+  }
+  __device__ __forceinline__ void load(const T *p, int n) {
+    if (n >= 8) return load(p);
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? ldr<T>(p + i) : kNone;
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = sizeof(T) == 4 ? bits(v[i]) : __builtin_amdgcn_perm(bits(v[2 * i + 1]), bits(v[2 * i]), 0x07060302u);
   }
-}
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return i % 2 ? upper(w[i / 2]) : lower(w[i / 2]);
+  }
+};
 
 __device__ __forceinline__ float at(const void *p, int dtype, int64_t i) {
   return dtype == REPLAY_DT_BF16 ? ldr<bf16_t>((const bf16_t *)p + i) : ldr<float>((const float *)p + i);
 }
 
+// The logit of a row's token, -infinity for one outside the vocabulary: loaded early.
+__device__ __forceinline__ float chosen_of(const replay_token_logprobs_args &a, int row) {
+  const int tok = a.tokens[row];
+  return tok >= 0 && tok < a.vocab ? at(a.logits, a.dtype, (int64_t)row * a.stride + tok) : kNone;
+}
+
 // A row's results from its sums and list.
-__device__ __forceinline__ void finish(const replay_token_logprobs_args &a, int row, Sums z, const List &list, int lane) {
+__device__ __forceinline__ void finish(const replay_token_logprobs_args &a, int row, Sums z, const List &list, float chosen, int lane) {
   const bool any = z.s > 0.f;
   const float log2_s = __builtin_amdgcn_logf(z.s), log_s = log2_s * kLn2;  // s is at least 1 where there is any weight
   if (lane == 0) {
-    const int tok = a.tokens[row];
-    float lp = kNone;
-    if (any && tok >= 0 && tok < a.vocab) {
-      const float x = clean(at(a.logits, a.dtype, (int64_t)row * a.stride + tok));
-      if (x > kNone) lp = (x - z.m) - log_s;
-    }
-    a.logprobs[row] = lp;
+    const float x = clean(chosen);
+    a.logprobs[row] = x > kNone ? (x - z.m) - log_s : kNone;
     a.entropy[row] = any ? (log2_s - z.t / z.s) * kLn2 : 0.f;
   }
   if (lane < a.top) {
@@ -179,6 +198,7 @@ __device__ __forceinline__ void join_lanes(Sums &z, int lane) {
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_args a, Slices sl) {
   __shared__ float4 part[kWaves];
+  __shared__ float lasts[kWaves];
   __shared__ Key some[kWaves][TOP ? kStep / kWaves : 1];  // a wave's words of one step beyond its list's last
   const int row = fdiv(blockIdx.x, sl.fn), slice = blockIdx.x - row * sl.n;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -187,46 +207,81 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
   Sums z{kLowest, 0.f, 0.f};
   List list;
   list.clear();
-  for (int v = v0; v < v1; v += kStep) {
-    const int at0 = v + threadIdx.x * 8;
-    float xv[8];
-    load8<T>(x + at0, v1 - at0, xv);
-    float largest = kNone;
+  const float chosen = sl.n == 1 ? chosen_of(a, row) : 0.f;
+  // The next turn's loads are under way while this one is worked on.  No branch stands
+  // between the loads of a turn: each would wait for the one before.
+  Eight<T> raw[kTurn];
+  auto fetch = [&](int v) {
+    const T *const p = x + v + threadIdx.x * 8;
+    if (v + kTurn * kStep <= v1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) largest = fmaxf(largest, xv[i]);
+      for (int u = 0; u < kTurn; ++u) raw[u].load(p + u * kStep);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kTurn; ++u) raw[u].load(p + u * kStep, v1 - (v + (int)threadIdx.x * 8 + u * kStep));
+    }
+  };
+  if constexpr (TOP) {
+    if (lane == 0) lasts[wave] = kNone;
+    __syncthreads();
+  }
+  fetch(v0);
+  for (int v = v0; v < v1; v += kTurn * kStep) {
+    const int at0 = v + threadIdx.x * 8;
+    float xv[kTurn][8], largest = kNone;
+#pragma unroll
+    for (int u = 0; u < kTurn; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xv[u][i] = raw[u].get(i), largest = fmaxf(largest, xv[u][i]);
+    if (v + kTurn * kStep < v1) fetch(v + kTurn * kStep);
     if (largest > -kLowest) {  // +infinity
       largest = kNone;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xv[i] = clean(xv[i]), largest = fmaxf(largest, xv[i]);
+      for (int u = 0; u < kTurn; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xv[u][i] = clean(xv[u][i]), largest = fmaxf(largest, xv[u][i]);
     }
     z.scale_to(fmaxf(z.m, largest));
     // The difference first: a product of m alone would be off by |m| 2^-24.
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = fmaxf((xv[i] - z.m) * kLog2e, kLeast), e = __builtin_amdgcn_exp2f(d);
-      z.s += e, z.t = fmaf(e, d, z.t);
+    for (int u = 0; u < kTurn; ++u) {
+      if (v + u * kStep >= v1) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = fmaxf((xv[u][i] - z.m) * kLog2e, kLeast), e = __builtin_amdgcn_exp2f(d);
+        z.s += e, z.t = fmaf(e, d, z.t);
+      }
     }
     if constexpr (TOP) {
-      const uint64_t beyond = __ballot(largest > list.last);
-      if (beyond) {
-        float least = list.last;
-        if (__popcll(beyond) > a.top) least = fmaxf(least, nth(largest, a.top, lane));
-        int n = 0;
+      // As many words as the list holds reach the last entry of any wave's list.
+      float least = list.last;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool is = xv[i] >= least && xv[i] > kNone;
-          const uint64_t mask = __ballot(is);
-          if (is) some[wave][n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
-              key_of(xv[i], at0 + i);
-          n += __popcll(mask);
+      for (int w = 0; w < kWaves; ++w)
+        least = fmaxf(least, __hip_atomic_load(&lasts[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
+      const uint64_t beyond = __ballot(largest > list.last && largest >= least);
+      if (beyond) {
+        if (__popcll(beyond) > a.top) least = fmaxf(least, nth(largest, a.top, lane));
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u) {
+          int n = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool is = xv[u][i] >= least && xv[u][i] > kNone;
+            const uint64_t mask = __ballot(is);
+            if (is) some[wave][n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
+                key_of(xv[u][i], at0 + u * kStep + i);
+            n += __popcll(mask);
+          }
+          if (!n) continue;
+          wave_lds_sync();
+          if (n <= kFew)
+            for (int i = 0; i < n; ++i) list.put(some[wave][i], lane);
+          else
+            list.sort_in(some[wave], n, lane);
+          wave_lds_sync();
         }
-        wave_lds_sync();
-        if (n <= kFew)
-          for (int i = 0; i < n; ++i) list.put(some[wave][i], lane);
-        else
-          list.sort_in(some[wave], n, lane);
         list.close(a.top);
-        wave_lds_sync();
+        if (lane == 0) __hip_atomic_store(&lasts[wave], list.last, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
       }
     }
   }
@@ -244,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
     }
   }
   if (sl.n == 1) {
-    finish(a, row, z, list, lane);
+    finish(a, row, z, list, chosen, lane);
     return;
   }
   if (lane == 0) sl.sums[(int64_t)row * sl.n + slice] = make_float4(z.m, z.s, z.t, 0.f);
@@ -258,6 +313,7 @@ __global__ __launch_bounds__(kWave) void join_k(replay_token_logprobs_args a, Sl
   const int row = blockIdx.x, lane = threadIdx.x;
   const float4 *const sums = sl.sums + (int64_t)row * sl.n;
   const Key *const keys = sl.keys + (int64_t)row * sl.n * a.top;
+  const float chosen = chosen_of(a, row);
   Sums z{kLowest, 0.f, 0.f};
   List list;
   list.clear();
@@ -293,7 +349,7 @@ __global__ __launch_bounds__(kWave) void join_k(replay_token_logprobs_args a, Sl
     if (is) z.join(Sums{v.x, v.y, v.z});
   }
   join_lanes(z, lane);
-  finish(a, row, z, list, lane);
+  finish(a, row, z, list, chosen, lane);
 }
 
 // Slices of 2048 values, longer where there would be more than 2048 workgroups.
