@@ -42,7 +42,10 @@ struct Cell {
   static constexpr int MP = sizeof(Y) == 4 ? 3 : 2;  // pieces of P, U and S in the output products
   static constexpr int A0 = 0;                       // [3][kSteps]
   static constexpr int P0 = A0 + 3 * kSteps * kFrag;     // [MP][kSteps]
-  static constexpr int G0 = P0 + MP * kSteps * kFrag;    // e^{g_t} [64], e^{g_C - g_t} [64]
+  static constexpr int ROW = sizeof(R) / 2 * kFrag;      // a record's rows, as loaded
+  static constexpr int K0 = P0 + MP * kSteps * kFrag;    // [4 tiles of 16 tokens][NK]
+  static constexpr int Q0 = K0 + 4 * NK * ROW;
+  static constexpr int G0 = Q0 + 4 * NK * ROW;           // e^{g_t} [64], e^{g_C - g_t} [64]
   static constexpr int BYTES = G0 + 2 * Q * 4;
 };
 
@@ -57,15 +60,41 @@ struct DeltaPlan {
 // Eight neighbouring columns of a record's row: as loaded, and as an operand in IP pieces.
 template <typename R>
 struct Rows {
+  typedef uint16_t bits;
   uint4 v;
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, int plus) { v = buffer_load16(b, at, plus); }
+  __device__ __forceinline__ void get(__amdgpu_buffer_rsrc_t b, int lane, int plus) { v = buffer_load16(b, lane * 16, plus); }
+  // The first or second four alone.
+  __device__ __forceinline__ void get_half(__amdgpu_buffer_rsrc_t b, int lane, int half, int plus) {
+    const i32x2 x = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane * 16 + 8 * half, plus, 0));
+    v = make_uint4(x[0], x[1], 0, 0);
+  }
+  __device__ __forceinline__ void put(char *to, int lane) const { reinterpret_cast<uint4 *>(to)[lane] = v; }
+  __device__ __forceinline__ void stage(char *to, int) const { *reinterpret_cast<uint4 *>(to) = v; }
+  __device__ __forceinline__ void staged(const char *from, int) { v = *reinterpret_cast<const uint4 *>(from); }
   __device__ __forceinline__ void cut(Frag (&f)[1]) const { f[0].v = __builtin_bit_cast(s16x8, v); }
 };
 template <>
 struct Rows<float> {
+  typedef uint32_t bits;
   uint4 v, w;
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, int at, int plus) {
     v = buffer_load16(b, at, plus), w = buffer_load16(b, at, plus + 16);
+  }
+  __device__ __forceinline__ void get(__amdgpu_buffer_rsrc_t b, int lane, int plus) {
+    v = buffer_load16(b, lane * 16, plus), w = buffer_load16(b, lane * 16, plus + kFrag);
+  }
+  __device__ __forceinline__ void get_half(__amdgpu_buffer_rsrc_t b, int lane, int half, int plus) {
+    v = buffer_load16(b, lane * 16 + half * kFrag, plus), w = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void put(char *to, int lane) const {
+    reinterpret_cast<uint4 *>(to)[lane] = v, reinterpret_cast<uint4 *>(to + kFrag)[lane] = w;
+  }
+  __device__ __forceinline__ void stage(char *to, int plane) const {
+    *reinterpret_cast<uint4 *>(to) = v, *reinterpret_cast<uint4 *>(to + plane) = w;
+  }
+  __device__ __forceinline__ void staged(const char *from, int plane) {
+    v = *reinterpret_cast<const uint4 *>(from), w = *reinterpret_cast<const uint4 *>(from + plane);
   }
   __device__ __forceinline__ void cut(Frag (&f)[3]) const {
     const uint32_t e[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
@@ -88,6 +117,13 @@ __device__ __forceinline__ Frag get(const char *from, int lane) {
 
 constexpr int kT = Q + 4;  // floats of a row of T and A in LDS
 
+// Place of granule g of a row of K or Q in LDS, permuted so that 16 rows at one granule
+// meet in no bank.
+template <int NK>
+__device__ __forceinline__ int place_of(int row, int g) {
+  return row * 64 * NK + (g ^ (NK == 4 ? row & 15 : NK == 2 ? row >> 1 & 7 : row >> 2 & 3)) * 16;
+}
+
 // v where `keep`, else 0: a mask, since a condition would become a branch around v.
 __device__ __forceinline__ float only(float v, bool keep) { return __uint_as_float(bits(v) & (keep ? ~0u : 0u)); }
 
@@ -96,7 +132,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
 void cells_k(DeltaArgs a, DeltaPlan plan) {
   typedef Cell<R, Y, NK> C;
   constexpr int IP = C::IP, MP = C::MP;
-  __shared__ __attribute__((aligned(16))) float sT[Q * kT], sA[Q * kT], sD[kWaves][16][20], sB[Q];
+  constexpr int NV = 4 * NK, RB = kThreads / NV;           // granules of eight columns in a row, rows a load
+  constexpr int PL = sizeof(R) / 2, ROWS = Q * 16 * NV;    // planes of 16 bytes a granule, bytes of one
+  constexpr int TA = 2 * Q * kT * 4, KQ = 2 * PL * ROWS;
+  // K and Q, then (they are in registers) T and A.
+  __shared__ __attribute__((aligned(16))) char pool[TA > KQ ? TA : KQ];
+  float *const sT = reinterpret_cast<float *>(pool), *const sA = sT + Q * kT;
+  __shared__ __attribute__((aligned(16))) float sD[kWaves][16][20], sB[Q];
   __shared__ __attribute__((aligned(16))) double sG[Q];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane % 16, q = lane / 16;
@@ -115,35 +157,20 @@ void cells_k(DeltaArgs a, DeltaPlan plan) {
   const size_t nK = (size_t)((rem - 1) * rK + N) * sizeof(R);
   const auto bK = buffer_of((const R *)a.k + row0 * rK + (int64_t)h * N, nK);
   const auto bQ = buffer_of((const R *)a.q + row0 * rK + (int64_t)h * N, nK);
-  const int oK = (int)((r * rK + 8 * q) * sizeof(R)), tile = (int)(16 * rK * sizeof(R));
-  auto at = [&](int s) { return NK > 1 || 8 * q < N ? oK + 32 * s * (int)sizeof(R) : kNowhere; };
-
-  // P^T of this wave's rows of 16 tokens, G^T = (K K^T)^T of the rows 3 - wave; all four
-  // tiles of a row, of which those right of the diagonal are masked away.
-  const int wg = 3 - wave;
-  floatx4 aP[4], aG[4];
+  // Whole rows of K and Q, as neighbouring lanes read them, into LDS.
+  {
+    const int trow = tid / NV, g = tid % NV;
+    const int at = 8 * g < N && trow < Q ? (int)((trow * rK + 8 * g) * sizeof(R)) : kNowhere;
+    Rows<R> k[Q / RB > 0 ? Q / RB : 1], x[Q / RB > 0 ? Q / RB : 1];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) aP[j] = aG[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll IP == 1 ? NK : 1
-  for (int s = 0; s < NK; ++s) {
-    Rows<R> rk[4], rq, rg;
-    Frag k[4][IP], qf[IP], kg[IP];
+    for (int i = 0; i < Q / RB; ++i) k[i].load(bK, at, (int)(i * RB * rK * sizeof(R)));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) rk[j].load(bK, at(s), j * tile);
-    rq.load(bQ, at(s), wave * tile);
-    rg.load(bK, at(s), wg * tile);
+    for (int i = 0; i < Q / RB; ++i) x[i].load(bQ, at, (int)(i * RB * rK * sizeof(R)));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) rk[j].cut(k[j]);
-    rq.cut(qf), rg.cut(kg);
-#pragma unroll
-    for (int u = IP - 1; u >= 0; --u)
-#pragma unroll
-      for (int v = IP - 1 - u; v >= 0; --v)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          aP[j] = mfma32(k[j][u], qf[v], aP[j]);
-          aG[j] = mfma32(k[j][u], kg[v], aG[j]);
-        }
+    for (int i = 0; i < Q / RB; ++i) {
+      k[i].stage(pool + place_of<NK>(trow + i * RB, g), ROWS);
+      x[i].stage(pool + PL * ROWS + place_of<NK>(trow + i * RB, g), ROWS);
+    }
   }
   if (wave == 0) {
     double g = lane < rem ? (double)log2f(al) : 0.0;
@@ -153,6 +180,39 @@ void cells_k(DeltaArgs a, DeltaPlan plan) {
     float *const e = reinterpret_cast<float *>(cell + C::G0);
     e[lane] = __builtin_amdgcn_exp2f((float)g);
     e[Q + lane] = __builtin_amdgcn_exp2f((float)(lane_value(g, kWave - 1) - g));
+  }
+  __syncthreads();
+
+  // P^T of this wave's rows of 16 tokens, G^T = (K K^T)^T of the rows 3 - wave; all four
+  // tiles of a row, of which those right of the diagonal are masked away.
+  const int wg = 3 - wave;
+  floatx4 aP[4], aG[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) aP[j] = aG[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll IP == 1 ? NK : 1
+  for (int s = 0; s < NK; ++s) {
+    Rows<R> row;
+    Frag k[4][IP], qf[IP], kg[IP];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      row.staged(pool + place_of<NK>(16 * j + r, 4 * s + q), ROWS);
+      row.cut(k[j]);
+    }
+    row.staged(pool + PL * ROWS + place_of<NK>(16 * wave + r, 4 * s + q), ROWS);
+    row.put(cell + C::Q0 + (wave * NK + s) * C::ROW, lane);
+    row.cut(qf);
+    row.staged(pool + place_of<NK>(16 * wg + r, 4 * s + q), ROWS);
+    row.put(cell + C::K0 + (wg * NK + s) * C::ROW, lane);
+    row.cut(kg);
+#pragma unroll
+    for (int u = IP - 1; u >= 0; --u)
+#pragma unroll
+      for (int v = IP - 1 - u; v >= 0; --v)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          aP[j] = mfma32(k[j][u], qf[v], aP[j]);
+          aG[j] = mfma32(k[j][u], kg[v], aG[j]);
+        }
   }
   __syncthreads();
   {
@@ -266,25 +326,21 @@ __device__ __forceinline__ void hand(char *to, int gap, const floatx4 &v) {
   for (int u = 0; u < NP; ++u) *reinterpret_cast<uint2 *>(to + u * gap) = make_uint2(a[u], b[u]);
 }
 
-// Byte of a granule of eight columns in its row of K in LDS, permuted so that neither the
-// writes (16 rows at a granule) nor the transposing reads (eight rows at two granules) meet
-// in a bank (rows of 128 and 64 bytes: the reads).
-template <int NK>
-__device__ __forceinline__ int granule(int row, int g) {
-  return (g ^ (NK == 4 ? 2 * (row & 7) | (row >> 3 & 1) : NK == 2 ? row & 6 : row >> 1 & 2)) * 16;
-}
-
 // Waves 0 to 3 carry the state, waves 4 to 7 make the outputs; wave w of either has the
-// chunk's tokens 16 w .. + 15.
+// chunk's tokens 16 w .. + 15, and of the former the state's columns 32 w .. + 31 too, in
+// two tiles: row 4 q + i of tile m is column 8 q + 4 m + i.  Where there are 64 or fewer
+// columns a wave has one of two such tiles.
 template <typename R, typename Y, int NK, int CT>
 __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan plan) {
   typedef Cell<R, Y, NK> C;
   constexpr int IP = C::IP, MP = C::MP, COLS = 16 * CT;
   constexpr int MT = NK == 4 ? 2 : 1;                // tiles of the state's columns that a wave has
+  constexpr int CW = NK == 1 ? 2 : 4;                // waves that have any
   constexpr int SR = 64 * NK + 16, TR = 2 * Q + 16;  // bytes of a row of S, and of 64 tokens, in LDS
-  constexpr int KR = 64 * NK;                        // bytes of a row of K in LDS
-  __shared__ __attribute__((aligned(16))) char sS[3][COLS * SR], sR[3][COLS * TR], sW[3][COLS * TR], sU[MP][COLS * TR];
-  __shared__ __attribute__((aligned(16))) char sK[IP][Q * KR];
+  constexpr int KR = 64;                             // bytes of a row of a wave's columns of K in LDS
+  __shared__ __attribute__((aligned(16))) char sS[MP][COLS * SR], sR[3][COLS * TR], sW[3][COLS * TR], sU[MP][COLS * TR];
+  __shared__ __attribute__((aligned(16))) char sK[kWaves][IP][Q * KR];
+  __shared__ float4 sX[CW][kWaves][CT][kWave];
   const int tid = threadIdx.x, lane = tid % kWave, eighth = __builtin_amdgcn_readfirstlane(tid / kWave), wave = eighth % 4;
   const int r = lane % 16, q = lane / 16;
   // Unit u, a sequence's head, on XCD u % 8: its slices share what cells_k left in an L2.
@@ -303,18 +359,12 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
 
   // Everything that a chunk reads from memory is loaded a chunk ahead, right behind the use
   // of the chunk before; behind the last one the loads repeat it, or read nothing.
-  const int64_t rK = (int64_t)a.H * N, rV = (int64_t)a.H * P, cells = (int64_t)a.H * C::BYTES;
+  const int64_t rV = (int64_t)a.H * P, cells = (int64_t)a.H * C::BYTES;
   const char *cell = plan.cells + ((int64_t)(base + c0 - plan.lo) * a.H + h) * C::BYTES;
   const int64_t row0 = (int64_t)begin + c0 * Q;
   int rem = len - c0 * Q;  // of the chunk to be loaded next
   const int most = wave / 2;  // the last step of the wave's rows of the lower triangle
   const int oF0 = step_of(wave, 0) * kFrag + lane * 16, oF1 = step_of(wave, min(1, most)) * kFrag + lane * 16;
-  const int oK = (int)(((16 * wave + r) * rK + 8 * q) * sizeof(R));
-  auto at_k = [&](int s) { return NK > 1 || 8 * q < N ? oK + 32 * s * (int)sizeof(R) : kNowhere; };
-  auto rows_k = [&](const char *p) {
-    const int m = min(rem, Q);
-    return buffer_of(p, m > 0 ? (size_t)((m - 1) * rK + N) * sizeof(R) : 0);
-  };
   auto rows_v = [&](const void *p, int esize) {
     const int m = min(rem, Q);
     return buffer_of(p, m > 0 ? (size_t)((m - 1) * rV + COLS) * esize : 0);
@@ -327,10 +377,11 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
   const int oF = r * TR + 16 * q;  // of 64 tokens' row r, slots 8 q .. + 7
 
   if (eighth < 4) {
-    // The state, transposed: tile m of this wave, columns 16 (wave + 4 m) + 4 q + i of k, row r of the slice's tile.
+    // The state, transposed: columns s0 + 4 m + i of k, row r of the slice's tile.
     floatx4 S[MT][CT];
-    auto there = [&](int m) { return NK > 1 || wave + 4 * m < 2 * NK; };
-    const size_t tile0 = ((size_t)row * a.H + h) * P * N + (size_t)(slice * COLS + r) * N + 16 * wave + 4 * q;
+    const int s0 = (MT == 2 ? 32 * wave : 32 * (wave / 2) + 4 * (wave % 2)) + 8 * q;
+    const bool any = CW == 4 || wave < CW;
+    const size_t tile0 = ((size_t)row * a.H + h) * P * N + (size_t)(slice * COLS + r) * N + s0;
     const bool known = a.initial && (!a.p.resume || a.p.resume[seq]);
     const float *const from = c0 ? a.state : known ? a.initial : nullptr;
 #pragma unroll
@@ -338,32 +389,29 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         S[m][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (from && 16 * (wave + 4 * m) < N) {
-          const float4 v = ld4(from + tile0 + (size_t)16 * ct * N + 64 * m);
+        if (from && s0 < N) {
+          const float4 v = ld4(from + tile0 + (size_t)16 * ct * N + 4 * m);
           S[m][ct] = floatx4{v.x, v.y, v.z, v.w};
         }
       }
-    auto hand_state = [&]() {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          if (there(m)) hand<3>(sS[0] + (16 * ct + r) * SR + (16 * (wave + 4 * m) + 4 * q) * 2, COLS * SR, S[m][ct]);
-    };
-    const char *pK = (const char *)((const R *)a.k + row0 * rK + (int64_t)h * N);
     const char *pV = (const char *)((const R *)a.v + row0 * rV + (int64_t)h * P + slice * COLS);
     int oV[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) oV[i] = (int)(((16 * wave + 4 * q + i) * rV + r) * sizeof(R));
-    Rows<R> kr[NK];
+    Rows<R> kr[4];
     Frag af[2][3];
-    float v[CT][4];
+    typename Rows<R>::bits v[CT][4];  // as loaded: a conversion would wait for it
     float4 eg4, left4;
     float whole;
     auto load_k = [&]() {
-      const auto b = rows_k(pK);
+      const auto b = buffer_of(cell, C::BYTES);
 #pragma unroll
-      for (int s = 0; s < NK; ++s) kr[s].load(b, at_k(s), 0);
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (MT == 2)
+          kr[t].get(b, lane, C::K0 + (t * NK + wave) * C::ROW);
+        else
+          kr[t].get_half(b, lane, wave % 2, C::K0 + (t * NK + (any ? wave / 2 : 0)) * C::ROW);
+      }
     };
     auto load_v = [&]() {
       const auto b = rows_v(pV, sizeof(R));
@@ -372,16 +420,17 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (IP == 1)
-            v[ct][i] = lower((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, oV[i] + 32 * ct, 0, 0));
+            v[ct][i] = __builtin_amdgcn_raw_buffer_load_b16(b, oV[i] + 32 * ct, 0, 0);
           else
-            v[ct][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, oV[i] + 64 * ct, 0, 0));
+            v[ct][i] = __builtin_amdgcn_raw_buffer_load_b32(b, oV[i] + 64 * ct, 0, 0);
         }
     };
-    auto load_g = [&]() {
-      const auto b = buffer_of(cell, C::BYTES);
-      eg4 = __builtin_bit_cast(float4, buffer_load16(b, 64 * wave + 16 * q, C::G0));
-      left4 = __builtin_bit_cast(float4, buffer_load16(b, 64 * wave + 16 * q, C::G0 + 4 * Q));
-      whole = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, 4 * (Q - 1), C::G0, 0));
+    auto load_eg = [&]() { eg4 = __builtin_bit_cast(float4, buffer_load16(buffer_of(cell, C::BYTES), 64 * wave + 16 * q, C::G0)); };
+    auto load_left = [&]() {
+      left4 = __builtin_bit_cast(float4, buffer_load16(buffer_of(cell, C::BYTES), 64 * wave + 16 * q, C::G0 + 4 * Q));
+    };
+    auto load_whole = [&]() {
+      whole = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer_of(cell, C::BYTES), 4 * (Q - 1), C::G0, 0));
     };
     auto load_a = [&]() {
       const auto b = buffer_of(cell, C::BYTES);
@@ -391,54 +440,100 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
         af[1][u] = operand(b, oF1, C::A0 + u * kSteps * kFrag);
       }
     };
-    // Where this lane writes its rows of K in LDS, and reads K's columns from: the transposing
-    // read leaves column r of rows 4 q .. + 3 in a lane, in the order of the slots.
-    char *const toK = sK[0] + (16 * wave + r) * KR;
-    const char *const fromK = sK[0] + (4 * q + r / 4) * KR + r % 2 * 8;
-    if (c0 < c1) load_k(), load_v(), load_g(), load_a();
-    hand_state();
+    // K in LDS, the wave's own columns: rows of eight 8-byte granules, permuted so that
+    // neither the writes (16 rows at two granules) nor the transposing reads (eight rows at
+    // every second granule) meet in a bank.  Those leave four rows 4 q .. + 3 of the column
+    // that is row r of a tile in a lane.
+    auto turned = [](int g) { return (g & 1) | (g >> 1) * 4; };
+    char *const toK = sK[wave][0] + r * KR;
+    const char *const fromK = sK[wave][0] + (4 * q + r / 4) * KR;
+    int gw[2], gr[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) gw[m] = ((2 * q + m) ^ turned(r >> 2)) * 8, gr[m] = ((2 * (r % 4) + m) ^ turned(q)) * 8;
+    if (c0 < c1) {  // in the loop's order: what waits for the first must not wait for the last
+      load_k();
+      __builtin_amdgcn_sched_barrier(0);
+      load_v();
+      load_eg();
+      __builtin_amdgcn_sched_barrier(0);
+      load_a();
+      load_left();
+      __builtin_amdgcn_sched_barrier(0);
+      load_whole();
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // Place of the wave's tokens 4 q + i in a row of 64: step wave / 2, half wave % 2.
     const int oT = r * TR + (32 * (wave / 2) + 8 * q + 4 * (wave % 2)) * 2;
     for (int c = c0; c < c1; ++c) {
       rem -= Q;
-      pK += Q * rK * sizeof(R), pV += Q * rV * sizeof(R);
+      pV += Q * rV * sizeof(R);
       if (c + 1 < c1) cell += cells;
-      lds_barrier();  // S is there
-      floatx4 X[CT];
+      // K S^T summed over the wave's columns, all tokens; S goes to the output waves.
+      if (any) {
+        Frag kf[4][IP];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) X[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t) {
+          kr[t].cut(kf[t]);
 #pragma unroll
-      for (int s = 0; s < NK; ++s) {
-        Frag kf[IP];
-        kr[s].cut(kf);
+          for (int u = 0; u < IP; ++u)
 #pragma unroll
-        for (int u = 0; u < IP; ++u)
-          *reinterpret_cast<s16x8 *>(toK + u * Q * KR + granule<NK>(r, 4 * s + q)) = kf[u].v;
+            for (int m = 0; m < MT; ++m) *reinterpret_cast<s16x4 *>(toK + (u * Q + 16 * t) * KR + gw[m]) = kf[t][u].h[m];
+        }
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           Frag sf[3];
 #pragma unroll
-          for (int u = 0; u < 3; ++u) sf[u].v = *reinterpret_cast<const s16x8 *>(sS[u] + (16 * ct + r) * SR + (32 * s + 8 * q) * 2);
+          for (int m = 0; m < 2; ++m) {
+            uint32_t w0[3] = {0, 0, 0}, w1[3] = {0, 0, 0};
+            if (m < MT) {
+              pieces<3>(S[m < MT ? m : 0][ct][0], S[m < MT ? m : 0][ct][1], w0);
+              pieces<3>(S[m < MT ? m : 0][ct][2], S[m < MT ? m : 0][ct][3], w1);
+            }
+#pragma unroll
+            for (int u = 0; u < 3; ++u) sf[u].w[2 * m] = w0[u], sf[u].w[2 * m + 1] = w1[u];
+          }
+#pragma unroll
+          for (int u = 0; u < MP; ++u) {
+            if constexpr (MT == 2)
+              *reinterpret_cast<s16x8 *>(sS[u] + (16 * ct + r) * SR + (32 * wave + 8 * q) * 2) = sf[u].v;
+            else
+              *reinterpret_cast<s16x4 *>(sS[u] + (16 * ct + r) * SR + (32 * (wave / 2) + 8 * q + 4 * (wave % 2)) * 2) = sf[u].h[0];
+          }
+          floatx4 X[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) X[t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int u = 2; u >= 0; --u)
 #pragma unroll
             for (int w = IP - 1; w >= 0; --w)
-              if (u + w < 3) X[ct] = mfma32(kf[w], sf[u], X[ct]);
+              if (u + w < 3) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) X[t] = mfma32(kf[t][w], sf[u], X[t]);
+              }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) sX[wave][t][ct][lane] = make_float4(X[t][0], X[t][1], X[t][2], X[t][3]);
         }
       }
       load_k();
-      const float egv[4] = {eg4.x, eg4.y, eg4.z, eg4.w}, lev[4] = {left4.x, left4.y, left4.z, left4.w}, all = whole;
+      lds_barrier();  // the waves' sums are there, and S
+      Frag kt[MT][2][IP];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
+        float4 x = sX[0][wave][ct][lane];
+#pragma unroll
+        for (int w = 1; w < CW; ++w) {
+          const float4 y = sX[w][wave][ct][lane];
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        const float egv[4] = {eg4.x, eg4.y, eg4.z, eg4.w}, xv[4] = {x.x, x.y, x.z, x.w};
         floatx4 d;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = fmaf(-egv[i], X[ct][i], v[ct][i]);
+        for (int i = 0; i < 4; ++i) d[i] = fmaf(-egv[i], xv[i], IP == 1 ? lower((uint32_t)v[ct][i]) : __uint_as_float(v[ct][i]));
         hand<3>(sR[0] + 16 * ct * TR + oT, COLS * TR, d);
       }
       load_v();
-      load_g();
-      lds_barrier();  // V - K S^T is there, and K
-      Frag kt[MT][2][IP];
+      load_eg();
+      lds_barrier();  // V - K S^T is there
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -446,9 +541,8 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
 #pragma unroll
           for (int u = 0; u < IP; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              kt[m][ts][u].h[e] = read_tr(fromK + (u * Q + 32 * ts + 16 * e) * KR +
-                                          granule<NK>(4 * q + r / 4, 2 * (there(m) ? wave + 4 * m : 0) + r % 4 / 2));
+            for (int e = 0; e < 2; ++e) kt[m][ts][u].h[e] = read_tr(fromK + (u * Q + 32 * ts + 16 * e) * KR + gr[m]);
+      const float lev[4] = {left4.x, left4.y, left4.z, left4.w};
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         floatx4 U = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -469,44 +563,49 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
         hand<3>(sW[0] + 16 * ct * TR + oT, COLS * TR, U);
       }
       load_a();
+      load_left();
       lds_barrier();  // U is there
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) S[m][ct] *= all;
+        for (int ct = 0; ct < CT; ++ct) {
+          S[m][ct] *= whole;
+          asm volatile("" : "+v"(S[m][ct]));  // before the next value is loaded: a copy of it would wait for the load
+        }
+      load_whole();
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts) {
           Frag wf[3];
 #pragma unroll
           for (int u = 0; u < 3; ++u) wf[u].v = *reinterpret_cast<const s16x8 *>(sW[u] + 16 * ct * TR + oF + 64 * ts);
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int u = 2; u >= 0; --u)
 #pragma unroll
-            for (int u = 2; u >= 0; --u)
+            for (int w = IP - 1; w >= 0; --w)
+              if (u + w < 3) {
 #pragma unroll
-              for (int w = IP - 1; w >= 0; --w)
-                if (u + w < 3) S[m][ct] = mfma32(kt[m][ts][w], wf[u], S[m][ct]);
+                for (int m = 0; m < MT; ++m) S[m][ct] = mfma32(kt[m][ts][w], wf[u], S[m][ct]);
+              }
         }
-      }
-      hand_state();
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        if (16 * (wave + 4 * m) < N)
-          st4(a.state + tile0 + (size_t)16 * ct * N + 64 * m, make_float4(S[m][ct][0], S[m][ct][1], S[m][ct][2], S[m][ct][3]));
+        if (s0 < N)
+          st4(a.state + tile0 + (size_t)16 * ct * N + 4 * m, make_float4(S[m][ct][0], S[m][ct][1], S[m][ct][2], S[m][ct][3]));
   } else {
-    const char *pQ = (const char *)((const R *)a.q + row0 * rK + (int64_t)h * N);
     char *pY = (char *)((Y *)a.y + row0 * rV + (int64_t)h * P + slice * COLS);
     const int oY = (int)(((16 * wave + r) * rV + 4 * q) * sizeof(Y));
     Rows<R> qr[NK];
     Frag pf[2][MP];
     float eg;
     auto load_q = [&]() {
-      const auto b = rows_k(pQ);
+      const auto b = buffer_of(cell, C::BYTES);
 #pragma unroll
-      for (int s = 0; s < NK; ++s) qr[s].load(b, at_k(s), 0);
+      for (int s = 0; s < NK; ++s) qr[s].get(b, lane, C::Q0 + (wave * NK + s) * C::ROW);
     };
     auto load_g = [&]() {
       eg = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer_of(cell, C::BYTES), 64 * wave + 4 * r, C::G0, 0));
@@ -519,11 +618,24 @@ __global__ __launch_bounds__(2 * kThreads) void chain_k(DeltaArgs a, DeltaPlan p
         pf[1][u] = operand(b, oF1, C::P0 + u * kSteps * kFrag);
       }
     };
-    if (c0 < c1) load_q(), load_g(), load_p();
+    if (c0 < c1) {
+      load_q();
+      __builtin_amdgcn_sched_barrier(0);
+      load_g();
+      __builtin_amdgcn_sched_barrier(0);
+      load_p();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    uint32_t far = 0;
     for (int c = c0; c < c1; ++c) {
+      // A line a lane of the cell two chunks on, a part of it in every slice: then it is in the
+      // L2 that the slices share when they load it (8192 tokens: 199 us, 187 with it).
+      asm volatile("" ::"v"(far));
+      if (eighth == 4 && c + 2 < c1)
+        far = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(cell + 2 * cells, C::BYTES), (slice * kWave + lane) * 128, 0, 0);
       const auto bY = rows_v(pY, sizeof(Y));  // rows past the end are not written
       rem -= Q;
-      pQ += Q * rK * sizeof(R), pY += Q * rV * sizeof(Y);
+      pY += Q * rV * sizeof(Y);
       if (c + 1 < c1) cell += cells;
       lds_barrier();  // S is there
       floatx4 O[CT];
