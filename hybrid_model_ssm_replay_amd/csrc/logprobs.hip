@@ -345,6 +345,8 @@ __global__ __launch_bounds__(kWave) void join_k(replay_token_logprobs_args a, Sl
       list.sort_in(some, n, lane);
       list.close(a.top);
       wave_lds_sync();
+      const float next = value_of(k[kAhead - 1]);  // at least what follows
+      if (!__ballot(next >= list.last && next > kNone)) break;
     }
     if (is) z.join(Sums{v.x, v.y, v.z});
   }
