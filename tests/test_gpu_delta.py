@@ -267,3 +267,103 @@ def test_other_stream_and_captured_calls():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, eager) and torch.equal(s, eager_state), turn
+
+
+def spread(n, tokens, seed):
+    """n lengths that differ widely and add up to about `tokens`."""
+    r = np.random.default_rng(seed).exponential(1.0, n) ** 2
+    return [int(x) for x in r * tokens / r.sum()]
+
+
+MANY = [
+    # sequences x heads that fill the card, as above
+    (128, 64, 64, [130], None, "bf16"),
+    (64, 128, 128, [1, 200], [1, 0], "f32"),
+    (64, 96, 128, [65, 64], "all", "bf16"),
+    (43, 80, 64, [70, 0, 3], [0, 1, 1], "f32"),
+    (32, 128, 128, [20, 300, 1, 900, 64, 250, 0, 100], [1, 0, 1, 1, 0, 1, 1, 0], "f32"),
+    (32, 112, 64, [900, 64, 300, 1, 250, 20, 0, 100], "all", "bf16"),
+    (64, 64, 128, [100, 500, 0, 450, 65], None, "bf16"),
+    (3, 32, 64, [17, 0, 1, 64, 65, 2] * 32, "all", "f32"),
+    (1, 32, 64, spread(300, 60000, 1), "all", "bf16"),
+    (2, 16, 64, spread(800, 3000, 2), "all", "f32"),
+]
+
+
+@pytest.mark.parametrize("H,P,N,lens,resumed,out", MANY)
+def test_delta_prompt_of_many_heads_and_sequences(H, P, N, lens, resumed, out):
+    announce("delta_prompt many", H, P, N, len(lens), lens[:8], resumed, out)
+    p = DeltaPrompts(H, P, N, lens, resumed, "bf16", tail=200).surround()
+    check(p, out, *p.run(out))
+
+
+@pytest.mark.parametrize("H,P,N,lens,name", [(4, 64, 128, [65, 30], "bf16"), (3, 32, 32, [1, 64], "f32"), (70, 64, 64, [65, 30], "bf16")])
+def test_rows_behind_the_last_sequence_are_not_read_nor_written(H, P, N, lens, name):
+    import torch
+    from hybrid_model_ssm_replay_amd import binding as B
+    from hybrid_model_ssm_replay_amd import ops
+    announce("delta_prompt rows behind", H, P, N, lens, name)
+    p = DeltaPrompts(H, P, N, lens, "all", name, tail=200).surround()
+    check(p, "f32", *p.run("f32"))
+    # The outputs of those rows stay what they are.
+    t, state, start = p.tensors(), torch.zeros((p.batch,) + p.shape, device="cuda"), torch.from_numpy(p.start).cuda()
+    at, args, y, ws = ops.delta_call(*t, start, state, None, None, None, None, None)
+    y.fill_(7.0)
+    ops.launch(B.replay_delta_prompt, at, *args)
+    torch.cuda.synchronize()
+    assert bool((y[:p.lead] == 7).all()) and bool((y[p.tokens - p.tail:] == 7).all())
+    assert bool(torch.isfinite(y).all()) and not bool((y[p.lead:p.tokens - p.tail] == 7).all())
+
+
+@pytest.mark.parametrize("what", ["same keys", "alpha 0", "tiny alpha", "beta 2", "zero keys"])
+def test_delta_prompt_of_many_heads_extremes(what):
+    announce("delta_prompt many extremes", what)
+    p = DeltaPrompts(64, 64, 64, [150, 70], "all", "bf16", seed=3)
+    r = np.random.default_rng(5)
+    if what == "same keys":
+        p.k[:], p.beta[:], p.alpha[:] = p.k[:1], 1.0, 1.0
+    elif what == "alpha 0":
+        p.alpha[r.random(p.alpha.shape) < 0.1] = 0.0
+    elif what == "tiny alpha":
+        p.alpha[r.random(p.alpha.shape) < 0.3] = 1e-38
+    elif what == "beta 2":
+        p.beta[:] = 2.0
+    else:
+        p.k[r.random(p.tokens) < 0.5] = 0.0
+        p.q[r.random(p.tokens) < 0.2] = 0.0
+    if what in ("same keys", "beta 2"):  # bf16 keys are longer than 1 by up to 2^-8: shrink them
+        p.k *= np.float32(1 - 2.0 ** -7)
+    p.surround()
+    check(p, "f32", *p.run("f32"))
+
+
+@pytest.mark.parametrize("H,lens", [(64, [1, 200]), (32, [20, 300, 1, 900, 64, 250, 0, 100])])
+def test_many_heads_on_another_stream_in_place_and_captured(H, lens):
+    """Two streams at once, and replays of a graph, give what one call gives."""
+    import torch
+    from hybrid_model_ssm_replay_amd import ops
+    announce("delta_prompt many captured", H, lens)
+    p = DeltaPrompts(H, 128, 128, lens, "all", "bf16")
+    t, start, rows = p.tensors(), torch.from_numpy(p.start).cuda(), torch.from_numpy(p.rows).cuda()
+    init = torch.from_numpy(p.init).nan_to_num(0.0).cuda()
+    want_s = init.clone()
+    want = ops.delta_prompt(*t, start, want_s, initial=want_s, rows=rows)
+    torch.cuda.synchronize()
+    states, got, streams = [init.clone(), init.clone()], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for s, st in zip(streams, states):
+        with torch.cuda.stream(s):
+            got.append(ops.delta_prompt(*t, start, st, initial=st, rows=rows))
+    torch.cuda.synchronize()
+    inside = slice(p.lead, p.tokens - p.tail)
+    for y, st in zip(got, states):
+        assert torch.equal(y[inside], want[inside]) and torch.equal(st, want_s)
+    state, graph = init.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ops.delta_prompt(*t, start, state, initial=state, rows=rows)
+    for _ in range(3):
+        state.copy_(init)
+        y.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y[inside], want[inside]) and torch.equal(state, want_s)
