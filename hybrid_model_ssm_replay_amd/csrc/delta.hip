@@ -1086,12 +1086,14 @@ void walk_k(DeltaArgs a, DeltaPlan plan) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const floatx4 o = O[t];
-      const int to = (int)(16 * t * rV * sizeof(Y));
+      // All of it in the vector offset: a 16-byte store with a scalar one may send the registers'
+      // next values if an instruction rewrites them right behind it.
+      const int to = oY + (int)(16 * t * rV * sizeof(Y));
       if constexpr (sizeof(Y) == 2)
-        __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, oY, to, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)pack_bf16(o[0], o[1]), (int)pack_bf16(o[2], o[3])}, bY, to, 0, 0);
       else
         __builtin_amdgcn_raw_buffer_store_b128(
-            i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, oY, to, 0);
+            i32x4{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])}, bY, to, 0, 0);
     }
   }
 #pragma unroll
