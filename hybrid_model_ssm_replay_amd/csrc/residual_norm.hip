@@ -8,7 +8,9 @@
 // one rounded product with the root, the largest |out| of a group is that of w h times
 // the root, and one turn through the row's lanes adds up the squares and finds it.
 //
-// HBM bound: a row stays in registers from its one read to its writes.
+// HBM bound: a row stays in registers from its one read to its writes.  8192 rows of 8192
+// (bf16): 98.7 us, 5.4 TB/s; 8192 rows of 4096 in e4m3 with scales of 128: 46 us, 5.1 TB/s; 256
+// rows of 4096: 4.9 us with its launch, the latency of one read, one sum and one write.
 #include "codecs.h"
 #include "ops.h"
 
@@ -17,6 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kCus = 256, kResident = 8;  // compute units, and workgroups of kThreads that one holds
 struct e4m3_t {};  // an output of codes and scales
 
 struct NormArgs {
@@ -72,12 +75,13 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int n, const float (&v)[
 
 // LANES threads a row (a wave, or the workgroup), IT steps of eight values each.
 template <typename TX, typename TR, typename TO, int LANES, int IT>
-__global__ __launch_bounds__(kThreads) void residual_norm_k(NormArgs n) {
+__global__ __launch_bounds__(LANES == kWave ? kThreads : LANES) void residual_norm_k(NormArgs n) {
   constexpr bool CODES = std::is_same<TO, e4m3_t>::value;
-  __shared__ float part[2][kWaves];
+  constexpr int ROWS = LANES == kWave ? kThreads / kWave : 1, WAVES = LANES / kWave;
+  __shared__ float part[2][WAVES];
   const replay_residual_norm_args &a = n.a;
   const int lane = threadIdx.x % LANES, wave = threadIdx.x / kWave;
-  const int t = blockIdx.x * (kThreads / LANES) + (LANES == kWave ? wave : 0), C = a.channels;
+  const int t = blockIdx.x * ROWS + (LANES == kWave ? wave : 0), C = a.channels;
   if (t >= a.tokens) return;  // LANES == kWave: no barrier follows
   const TX *x = (const TX *)a.x + t * a.x_stride + lane * 8;
   const TR *res = (const TR *)a.residual + t * a.residual_stride + lane * 8;
@@ -125,8 +129,9 @@ __global__ __launch_bounds__(kThreads) void residual_norm_k(NormArgs n) {
   if constexpr (LANES > kWave) {
     if (threadIdx.x % kWave == 0) part[0][wave] = ss, part[1][wave] = largest;
     __syncthreads();
-    ss = part[0][0] + part[0][1] + part[0][2] + part[0][3];
-    largest = fmaxf(fmaxf(part[1][0], part[1][1]), fmaxf(part[1][2], part[1][3]));
+    ss = part[0][0], largest = part[1][0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) ss += part[0][w], largest = fmaxf(largest, part[1][w]);
   }
   const float r = rsqrtf(ss / (float)C + a.eps);
 #pragma unroll
@@ -146,7 +151,9 @@ __global__ __launch_bounds__(kThreads) void residual_norm_k(NormArgs n) {
   }
 }
 
-// Longer rows: a workgroup each, two passes (the second reads what the first left in L2).
+// Rows of more than 16384: a workgroup each, two passes (the second reads what the first left
+// in L2): 4096 rows of 24576 231 us, 3.5 TB/s of the one read and the writes; 4096 of 16384 146
+// where one pass takes 101.
 // Nothing is written in the first, so the sum may take the place of an input.
 template <typename TX, typename TR, typename TO>
 __global__ __launch_bounds__(kThreads) void residual_norm_long_k(NormArgs n) {
@@ -225,20 +232,36 @@ __global__ __launch_bounds__(kThreads) void residual_norm_long_k(NormArgs n) {
 
 template <typename TX, typename TR, typename TO, int LANES, int IT>
 int launch_fast(const NormArgs &n, hipStream_t st) {
-  constexpr int PER = kThreads / LANES;
+  constexpr int PER = LANES == kWave ? kThreads / kWave : 1, THREADS = LANES == kWave ? kThreads : LANES;
   const int64_t blocks = ((int64_t)n.a.tokens + PER - 1) / PER;
-  if (blocks > kMostBlocks) return kTooLarge;
-  hipLaunchKernelGGL((residual_norm_k<TX, TR, TO, LANES, IT>), dim3((uint32_t)blocks), dim3(kThreads), 0, st, n);
+  if (blocks * THREADS >= (int64_t)1 << 32) return kTooLarge;
+  hipLaunchKernelGGL((residual_norm_k<TX, TR, TO, LANES, IT>), dim3((uint32_t)blocks), dim3(THREADS), 0, st, n);
   return (int)hipGetLastError();
+}
+
+// A row's threads.  More than 256, and so fewer steps, where a CU has two rows at most, whose
+// latency counts (256 rows of 4096: 4.9 us, 5.7 with 256; of 8192: 6.1 and 8.2; of 16384: 9.1
+// and 13.3), and where the rows are more than are resident at once with 256 threads each
+// (16384 rows of 8192: 184 and 205 us, 5.8 TB/s; of 4096: 95.8 and 101), but not between
+// (2048 rows of 8192: 27.4 and 23.8) nor for rows that start at odd places (16384 of 5003: 218
+// and 165).  Up to 1024 channels a wave each and no barrier (65536 rows of 512: 46.6 us, 85.5
+// with a workgroup; 8192 of 1024: 13.6 and 17.3).
+bool wide(const NormArgs &n) {
+  const replay_residual_norm_args &a = n.a;
+  if (a.tokens <= 2 * kCus) return true;
+  return a.tokens > kResident * kCus && ((a.channels | a.x_stride | a.residual_stride) & 7) == 0;
 }
 
 template <typename TX, typename TR, typename TO>
 int launch(const NormArgs &n, hipStream_t st) {
   const int C = n.a.channels;
+  const bool w = wide(n);
   if (C <= 512) return launch_fast<TX, TR, TO, kWave, 1>(n, st);
+  if (C <= 1024) return launch_fast<TX, TR, TO, kWave, 2>(n, st);
   if (C <= 2048) return launch_fast<TX, TR, TO, kThreads, 1>(n, st);
-  if (C <= 4096) return launch_fast<TX, TR, TO, kThreads, 2>(n, st);
-  if (C <= 8192) return launch_fast<TX, TR, TO, kThreads, 4>(n, st);
+  if (C <= 4096) return w ? launch_fast<TX, TR, TO, 512, 1>(n, st) : launch_fast<TX, TR, TO, kThreads, 2>(n, st);
+  if (C <= 8192) return w ? launch_fast<TX, TR, TO, 1024, 1>(n, st) : launch_fast<TX, TR, TO, kThreads, 4>(n, st);
+  if (C <= 16384) return w ? launch_fast<TX, TR, TO, 1024, 2>(n, st) : launch_fast<TX, TR, TO, kThreads, 8>(n, st);
   if (n.a.tokens > kMostBlocks) return kTooLarge;
   hipLaunchKernelGGL((residual_norm_long_k<TX, TR, TO>), dim3((uint32_t)n.a.tokens), dim3(kThreads), 0, st, n);
   return (int)hipGetLastError();

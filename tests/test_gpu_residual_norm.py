@@ -165,3 +165,30 @@ def test_replayed_from_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(g.view(torch.uint8), e.view(torch.uint8)) for g, e in zip(got, want))
+
+
+@pytest.mark.parametrize("T,C,pad", [(5, 600, 0), (5, 1000, 3), (9, 1024, 0), (600, 600, 0), (600, 2049, 0), (600, 4096, 0), (513, 5003, 0),
+                                     (600, 8192, 8), (520, 10000, 0), (514, 16384, 0), (2049, 4096, 0), (2100, 2056, 8), (2060, 8192, 0),
+                                     (2050, 8200, 0), (2055, 4099, 0), (2055, 4096, 1), (20001, 1016, 0)])
+@pytest.mark.parametrize("out", ["bf16", "e4m3"])
+def test_rows_by_other_numbers_of_threads(T, C, pad, out):
+    """From a wave to 1024 threads a row, which the numbers of rows and channels decide."""
+    import torch
+    from hybrid_model_ssm_replay_amd import ops
+    announce("residual_norm threads", T, C, pad, out)
+    a, res, w = _inputs(T, C, "bf16", "bf16", seed=2, pad=pad)
+    want, h = L.residual_norm(values(a), values(res), values(w), 1e-5)
+    if out == "bf16":
+        got, total = ops.residual_norm(a, res, w)
+        near(values(got), want, (_bar(C) + U + HALF["bf16"]) * np.abs(want) + 1e-37)
+    else:
+        group = 128 if C % 128 == 0 else C
+        got, scales, total = ops.residual_norm(a, res, w, out_dtype=torch.float8_e4m3fn, scale_group=group)
+        want = want.reshape(T, C // group, group)
+        code, scale = _codes(got, scales, group)
+        exact = np.maximum(np.abs(want).max(-1, keepdims=True) / 448.0, 2.0 ** -126)
+        near(scale, exact, (_bar(C) + 2 * U) * exact)
+        off = 2 * _bar(C) + 4 * U
+        low, high = (L.e4m3(np.abs(want) / exact * f) for f in (1 - off, 1 + off))
+        assert ((np.abs(code) >= low) & (np.abs(code) <= high) & ((code == 0) | (np.sign(code) == np.sign(want)))).all()
+    near(values(total), h, (HALF["bf16"] + U) * np.abs(h))
