@@ -19,14 +19,15 @@
 // takes 1.5 us: one sequence of 8192 tokens, 32 heads, 128 x 128 (bf16): 269 us, of which
 // cells_k 68 (it writes 280 MB at 4.1 TB/s) and chain_k 195.
 //
-// walk_k, calls of many: both in one launch, 128 rows to a workgroup, no cell in memory.  A
-// chunk takes 5.5 us, for eight times the rows.  24 sequences of 16384 tokens together, 32
+// walk_k, calls of many (bf16 records): both in one launch, 128 rows to a workgroup, no cell
+// in memory.  A chunk takes 5.5 us, for eight times the rows.  24 sequences of 16384 tokens together, 32
 // heads, 128 x 128, float32 outputs: 305 us, 669 by the other two; eight of 2048 tokens: 236
 // (2.3 TB/s of q, k, v and y), 525; one of 8192 and 64 heads: 529, 511.
 //
 // The inverse is a forward substitution inside the diagonal blocks of 16 tokens, joined
 // block by block below them in float32 matrix products; no power of T is formed, whose
-// entries would grow where keys are alike.  Differences g_t - g_j are taken in float64.
+// entries would grow where keys are alike.  Decays are exponentials of differences of g, taken
+// in float64.
 #include <algorithm>
 
 #include "ops.h"
