@@ -18,7 +18,7 @@
 //
 // Bound by HBM where rows are many and no words are asked for: 4096 rows of 131072 (bf16) 188
 // us, 5.7 TB/s; by the exponentials and the words' comparisons beside it: 1152 rows of 50021,
-// five words, 37 us, 3.1 TB/s; by latency for one row: 131072 of float32, twenty words, 6.2 us
+// five words, 39 us, 2.9 TB/s, none 31; by latency for one row: 131072 of float32, twenty words, 6.2 us
 // and 5.8 us for the join.
 #include "ops.h"
 #include "pieces.h"
@@ -208,7 +208,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
   const int row = fdiv(blockIdx.x, sl.fn), slice = blockIdx.x - row * sl.n;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const T *x = (const T *)a.logits + (int64_t)row * a.stride;
-  const int v0 = slice * sl.size, v1 = min(a.vocab, v0 + sl.size);
+  // A row of bf16 between two words starts with the value before it, which counts for nothing:
+  // loads off a word's bounds are slower (1152 rows of 50021: 36.2 us, 29.6 so, 29.4 of 50016).
+  const int odd = sizeof(T) == 2 && row > 0 && ((uintptr_t)x & 2) ? 1 : 0;
+  x -= odd;
+  const int v0 = slice * sl.size, v1 = slice + 1 == sl.n ? a.vocab + odd : v0 + sl.size;
   Sums z{kLowest, 0.f, 0.f};
   List list;
   list.clear();
@@ -237,7 +241,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
 #pragma unroll
     for (int u = 0; u < kTurn; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xv[u][i] = raw[u].get(i), largest = fmaxf(largest, xv[u][i]);
+      for (int i = 0; i < 8; ++i) {
+        xv[u][i] = raw[u].get(i);
+        if (u == 0 && i == 0) xv[u][i] = at0 < odd ? kNone : xv[u][i];
+        largest = fmaxf(largest, xv[u][i]);
+      }
     if (v + kTurn * kStep < v1) fetch(v + kTurn * kStep);
     if (largest > -kLowest) {  // +infinity
       largest = kNone;
@@ -274,7 +282,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
             const bool is = xv[u][i] >= least && xv[u][i] > kNone;
             const uint64_t mask = __ballot(is);
             if (is) some[wave][n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
-                key_of(xv[u][i], at0 + u * kStep + i);
+                key_of(xv[u][i], at0 + u * kStep + i - odd);
             n += __popcll(mask);
           }
           if (!n) continue;

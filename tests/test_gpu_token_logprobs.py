@@ -120,3 +120,19 @@ def test_replays_and_streams_give_the_same_bits():
         torch.cuda.synchronize()
         for a, b, c in zip(got, want, other):
             assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("V,stride,first", [(1, 3, 1), (2, 3, 1), (8, 9, 0), (7, 15, 2), (2047, 2049, 1), (2048, 2049, 0), (2048, 2051, 1),
+                                            (4096, 4097, 1), (5003, 5003, 0), (50021, 50023, 1), (131072, 131073, 1)])
+@pytest.mark.parametrize("around", [np.nan, INF, 1e30])
+@pytest.mark.parametrize("rows", [3, 9])
+def test_what_is_between_the_rows_counts_for_nothing(V, stride, first, around, rows):
+    """Rows that start between two words, slices and their ends, the values around them large or no numbers."""
+    import torch
+    announce("token_logprobs between", V, stride, first, around, rows)
+    r = np.random.default_rng(V + stride + rows)
+    flat = torch.full((rows * stride + 9,), float(around), device="cuda", dtype=torch.bfloat16)
+    x = torch.as_strided(flat, (rows, V), (stride, 1), first)
+    x.copy_(_dev((3.0 * r.normal(size=(rows, V))).astype(np.float32), "bf16"))
+    for top in (0, 5):
+        _check(x, r.integers(0, V, rows), top)
