@@ -5,8 +5,9 @@ This package only marshals arguments: ``binding`` mirrors the C calls one for on
 (``replay_init``, ``replay_step``, ``replay_flush``, ``replay_verify``,
 ``replay_commit`` and the baselines), and ``layer.ReplayLayer`` allocates the
 device buffers with PyTorch and passes their addresses and the current stream.
-``ops`` has the operators around the recurrence (short convolution, prompt scan,
-gated norm, draft acceptance), and ``generate`` a small model that runs them all.
+``ops`` has the operators around the recurrence (short convolution, prompts of both
+layer kinds, gated and residual norm, log probabilities, draft acceptance), and
+``generate`` small models that run them all.
 
 Importing the package does not load the library; the first call does, and it
 raises if ``libreplayssm.so`` has not been built -- there is no fallback path.

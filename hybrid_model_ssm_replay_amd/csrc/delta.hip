@@ -66,7 +66,8 @@ struct DeltaPlan {
   int lo, hi;      // the chunks of this pass: places start / 64 + sequence + chunk
   int ny;          // slices of a head's rows
   int units;       // sequences x heads of the pass at most
-  int sort, apart; // walk_k: whether sequences go by length; chunks from which a head's rows are split
+  int sort, apart; // walk_k: whether sequences go by length; chunks from which a head's rows are split,
+  int halves;      // of so many sequences at most
   FastDiv fH, fny;
   char *cells;     // [hi - lo][H] of Cell
 };
@@ -832,7 +833,7 @@ void walk_k(DeltaArgs a, DeltaPlan plan) {
       }
     }
   }
-  const int two = P > 64 ? halved * a.H : 0, round = (two + kXcds - 1) / kXcds * kXcds;
+  const int two = min(halved, plan.halves) * a.H, round = (two + kXcds - 1) / kXcds * kXcds;
   if (unit < 2 * round) {
     split = 1 + unit / kXcds % 2;
     unit = unit / (2 * kXcds) * kXcds + unit % kXcds;
@@ -1125,8 +1126,8 @@ int launch_walk(const DeltaArgs &a, hipStream_t st) {
   // By length where it can matter: 24 sequences of 64 tokens take 46 us without it, 62 with it.
   p.sort = units >= kCus && a.p.n > 1 && a.p.n <= kWalkThreads && all >= 4 * (int64_t)a.p.n;
   p.apart = units < kCus ? 0 : p.sort ? (int)std::max<int64_t>(all * a.H / kCus, 1) : 0x1000000;
-  const int64_t two = a.P > 64 ? std::min<int64_t>(a.p.n, p.apart ? all / p.apart : a.p.n) * a.H : 0;
-  const int64_t blocks = units + two + 2 * kXcds;
+  p.halves = a.P <= 64 ? 0 : p.apart ? (int)std::min<int64_t>(a.p.n, all / p.apart) : a.p.n;  // more only with offsets that fall
+  const int64_t blocks = units + (int64_t)p.halves * a.H + 2 * kXcds;
   if (blocks * kWalkThreads >= (int64_t)1 << 32) return kTooLarge;
   p.units = (int)units;
   hipLaunchKernelGGL((walk_k<Y, NK>), dim3((uint32_t)blocks), dim3(kWalkThreads), 0, st, a, p);

@@ -367,3 +367,33 @@ def test_many_heads_on_another_stream_in_place_and_captured(H, lens):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y[inside], want[inside]) and torch.equal(state, want_s)
+
+
+def test_bad_rows_and_offsets_of_many_heads():
+    """Rows outside the batch, offsets past the tokens, falling ones (empty): nothing else is touched."""
+    import torch
+    from hybrid_model_ssm_replay_amd import binding as B
+    from hybrid_model_ssm_replay_amd import ops
+    announce("delta_prompt many, bad rows")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    tokens, H, P, N = 6400, 64, 80, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k = (torch.nn.functional.normalize(torch.randn(tokens, H, N, generator=g, device="cuda"), dim=-1).bfloat16() for _ in range(2))
+    v = torch.randn(tokens, H, P, generator=g, device="cuda").bfloat16()
+    alpha, beta = (torch.rand(tokens, H, generator=g, device="cuda") for _ in range(2))
+    state, status = torch.full((4, H, P, N), 7.0, device="cuda"), i32([0])
+    ops.delta_prompt(q, k, v, alpha, beta, i32([0, 3000, 3001, 6400]), state, rows=i32([-1, 2, 9]), status=status)
+    assert int(status) == B.STATUS_BAD_PROMPT
+    assert bool((state[[0, 1, 3]] == 7).all()) and not bool((state[2] == 7).any())
+    one = torch.empty(1, H, P, N, device="cuda")
+    ops.delta_prompt(q, k, v, alpha, beta, i32([0, tokens]), one)
+    for start in ([0, tokens] * 4 + [0], [-5, tokens + 9, 70], [tokens, 0, tokens], [9, 9, 9, 9]):
+        n = len(start) - 1
+        state = torch.full((n, H, P, N), 7.0, device="cuda")
+        ops.delta_prompt(q, k, v, alpha, beta, i32(start), state)
+        at = np.clip(start, 0, tokens)
+        for i in range(n):
+            if at[i + 1] <= at[i]:
+                assert bool((state[i] == 0).all())
+            elif at[i + 1] - at[i] == tokens:
+                assert bool(((state[i] - one[0]).abs() <= 1e-5 * one[0].abs() + 1e-6).all())
