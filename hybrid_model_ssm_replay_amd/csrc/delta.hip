@@ -1110,12 +1110,15 @@ constexpr size_t kCells = 256u << 20;
 // Whether a call walks: heads of all sequences, and their rows, that give at least half of
 // the CUs something to do.  Sequences of 640 tokens, 32 heads (the other form in brackets):
 // 128 rows, four of them 54 us (77), two 48 (43); 64 rows, four 49 (58); 32 rows, four of 1024
-// tokens 67 (65), 24 of 683 162 (338).
+// tokens 67 (65), 24 of 683 162 (338).  And a chunk or so a sequence, where one launch and no
+// workspace count: 37 tokens 12.5 (16.1), three of 64 13.5 (17.2), but one of 128 16.4 (16.8)
+// and 16.8 (13.7) in a graph.
 constexpr int64_t kWalk = 128, kWalkRows = 64;
 template <typename R>
 bool walks(const DeltaArgs &a) {
   const int64_t units = (int64_t)a.p.n * a.H;
-  return sizeof(R) == 2 && a.N >= 64 && units >= kWalk && units * a.P >= kWalk * kWalkRows;
+  const bool brief = a.p.tokens <= Q * std::min(a.p.n, 3) && a.P >= kWalkRows;
+  return sizeof(R) == 2 && a.N >= 64 && (brief || (units >= kWalk && units * a.P >= kWalk * kWalkRows));
 }
 
 template <typename Y, int NK>
