@@ -138,6 +138,8 @@ struct List {
 };
 constexpr int kFew = 12;  // put in one by one: about as long as sorting them in (one row: 12.7 us, 14.0 with 24, 12.8 with 4)
 
+constexpr int kSpread = kWave / (8 * kTurn);  // lanes whose values of a turn are one for each lane of a wave
+
 // Eight neighbouring values as loaded; places past the n-th: no weight.
 template <typename T>
 struct Eight {
@@ -273,9 +275,42 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
         least = fmaxf(least, __hip_atomic_load(&lasts[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
       const uint64_t beyond = __ballot(largest > list.last && largest >= least);
       if (beyond) {
-        if (__popcll(beyond) > a.top) least = fmaxf(least, nth(largest, a.top, lane));
+        const int lanes = __popcll(beyond);
+        if (lanes > a.top) least = fmaxf(least, nth(largest, a.top, lane));
+        // A few lanes' words: one to a lane, all at once.
+        if (lanes <= kSpread) {
+          float *const values = reinterpret_cast<float *>(some[wave]);
+          int *const first = reinterpret_cast<int *>(values + kWave);
+          if (beyond >> lane & 1) {
+            const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(beyond >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)beyond, 0));
+#pragma unroll
+            for (int i = 0; i < 8 * kTurn; i += 4)
+              st4(values + rank * 8 * kTurn + i, make_float4(xv[i / 8][i % 8], xv[i / 8][i % 8 + 1], xv[i / 8][i % 8 + 2], xv[i / 8][i % 8 + 3]));
+            first[rank] = at0 - odd;
+          }
+          wave_lds_sync();
+          const int from = lane / (8 * kTurn), i = lane % (8 * kTurn);
+          const float value = from < lanes ? values[lane] : kNone;
+          const int word = first[from < lanes ? from : 0] + i / 8 * kStep + i % 8;
+          wave_lds_sync();
+          const bool is = value >= least && value > kNone;
+          const Key key = is ? key_of(value, word) : 0;
+          uint64_t mask = __ballot(is);
+          if (__popcll(mask) <= kFew) {
+            for (; mask; mask &= mask - 1) {
+              const int l = __builtin_ctzll(mask);
+              list.put((Key)__builtin_amdgcn_readlane((uint32_t)(key >> 32), l) << 32 | (uint32_t)__builtin_amdgcn_readlane((uint32_t)key, l), lane);
+            }
+          } else {
+            some[wave][lane] = key;
+            wave_lds_sync();
+            list.sort_in(some[wave], kWave, lane);
+            wave_lds_sync();
+          }
+        }
 #pragma unroll
         for (int u = 0; u < kTurn; ++u) {
+          if (lanes <= kSpread) break;
           int n = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
