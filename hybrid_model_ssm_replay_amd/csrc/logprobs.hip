@@ -18,7 +18,7 @@
 //
 // Bound by HBM where rows are many and no words are asked for: 4096 rows of 131072 (bf16) 188
 // us, 5.7 TB/s; by the exponentials and the words' comparisons beside it: 1152 rows of 50021,
-// five words, 39 us, 2.9 TB/s, none 31; by latency for one row: 131072 of float32, twenty words, 6.2 us
+// five words, 36 us, 3.2 TB/s, none 30; by latency for one row: 131072 of float32, twenty words, 6.2 us
 // and 5.8 us for the join.
 #include "ops.h"
 #include "pieces.h"
@@ -277,7 +277,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
       if (beyond) {
         const int lanes = __popcll(beyond);
         if (lanes > a.top) least = fmaxf(least, nth(largest, a.top, lane));
-        // A few lanes' words: one to a lane, all at once.
+        // A few lanes' words: one to a lane, all at once, and not by the place in the lanes (1152 rows
+        // of 50021, five words: 36 us, 39; 1024 of 131072, twenty: 74, 84).
         if (lanes <= kSpread) {
           float *const values = reinterpret_cast<float *>(some[wave]);
           int *const first = reinterpret_cast<int *>(values + kWave);
@@ -307,26 +308,26 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
             list.sort_in(some[wave], kWave, lane);
             wave_lds_sync();
           }
-        }
+        } else {
 #pragma unroll
-        for (int u = 0; u < kTurn; ++u) {
-          if (lanes <= kSpread) break;
-          int n = 0;
+          for (int u = 0; u < kTurn; ++u) {
+            int n = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bool is = xv[u][i] >= least && xv[u][i] > kNone;
-            const uint64_t mask = __ballot(is);
-            if (is) some[wave][n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
-                key_of(xv[u][i], at0 + u * kStep + i - odd);
-            n += __popcll(mask);
+            for (int i = 0; i < 8; ++i) {
+              const bool is = xv[u][i] >= least && xv[u][i] > kNone;
+              const uint64_t mask = __ballot(is);
+              if (is) some[wave][n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
+                  key_of(xv[u][i], at0 + u * kStep + i - odd);
+              n += __popcll(mask);
+            }
+            if (!n) continue;
+            wave_lds_sync();
+            if (n <= kFew)
+              for (int i = 0; i < n; ++i) list.put(some[wave][i], lane);
+            else
+              list.sort_in(some[wave], n, lane);
+            wave_lds_sync();
           }
-          if (!n) continue;
-          wave_lds_sync();
-          if (n <= kFew)
-            for (int i = 0; i < n; ++i) list.put(some[wave][i], lane);
-          else
-            list.sort_in(some[wave], n, lane);
-          wave_lds_sync();
         }
         list.close(a.top);
         if (lane == 0) __hip_atomic_store(&lasts[wave], list.last, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(kWave) void join_k(replay_token_logprobs_args a, Sl
 
 // Slices of 2048 values, longer where there would be more than 1024 workgroups: each slice
 // starts its words anew (1024 rows of 131072, bf16, twenty alternatives: 83 us, 98 with up to
-// 2048 and 82 with up to 512; 256 rows of 50016 and five: 22.7, 23.0 and 24.9).
+// 2048 and 82 with up to 512, all three 10 less since; 256 rows of 50016 and five: 22.7, 23.0 and 24.9).
 Slices slices_of(int rows, int vocab) {
   Slices s{};
   s.size = kStep;
