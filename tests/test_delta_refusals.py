@@ -63,11 +63,14 @@ def test_calls(B):
 
 
 def test_workspace(B):
-    """None without tokens; bounded however many there are; none for what is refused."""
+    """None without tokens, for a chunk or so a sequence and for many heads; bounded however many
+    tokens there are; none for what is refused."""
     c, low = B.make_config(1, 200, 32, 32, 128, 128, 1, flags=B.FLAG_BF16_RECORDS), B.make_config(1, 2, 32, 32, 128, 128, 1)
     assert B.replay_delta_workspace_bytes(c, 0, 3, B.DT_F32) == 0
     sizes = [B.replay_delta_workspace_bytes(c, n, 3, B.DT_BF16) for n in (1, 1000, 100000, 1 << 30)]
-    assert 0 < sizes[0] < sizes[1] < sizes[2] == sizes[3] <= 256 << 20
+    assert 0 == sizes[0] < sizes[1] < sizes[2] == sizes[3] <= 256 << 20
+    assert B.replay_delta_workspace_bytes(c, 1 << 30, 4, B.DT_BF16) == 0 == B.replay_delta_workspace_bytes(c, 192, 3, B.DT_F32)
+    assert 0 < B.replay_delta_workspace_bytes(c, 193, 3, B.DT_F32) and 0 < B.replay_delta_workspace_bytes(low, 1, 1, B.DT_F32)
     assert B.replay_delta_workspace_bytes(low, 100, 1, B.DT_BF16) == 0 < B.replay_delta_workspace_bytes(low, 100, 1, B.DT_F32)
     assert B.replay_delta_workspace_bytes(c, 100, 201, B.DT_F32) == 0 and B.replay_delta_workspace_bytes(c, -1, 1, B.DT_F32) == 0
 
