@@ -212,7 +212,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_k(replay_token_logprobs_arg
   const T *x = (const T *)a.logits + (int64_t)row * a.stride;
   // A row of bf16 between two words starts with the value before it, which counts for nothing:
   // loads off a word's bounds are slower (1152 rows of 50021: 36.2 us, 29.6 so, 29.4 of 50016).
-  const int odd = sizeof(T) == 2 && row > 0 && ((uintptr_t)x & 2) ? 1 : 0;
+  // The first row, and rows that repeat it (stride 0), have none of the logits before them.
+  const int odd = sizeof(T) == 2 && row > 0 && a.stride > 0 && ((uintptr_t)x & 2) ? 1 : 0;
   x -= odd;
   const int v0 = slice * sl.size, v1 = slice + 1 == sl.n ? a.vocab + odd : v0 + sl.size;
   Sums z{kLowest, 0.f, 0.f};

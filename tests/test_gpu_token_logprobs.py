@@ -136,3 +136,18 @@ def test_what_is_between_the_rows_counts_for_nothing(V, stride, first, around, r
     x.copy_(_dev((3.0 * r.normal(size=(rows, V))).astype(np.float32), "bf16"))
     for top in (0, 5):
         _check(x, r.integers(0, V, rows), top)
+
+
+@pytest.mark.parametrize("V", [7, 1000, 9001])
+@pytest.mark.parametrize("first", [0, 1])
+def test_rows_that_repeat_one_from_between_two_words(V, first):
+    """Stride 0 from an even and an odd element of bf16, alone and as part of every row: nothing before them is theirs."""
+    import torch
+    announce("token_logprobs repeated", V, first)
+    r = np.random.default_rng(V)
+    flat = torch.full((V + 9,), float("nan"), device="cuda", dtype=torch.bfloat16)
+    row = flat[first:first + V]
+    row.copy_(_dev((3.0 * r.normal(size=V)).astype(np.float32), "bf16"))
+    for top in (0, 5):
+        _check(row.expand(4, V), [0, V - 1, V // 2, 3], top)
+        _check(torch.as_strided(flat, (3, V - 2), (1, 1), first), [0, V - 3, 2], top)  # each row a value further on
