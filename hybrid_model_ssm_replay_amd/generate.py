@@ -192,8 +192,11 @@ def _packed(model, prompts):
 def score(model, prompts, top=0):
     """How likely the model finds each prompt's tokens, given those before them (the first is
     given): for each prompt a list of (log probability, entropy, [(word, its log probability),
-    ...] of the top words) for its second token, third token, ...  Prompts as for ``generate``."""
+    ...] of the ``top`` words, 0 to 32) for its second token, third token, ...  Prompts as for
+    ``generate``.  The model's sequences start anew, and are left behind their prompts' last tokens."""
     tokens, start = _packed(model, prompts)
+    if not 0 <= top <= B.MAX_TOP:
+        raise ValueError(f"top is 0 to {B.MAX_TOP}")
     following = torch.cat([tokens[1:], tokens[:1]]).to(torch.int32)
     following[start[1:].long() - 1] = -1  # nothing follows a prompt's last token
     got = ops.token_logprobs(model.logits(tokens, start), following, top=top)

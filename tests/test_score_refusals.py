@@ -25,3 +25,11 @@ def test_commands_and_kinds_refused():
             generate.main(bad)
     with pytest.raises(ValueError, match="kind"):
         generate.Model(kind="rnn")
+
+
+@pytest.mark.parametrize("top", [-1, 33])
+def test_score_refuses_alternatives_before_the_model_runs(top):
+    """A refused call leaves the model's sequences where they were."""
+    from hybrid_model_ssm_replay_amd.generate import score
+    with pytest.raises(ValueError, match="top is 0 to 32"):
+        score(_model(), [[1, 2], [3]], top=top)
