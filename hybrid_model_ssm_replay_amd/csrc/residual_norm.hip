@@ -245,9 +245,11 @@ int launch_fast(const NormArgs &n, hipStream_t st) {
 // (16384 rows of 8192: 184 and 205 us, 5.8 TB/s; of 4096: 95.8 and 101), but not between
 // (2048 rows of 8192: 27.4 and 23.8) nor for rows that start at odd places (16384 of 5003: 218
 // and 165).  Up to 1024 channels a wave each and no barrier (65536 rows of 512: 46.6 us, 85.5
-// with a workgroup; 8192 of 1024: 13.6 and 17.3).
-bool wide(const NormArgs &n) {
+// with a workgroup; 8192 of 1024: 13.6 and 17.3).  Rows too many for a launch of so many
+// threads each (2^23 with 512, 2^22 with 1024) have 256.
+bool wide(const NormArgs &n, int threads) {
   const replay_residual_norm_args &a = n.a;
+  if ((int64_t)a.tokens * threads >= (int64_t)1 << 32) return false;
   if (a.tokens <= 2 * kCus) return true;
   return a.tokens > kResident * kCus && ((a.channels | a.x_stride | a.residual_stride) & 7) == 0;
 }
@@ -255,7 +257,7 @@ bool wide(const NormArgs &n) {
 template <typename TX, typename TR, typename TO>
 int launch(const NormArgs &n, hipStream_t st) {
   const int C = n.a.channels;
-  const bool w = wide(n);
+  const bool w = wide(n, C <= 4096 ? 512 : 1024);
   if (C <= 512) return launch_fast<TX, TR, TO, kWave, 1>(n, st);
   if (C <= 1024) return launch_fast<TX, TR, TO, kWave, 2>(n, st);
   if (C <= 2048) return launch_fast<TX, TR, TO, kThreads, 1>(n, st);

@@ -192,3 +192,24 @@ def test_rows_by_other_numbers_of_threads(T, C, pad, out):
         low, high = (L.e4m3(np.abs(want) / exact * f) for f in (1 - off, 1 + off))
         assert ((np.abs(code) >= low) & (np.abs(code) <= high) & ((code == 0) | (np.sign(code) == np.sign(want)))).all()
     near(values(total), h, (HALF["bf16"] + U) * np.abs(h))
+
+
+@pytest.mark.parametrize("T,C,out", [((1 << 22) + 5, 4104, "e4m3"), ((1 << 23) + 3, 2056, "bf16")])
+def test_as_many_rows_as_a_launch_of_256_threads_each_holds(T, C, out):
+    """More rows than a launch of 512 or 1024 threads each: below 2^32 work-items."""
+    import torch
+    from hybrid_model_ssm_replay_amd import ops
+    announce("residual_norm rows", T, C, out)
+    a, _, w = _inputs(1, C, "bf16", "bf16")
+    x = a.expand(T, C)
+    want, _ = L.residual_norm(values(a), None, values(w), 1e-5)
+    if out == "bf16":
+        got, _ = ops.residual_norm(x, None, w)
+        near(values(got[:1]), want, (_bar(C) + U + HALF["bf16"]) * np.abs(want) + 1e-37)
+    else:
+        got, scales, _ = ops.residual_norm(x, None, w, out_dtype=torch.float8_e4m3fn)
+        assert bool((scales == scales[0]).all())
+        near(values(scales[0]), np.abs(want).max(-1) / 448.0, (_bar(C) + 2 * U) * np.abs(want).max(-1) / 448.0)
+        got = got.view(torch.uint8)
+    for at in range(0, T, 1 << 20):
+        assert bool((got[at:at + (1 << 20)] == got[:1]).all())
