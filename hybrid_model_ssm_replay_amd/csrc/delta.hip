@@ -1113,26 +1113,34 @@ constexpr size_t kCells = 256u << 20;
 // tokens 67 (65), 24 of 683 162 (338).  And a chunk or so a sequence, where one launch and no
 // workspace count: 37 tokens 12.5 (16.1), three of 64 13.5 (17.2), but one of 128 16.4 (16.8)
 // and 16.8 (13.7) in a graph.
+// Heads past what a launch of workgroups so large holds go by the other form, in passes.
 constexpr int64_t kWalk = 128, kWalkRows = 64;
-template <typename R>
-bool walks(const DeltaArgs &a) {
-  const int64_t units = (int64_t)a.p.n * a.H;
-  const bool brief = a.p.tokens <= Q * std::min(a.p.n, 3) && a.P >= kWalkRows;
-  return sizeof(R) == 2 && a.N >= 64 && (brief || (units >= kWalk && units * a.P >= kWalk * kWalkRows));
-}
 
-template <typename Y, int NK>
-int launch_walk(const DeltaArgs &a, hipStream_t st) {
-  DeltaPlan p{};
+// How a call would walk, and its workgroups.
+int64_t walk_plan(const DeltaArgs &a, DeltaPlan &p) {
   p.fH = make_fastdiv((uint32_t)a.H);
   const int64_t units = (int64_t)a.p.n * a.H, all = items_of(a.p.tokens, a.p.n, Q);
   // By length where it can matter: 24 sequences of 64 tokens take 46 us without it, 62 with it.
   p.sort = units >= kCus && a.p.n > 1 && a.p.n <= kWalkThreads && all >= 4 * (int64_t)a.p.n;
   p.apart = units < kCus ? 0 : p.sort ? (int)std::max<int64_t>(all * a.H / kCus, 1) : 0x1000000;
   p.halves = a.P <= 64 ? 0 : p.apart ? (int)std::min<int64_t>(a.p.n, all / p.apart) : a.p.n;  // more only with offsets that fall
-  const int64_t blocks = units + (int64_t)p.halves * a.H + 2 * kXcds;
-  if (blocks * kWalkThreads >= (int64_t)1 << 32) return kTooLarge;
   p.units = (int)units;
+  return units + (int64_t)p.halves * a.H + 2 * kXcds;
+}
+
+template <typename R>
+bool walks(const DeltaArgs &a) {
+  const int64_t units = (int64_t)a.p.n * a.H;
+  const bool brief = a.p.tokens <= Q * std::min(a.p.n, 3) && a.P >= kWalkRows;
+  if (!(sizeof(R) == 2 && a.N >= 64 && (brief || (units >= kWalk && units * a.P >= kWalk * kWalkRows)))) return false;
+  DeltaPlan p{};
+  return walk_plan(a, p) * kWalkThreads < (int64_t)1 << 32;
+}
+
+template <typename Y, int NK>
+int launch_walk(const DeltaArgs &a, hipStream_t st) {
+  DeltaPlan p{};
+  const int64_t blocks = walk_plan(a, p);
   hipLaunchKernelGGL((walk_k<Y, NK>), dim3((uint32_t)blocks), dim3(kWalkThreads), 0, st, a, p);
   return (int)hipGetLastError();
 }

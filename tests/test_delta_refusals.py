@@ -75,6 +75,16 @@ def test_workspace(B):
     assert B.replay_delta_workspace_bytes(c, 100, 201, B.DT_F32) == 0 and B.replay_delta_workspace_bytes(c, -1, 1, B.DT_F32) == 0
 
 
+def test_workspace_of_more_heads_than_one_launch_walks(B):
+    """Workgroups of 768 threads, one for a head and 16 more: below 2^32 work-items.  Others go in passes, with a workspace."""
+    most = ((1 << 32) - 1) // 768 - 16
+    for sequences, some in (((1 << 22) // 32, 0), (most // 32, 0), (most // 32 + 1, 1), (1 << 18, 1)):
+        for P, N in ((32, 64), (128, 128)):
+            c = B.make_config(1, 1 << 18, 32, 32, P, N, 1, flags=B.FLAG_BF16_RECORDS)
+            size = B.replay_delta_workspace_bytes(c, sequences, sequences, B.DT_F32)
+            assert (0 < size <= 256 << 20) if some else size == 0, (sequences, P)
+
+
 def _on(*shape, dtype=torch.float32):
     return Placed.of(torch.zeros(shape, dtype=dtype))
 

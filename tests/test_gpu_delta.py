@@ -397,3 +397,25 @@ def test_bad_rows_and_offsets_of_many_heads():
                 assert bool((state[i] == 0).all())
             elif at[i + 1] - at[i] == tokens:
                 assert bool(((state[i] - one[0]).abs() <= 1e-5 * one[0].abs() + 1e-6).all())
+
+
+def test_more_heads_than_one_launch_walks():
+    """A token a sequence from a state of zeros: o = beta v (k . q), S = beta v k^T.  In passes, by the form with a workspace."""
+    import torch
+    from hybrid_model_ssm_replay_amd import ops
+    announce("delta_prompt most heads")
+    H, P, N, n = 32, 32, 64, ((1 << 32) - 1) // 768 // 32 + 1
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k = (torch.nn.functional.normalize(torch.randn(n, H, N, generator=g, device="cuda"), dim=-1).bfloat16() for _ in range(2))
+    v = torch.randn(n, H, P, generator=g, device="cuda").bfloat16()
+    alpha, beta = (torch.rand(n, H, generator=g, device="cuda") for _ in range(2))
+    state = torch.full((n, H, P, N), float("nan"), device="cuda")
+    y = ops.delta_prompt(q, k, v, alpha, beta, torch.arange(n + 1, dtype=torch.int32, device="cuda"), state)
+    # Products of three factors and pieces that hold 24 bits: the state within 4 U, o within its sum's N more of |k| . |q|.
+    for at in range(0, n, 8192):
+        kd, qd, vd = (t[at:at + 8192].double() for t in (k, q, v))
+        u = beta[at:at + 8192].double()[..., None] * vd
+        want = u[..., :, None] * kd[..., None, :]
+        assert bool(((state[at:at + 8192] - want).abs() <= 4 * 2.0 ** -24 * want.abs() + 1e-37).all())
+        dot, size = (kd * qd).sum(-1, keepdim=True), (kd * qd).abs().sum(-1, keepdim=True)
+        assert bool(((y[at:at + 8192] - u * dot).abs() <= (N + 8) * 2.0 ** -24 * u.abs() * size + 1e-37).all())
