@@ -1103,8 +1103,10 @@ void walk_k(DeltaArgs a, DeltaPlan plan) {
     st4(a.state + tile0 + 32 * (m / 2) + 4 * (m % 2), make_float4(S[m][0], S[m][1], S[m][2], S[m][3]));
 }
 
-// Cells of one pass: at most 256 MB of them, so that long prompts need no more than that
-// (24 prompts of 16384 tokens by cells_k and chain_k: 128 MB 683 us, 256 MB 660, 768 MB 616).
+// Cells of one pass: 256 MB of them at most, so that long prompts need no more than that (24
+// prompts of 16384 tokens by cells_k and chain_k: 128 MB 683 us, 256 MB 660, 768 MB 616), but eight
+// chunks of all heads at least, whose states each pass reads and writes (float32 records, 128 x 128:
+// 2048 tokens of 400 heads 1399 us, 1469 in 256 MB; 1024 of 1000 heads 1667, 2038).
 constexpr size_t kCells = 256u << 20;
 
 // Whether a call walks: heads of all sequences, and their rows, that give at least half of

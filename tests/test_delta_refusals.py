@@ -75,6 +75,23 @@ def test_workspace(B):
     assert B.replay_delta_workspace_bytes(c, 100, 201, B.DT_F32) == 0 and B.replay_delta_workspace_bytes(c, -1, 1, B.DT_F32) == 0
 
 
+def test_workspace_of_wide_layers(B):
+    """Eight chunks of all heads at least, and otherwise 256 MB at most, however many tokens there are."""
+    seen = set()
+    for heads in (32, 300, 326, 327, 400, 4000):
+        for flags, P, N in ((0, 128, 128), (0, 64, 64), (0, 16, 16), (B.FLAG_BF16_RECORDS, 128, 128)):
+            c = B.make_config(1, 1, heads, heads, P, N, 1, flags=flags)
+            if flags and heads > 100:
+                continue  # these walk
+            size = [B.replay_delta_workspace_bytes(c, n, 1, B.DT_F32) for n in (7 * 64, 1 << 20, 1 << 30)]
+            assert 0 < size[0] <= size[1] == size[2] and size[0] % (8 * heads) == 0
+            assert size[2] == size[0] if size[0] > 256 << 20 else size[2] <= 256 << 20
+            if (flags, N) == (0, 128):
+                seen.add(size[0] > 256 << 20)
+                assert (size[0] > 256 << 20) == (heads > 326)
+    assert seen == {False, True}
+
+
 def test_workspace_of_more_heads_than_one_launch_walks(B):
     """Workgroups of 768 threads, one for a head and 16 more: below 2^32 work-items.  Others go in passes, with a workspace."""
     most = ((1 << 32) - 1) // 768 - 16
