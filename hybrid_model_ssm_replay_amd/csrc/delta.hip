@@ -17,7 +17,7 @@
 // of the others, so that even one sequence's 32 heads are a workgroup for every CU; its
 // waves share the products and hand each other S, V - K S0^T and U through LDS.  A chunk
 // takes 1.5 us: one sequence of 8192 tokens, 32 heads, 128 x 128 (bf16): 269 us, of which
-// cells_k 68 (it writes 280 MB at 4.1 TB/s) and chain_k 195.
+// cells_k 68 (it writes 270 MB at 3.9 TB/s) and chain_k 200.
 //
 // walk_k, calls of many (bf16 records): both in one launch, 128 rows to a workgroup, no cell
 // in memory.  A chunk takes 5.5 us, for eight times the rows.  24 sequences of 16384 tokens together, 32
@@ -52,7 +52,9 @@ __device__ __forceinline__ int step_of(int w, int s) { return w < 2 ? w : 2 * w 
 template <typename R, typename Y, int NK>
 struct Cell {
   static constexpr int IP = sizeof(R) == 4 ? 3 : 1;  // pieces of an input
-  static constexpr int MP = sizeof(Y) == 4 ? 3 : 2;  // pieces of P, U and S in the output products
+  // Pieces of P, U and S in the output products: two are within 2^-16 of a term, where a bf16
+  // output is then rounded by up to 2^-8 (8192 tokens 268 us, 299 with three; eight of 2048 229, 247).
+  static constexpr int MP = sizeof(Y) == 4 ? 3 : 2;
   static constexpr int A0 = 0;                       // [3][kSteps]
   static constexpr int P0 = A0 + 3 * kSteps * kFrag;     // [MP][kSteps]
   static constexpr int ROW = sizeof(R) / 2 * kFrag;      // a record's rows, as loaded
@@ -1114,7 +1116,9 @@ constexpr size_t kCells = 256u << 20;
 // 128 rows, four of them 54 us (77), two 48 (43); 64 rows, four 49 (58); 32 rows, four of 1024
 // tokens 67 (65), 24 of 683 162 (338).  And a chunk or so a sequence, where one launch and no
 // workspace count: 37 tokens 12.5 (16.1), three of 64 13.5 (17.2), but one of 128 16.4 (16.8)
-// and 16.8 (13.7) in a graph.
+// and 16.8 (13.7) in a graph.  The lengths are on the device, so a prompt that outlasts the others walks
+// with them: one of 8192 with three of ten tokens 527 (287), with 15 528 (312), alone 270; four
+// of 4000 288 (503).
 // Heads past what a launch of workgroups so large holds go by the other form, in passes.
 constexpr int64_t kWalk = 128, kWalkRows = 64;
 

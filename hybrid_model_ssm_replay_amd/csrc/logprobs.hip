@@ -16,10 +16,10 @@
 //
 // -infinity and NaN have no weight; +infinity counts as the largest float32.
 //
-// Bound by HBM where rows are many and no words are asked for: 4096 rows of 131072 (bf16) 188
-// us, 5.7 TB/s; by the exponentials and the words' comparisons beside it: 1152 rows of 50021,
-// five words, 36 us, 3.2 TB/s, none 30; by latency for one row: 131072 of float32, twenty words, 6.2 us
-// and 5.8 us for the join.
+// Bound by HBM where rows are many and no words are asked for: 4096 rows of 131072 (bf16) 190
+// us, 5.6 TB/s; by the exponentials and the words' comparisons beside it: 1152 rows of 50021 (bf16),
+// five words, 35 us, 3.3 TB/s (32 where a third of the words is masked), none 29; of float32 50 and 47,
+// 4.6 and 4.9 TB/s; by latency for one row: 131072 of float32, twenty words, 6.3 us and 5.0 for the join.
 #include "ops.h"
 #include "pieces.h"
 
@@ -405,8 +405,9 @@ __global__ __launch_bounds__(kWave) void join_k(replay_token_logprobs_args a, Sl
 }
 
 // Slices of 2048 values, longer where there would be more than 1024 workgroups: each slice
-// starts its words anew (1024 rows of 131072, bf16, twenty alternatives: 83 us, 98 with up to
-// 2048 and 82 with up to 512, all three 10 less since; 256 rows of 50016 and five: 22.7, 23.0 and 24.9).
+// starts its words anew (1024 rows of 131072, bf16, twenty alternatives: 77 us, 91 with up to
+// 2048 and 76 with up to 512; 600 rows of 32000, float32, five: 21.4, 28.7 and 21.4; 256 rows of 50016,
+// bf16, five: 21.1, 23.3 and 21.3).
 Slices slices_of(int rows, int vocab) {
   Slices s{};
   s.size = kStep;

@@ -298,8 +298,8 @@ def residual_norm(x, residual, weight, *, eps=1e-5, out_dtype=None, scale_group=
 
     x, residual [tokens, channels] float32 or bfloat16, rows may be strided; residual
     None: nothing is added; weight float32 [channels], or None: 1.  The norm is that of
-    x + residual in float32.  Returns (out, total): total is x + residual in residual's
-    type, or x itself without one; out has out_dtype (x's type if None).  With out_dtype
+    x + residual in float32.  Returns (out, total): total is x + residual in a new tensor of
+    residual's type, or x itself without one; out has out_dtype (x's type if None).  With out_dtype
     torch.float8_e4m3fn it returns (codes, scales, total): scale_group channels (a power
     of two from 16 to 512, or all of them: None) share a scale, float32 [tokens,
     channels / scale_group], and code times scale is the value."""

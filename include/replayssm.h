@@ -349,6 +349,7 @@ int replay_record_slots(const replay_ctx *ctx, int32_t *slots, void *stream);
  * how many drafts to commit, and the log probabilities of tokens.
  * They share the conventions at the top of this file.  Vector arrays have an
  * element type (REPLAY_DT_*); sums, statistics and states are float32 or wider.
+ * A call whose launch would hold 2^32 work-items or more is refused.
  */
 
 /* Element types. */
@@ -522,7 +523,8 @@ int replay_gated_norm(const replay_gated_norm_args *args, void *stream);
  *   out_dtype  REPLAY_DT_F32, _BF16, or REPLAY_DT_E4M3: codes, one byte each, that
  *              stand for code x scale; scales float32 [tokens][channels / group],
  *              max(largest |out| of the group / 448, 2^-126).  A code is out / scale
- *              (by the scale's float32 reciprocal), rounded to nearest even; NaN stays NaN.
+ *              (by the scale's float32 reciprocal), rounded to nearest even; NaN stays NaN,
+ *              and a code of zero has no sign.
  *   group      channels that share a scale: channels, or 16, 32, 64, 128, 256 or 512
  *              that divide them; 0 for other outputs. */
 typedef struct replay_residual_norm_args {
