@@ -53,7 +53,7 @@ def test_delta_prompt_of_32_rows_extremes(what):
 
 @pytest.mark.parametrize("H,P,lens", [(64, 128, (6016,)), (64, 128, (64, 2560, 320, 3100)), (32, 48, (11008, 70)), (32, 32, (64, 5500, 30, 6016))])
 def test_several_passes_are_bit_equal_to_calls_of_whole_chunks(H, P, lens):
-    """More chunks than one pass holds (39 of 64 heads, 79 of 32); calls of 1024 tokens are one pass each, of as many
+    """More chunks than one pass holds (40 of 64 heads, 81 of 32); calls of 1024 tokens are one pass each, of as many
     rows to a workgroup (32 with 64 heads of 128; 16 with the others, also for all their sequences)."""
     import torch
     from hybrid_model_ssm_replay_amd import binding as B
